@@ -16,7 +16,9 @@
  * pkv_paged_attention_decode_planned (the decode work split made once per
  * step for every layer), pkv_copy_blocks (copy-on-write),
  * pkv_paged_attention_decode_noalloc (decode without a caller workspace),
- * the workspace size queries, pkv_status_string, pkv_abi_version and
+ * the 8-bit cache (pkv_kv_write_fp8, pkv_kv_gather_fp8,
+ * pkv_paged_attention_decode_fp8, pkv_paged_attention_prefill_fp8: e4m3 pools
+ * with a scale per block and KV head), the workspace size queries, pkv_status_string, pkv_abi_version and
  * pkv_selftest_bounded_wait (the kernels' bounded-wait failure path).
  *
  * Sources of the operations (page title, section):
@@ -98,7 +100,9 @@ typedef enum pkv_status {
 
 typedef enum pkv_dtype {
   PKV_F32 = 0,   /* IEEE binary32 */
-  PKV_BF16 = 1   /* bfloat16; attention accumulates in fp32, rounds RNE   */
+  PKV_BF16 = 1,  /* bfloat16; attention accumulates in fp32, rounds RNE   */
+  PKV_FP8_E4M3 = 2  /* pools of the pkv_*_fp8 entries alone: e4m3 with a
+                       scale per block and KV head (see pkv_kv_write_fp8) */
 } pkv_dtype;
 
 /* Bits OR-ed into *err_word by kernels that meet bad device-resident data. */
@@ -484,6 +488,128 @@ pkv_status pkv_paged_attention_decode_noalloc(const void* q, int32_t num_seqs, i
                                               const int32_t* seq_lens, int32_t max_seq_len,
                                               float scale, int32_t max_ctas, void* out,
                                               int32_t* err_word, void* stream);
+
+/*
+ * The 8-bit cache.
+ *
+ * The pages have no counterpart of these entries.  Decode time is the time
+ * to read the cache ("nano-vLLM", Where the time went), so a cache held in
+ * 8 bits halves it and holds twice the tokens in the same memory ("Day 38",
+ * how many blocks fit).
+ *
+ * Pools are [num_blocks, block_size, n_kv, head_dim] of e4m3 bytes
+ * (pool->dtype = PKV_FP8_E4M3) with one fp32 scale per block and KV head,
+ * k_scales and v_scales [num_blocks, n_kv]: an element stands for its e4m3
+ * value times its block's and head's scale.  The write leaves scales that are
+ * powers of two, 2^-60 .. 2^60.  With them quantising rounds once (to e4m3),
+ * reading back rounds nothing (every value is a bf16 number) and attention
+ * applies them exactly.  The reading entries take any positive finite scale
+ * within those bounds; with one that is no power of two, value x scale is
+ * rounded to the type that the entry computes in (bf16 for read-back and
+ * prefill to bf16).
+ *
+ * head_dim must be a multiple of 16 (attention: 16, 32, 64 or 128, with
+ * block_size 16).  `dtype` is the type of k, v, q and the outputs (PKV_F32
+ * or PKV_BF16).  A block is copied on write with two pkv_copy_blocks calls:
+ * one on the pools described as bf16 with head_dim / 2 (the bytes are copied
+ * as they are), one on the scales described as fp32 blocks of one token,
+ * one head and head_dim n_kv (n_kv a multiple of 4).
+ */
+
+/*
+ * pkv_kv_write_fp8 - quantise this step's new K and V into an 8-bit cache.
+ *
+ * The 8-bit pkv_kv_write.  It takes the block tables in place of a slot
+ * mapping, because a block's scale depends on which of its rows are tokens.
+ * Sequence b's last n_b = cu_new_lens[b+1] - cu_new_lens[b] tokens are k / v
+ * rows cu_new_lens[b] ..., and go to positions seq_lens[b] - n_b ..
+ * seq_lens[b] - 1 (as in pkv_slot_mapping).  For each block that they touch,
+ * each KV head, and K and V each for itself, with a the largest magnitude
+ * of the new elements there (NaN passed over) and f the smallest power of
+ * two in 2^-60 .. 2^60 with a <= 448 f:
+ *     s = f               if the block's first token is among the new ones
+ *     s = max(s_old, f)   if the block holds earlier tokens of the sequence
+ *     new elements   x -> e4m3(x / s)  (nearest even; past 448: +-448; NaN: NaN)
+ *     earlier rows   if s > s_old, their values move to the new scale:
+ *                    e4m3(value * s_old / s)
+ * Rows past the sequence's end are left as they were.  Results do not
+ * depend on any order of execution.
+ *
+ *   k, v          [num_tokens, n_kv, head_dim] of `dtype`, 16-byte aligned
+ *   block_tables  int32 [num_seqs, max_blocks_per_seq]; a block written to
+ *                 must belong to one sequence only (copy a shared one first)
+ *   cu_new_lens   int32 [num_seqs + 1], cu_new_lens[0] = 0, nondecreasing,
+ *                 cu_new_lens[num_seqs] = num_tokens (n_b = 0: writes nothing)
+ *   k_pool, v_pool  16-byte aligned; k_scales, v_scales fp32 [num_blocks, n_kv]
+ *   A token whose length, offset or block id is bad is skipped and reported.
+ */
+pkv_status pkv_kv_write_fp8(const void* k, const void* v, int32_t dtype,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            const int32_t* seq_lens, const int32_t* cu_new_lens,
+                            int32_t num_seqs, int32_t num_tokens, void* k_pool, void* v_pool,
+                            float* k_scales, float* v_scales, const pkv_pool_desc* pool,
+                            int32_t* err_word, void* stream);
+
+/*
+ * pkv_kv_gather_fp8 - read an 8-bit cache back: pkv_kv_gather with every
+ * value times its scale, in `dtype`.
+ */
+pkv_status pkv_kv_gather_fp8(const void* k_pool, const void* v_pool, const float* k_scales,
+                             const float* v_scales, const pkv_pool_desc* pool,
+                             const int32_t* block_tables, int32_t max_blocks_per_seq,
+                             const int32_t* seq_lens, const int32_t* cu_seq_lens,
+                             int32_t num_seqs, int32_t total_tokens, int32_t dtype, void* k_out,
+                             void* v_out, int32_t* err_word, void* stream);
+
+/*
+ * pkv_paged_attention_decode_fp8 - pkv_paged_attention_decode over an 8-bit
+ * cache: one query token per sequence attends to its whole history, read in
+ * place.  seq_lens[b] counts this step's token (write it with
+ * pkv_kv_write_fp8 first).  A sequence of length 0 gets zeros; slots past the
+ * length are never used, whatever bytes they hold.
+ *
+ * The work split, and with it what results depend on, is that of
+ * pkv_paged_attention_decode: logical positions, lengths and max_ctas, never
+ * physical block ids; identical calls give identical bits.  Scores, softmax
+ * sums and outputs are held in fp32.  For bf16, weights are rounded to 11
+ * significand bits before they multiply V; for fp32 queries and weights keep
+ * 22.  A query element more than 2^28 below its row's largest loses bits.
+ *
+ *   q, out      [num_seqs, n_heads, head_dim] of `dtype`, 16-byte aligned
+ *   workspace   at least pkv_decode_fp8_workspace_bytes(...) bytes, 16-byte
+ *               aligned; calls that may run at the same time need one each
+ *   Supported: head_dim 16, 32, 64, 128; block_size 16; n_heads % n_kv == 0,
+ *              n_heads / n_kv <= 16.
+ */
+size_t pkv_decode_fp8_workspace_bytes(int32_t num_seqs, int32_t n_heads, int32_t head_dim,
+                                      int32_t max_seq_len, int32_t max_ctas, int32_t block_size);
+
+pkv_status pkv_paged_attention_decode_fp8(const void* q, int32_t dtype, int32_t num_seqs,
+                                          int32_t n_heads, const void* k_pool, const void* v_pool,
+                                          const float* k_scales, const float* v_scales,
+                                          const pkv_pool_desc* pool, const int32_t* block_tables,
+                                          int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                          int32_t max_seq_len, float scale, int32_t max_ctas,
+                                          void* out, void* workspace, size_t workspace_bytes,
+                                          int32_t* err_word, void* stream);
+
+/*
+ * pkv_paged_attention_prefill_fp8 - pkv_paged_attention_prefill over an
+ * 8-bit cache: causal attention of each sequence's query chunk over its
+ * paged history (the chunk's own K/V written with pkv_kv_write_fp8 first).
+ * A key or value that a query may not see does not reach its output, NaN
+ * included.  It needs no workspace.
+ *
+ *   q, out      [total_q, n_heads, head_dim] of `dtype`, 16-byte aligned
+ *   everything else as for pkv_paged_attention_prefill; supported shapes as
+ *   for pkv_paged_attention_decode_fp8
+ */
+pkv_status pkv_paged_attention_prefill_fp8(
+    const void* q, int32_t dtype, const int32_t* cu_q_lens, int32_t num_seqs, int32_t total_q,
+    int32_t max_q_len, int32_t n_heads, const void* k_pool, const void* v_pool,
+    const float* k_scales, const float* v_scales, const pkv_pool_desc* pool,
+    const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+    int32_t max_seq_len, float scale, void* out, int32_t* err_word, void* stream);
 
 /*
  * pkv_selftest_bounded_wait - check the kernels' failure path on this GPU.

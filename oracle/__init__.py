@@ -26,6 +26,7 @@ values and properties the pages and mathematics fix (worked examples under
 ``tests/golden/``, closed forms, a library attention routine, invariants).
 No function is "parity unpinned".
 """
+from . import paged_fp8  # noqa: F401
 from .paged import (  # noqa: F401
     to_float64,
     slot_of,

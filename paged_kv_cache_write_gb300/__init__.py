@@ -25,7 +25,8 @@ __all__ = [
     "decode_shared_prefix_workspace_bytes", "paged_attention_decode_shared_prefix",
     "decode_plan", "paged_attention_decode_planned", "prefill_workspace_bytes",
     "paged_attention_prefill", "status_string", "abi_version", "paged_attention_decode_noalloc",
-    "selftest_bounded_wait",
+    "selftest_bounded_wait", "PKV_FP8_E4M3", "kv_write_fp8", "kv_gather_fp8",
+    "decode_fp8_workspace_bytes", "paged_attention_decode_fp8", "paged_attention_prefill_fp8",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -33,6 +34,7 @@ library_path = os.path.join(HERE, "libpkv.so")
 
 PKV_F32 = 0
 PKV_BF16 = 1
+PKV_FP8_E4M3 = 2
 DEVERR = {"block_id": 1, "slot": 2, "table_width": 4, "length": 8, "timeout": 16, "prefix": 32,
           "plan": 64}
 
@@ -100,6 +102,20 @@ def _load():
     L.pkv_paged_attention_prefill.restype = _i32
     L.pkv_paged_attention_prefill.argtypes = [_p, _p, _i32, _i32, _i32, _i32, _p, _p, _desc, _p,
                                               _i32, _p, _i32, _f, _p, _p, _sz, _p, _p]
+    L.pkv_kv_write_fp8.restype = _i32
+    L.pkv_kv_write_fp8.argtypes = [_p, _p, _i32, _p, _i32, _p, _p, _i32, _i32, _p, _p, _p, _p, _desc,
+                                   _p, _p]
+    L.pkv_kv_gather_fp8.restype = _i32
+    L.pkv_kv_gather_fp8.argtypes = [_p, _p, _p, _p, _desc, _p, _i32, _p, _p, _i32, _i32, _i32, _p,
+                                    _p, _p, _p]
+    L.pkv_decode_fp8_workspace_bytes.restype = _sz
+    L.pkv_decode_fp8_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32, _i32, _i32]
+    L.pkv_paged_attention_decode_fp8.restype = _i32
+    L.pkv_paged_attention_decode_fp8.argtypes = [_p, _i32, _i32, _i32, _p, _p, _p, _p, _desc, _p,
+                                                 _i32, _p, _i32, _f, _i32, _p, _p, _sz, _p, _p]
+    L.pkv_paged_attention_prefill_fp8.restype = _i32
+    L.pkv_paged_attention_prefill_fp8.argtypes = [_p, _i32, _p, _i32, _i32, _i32, _i32, _p, _p, _p,
+                                                  _p, _desc, _p, _i32, _p, _i32, _f, _p, _p, _p]
     _lib = L
     return L
 
@@ -442,4 +458,174 @@ def paged_attention_decode_noalloc(q, k_pool, v_pool, block_tables, seq_lens, sc
         block_tables.shape[1], _dev(seq_lens, "seq_lens", torch.int32), int(max_seq_len),
         float(scale), int(max_ctas), _dev(out, "out", k_pool.dtype),
         _opt(err, "err", torch.int32), _stream(stream)))
+    return out
+
+
+# ------------------------------------------------------------ 8-bit cache
+
+
+def _call_on(device, name, stream, *args):
+    """Call entry point ``name`` with ``device`` current; its stream comes last."""
+    fn = getattr(_lib or _load(), name)
+    if device.index == torch.cuda.current_device():
+        _check(name, fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(name, fn(*args, _stream(stream)))
+
+
+def _fp8_pool(k_pool, v_pool, k_scales, v_scales):
+    """Descriptor and pointers of an 8-bit cache, its four tensors checked."""
+    if k_pool.dim() != 4:
+        raise ValueError("pool must be [num_blocks, block_size, n_kv, head_dim]")
+    if v_pool.shape != k_pool.shape:
+        raise ValueError("k_pool and v_pool must have the same shape")
+    nb, bs, nkv, hd = k_pool.shape
+    if tuple(k_scales.shape) != (nb, nkv) or tuple(v_scales.shape) != (nb, nkv):
+        raise ValueError(f"k_scales and v_scales must be {(nb, nkv)}: one per block and KV head")
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    desc = PoolDesc(nb, bs, nkv, hd, PKV_FP8_E4M3)
+    return desc, (_dev(k_pool, "k_pool", f8), _dev(v_pool, "v_pool", f8),
+                  _dev(k_scales, "k_scales", f32), _dev(v_scales, "v_scales", f32))
+
+
+def _batch(block_tables, seq_lens, cu=None, cu_name=""):
+    """(num_seqs, table width) of a batch's tables, lengths and offsets."""
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    B, W = block_tables.shape
+    if tuple(seq_lens.shape) != (B,):
+        raise ValueError(f"seq_lens must be {(B,)}: one per row of block_tables")
+    if cu is not None and tuple(cu.shape) != (B + 1,):
+        raise ValueError(f"{cu_name} must be {(B + 1,)}")
+    return B, W
+
+
+def _one_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+
+
+def kv_write_fp8(k, v, block_tables, seq_lens, cu_new_lens, k_pool, v_pool, k_scales, v_scales, *,
+                 err=None, stream=None):
+    """Quantise k/v [T, n_kv, head_dim] (float32 or bfloat16) into an 8-bit
+    cache: pools of ``torch.float8_e4m3fn`` [num_blocks, block_size, n_kv,
+    head_dim] and float32 scales [num_blocks, n_kv], powers of two.
+
+    Sequence b's rows ``cu_new_lens[b] : cu_new_lens[b+1]`` go to its last
+    positions, up to ``seq_lens[b] - 1``.  A block that holds earlier tokens
+    keeps at least its scale; where a new token needs a larger one the earlier
+    rows are moved to it.
+    """
+    desc, pools = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
+    B, W = _batch(block_tables, seq_lens, cu_new_lens, "cu_new_lens")
+    if k.dim() != 3 or k.shape[1:] != k_pool.shape[2:] or v.shape != k.shape:
+        raise ValueError("k, v must be [T, n_kv, head_dim] matching the pool")
+    _one_device(k_pool.device, v_pool=v_pool, k_scales=k_scales, v_scales=v_scales, k=k, v=v,
+                block_tables=block_tables, seq_lens=seq_lens, cu_new_lens=cu_new_lens, err=err)
+    i32 = torch.int32
+    _call_on(k_pool.device, "pkv_kv_write_fp8", stream, _dev(k, "k"), _dev(v, "v", k.dtype),
+             _dtype_code(k.dtype), _dev(block_tables, "block_tables", i32), W,
+             _dev(seq_lens, "seq_lens", i32), _dev(cu_new_lens, "cu_new_lens", i32), B, k.shape[0],
+             *pools, ctypes.byref(desc), _opt(err, "err", i32))
+
+
+def kv_gather_fp8(k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, cu_seq_lens,
+                  total_tokens: int, *, dtype=torch.bfloat16, k_out=None, v_out=None, err=None,
+                  stream=None):
+    """Contiguous [total_tokens, n_kv, head_dim] K and V of an 8-bit cache in
+    logical order, each value times its scale, in ``dtype`` (float32 or
+    bfloat16; that of ``k_out`` / ``v_out`` where given)."""
+    desc, pools = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
+    B, W = _batch(block_tables, seq_lens, cu_seq_lens, "cu_seq_lens")
+    dtype = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else dtype
+    code = _dtype_code(dtype)
+    shape = (int(total_tokens), desc.n_kv, desc.head_dim)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=k_pool.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=k_pool.device)
+    if tuple(k_out.shape) != shape or tuple(v_out.shape) != shape:
+        raise ValueError(f"k_out, v_out must be {shape}")
+    _one_device(k_pool.device, v_pool=v_pool, k_scales=k_scales, v_scales=v_scales, k_out=k_out,
+                v_out=v_out, block_tables=block_tables, seq_lens=seq_lens,
+                cu_seq_lens=cu_seq_lens, err=err)
+    i32 = torch.int32
+    _call_on(k_pool.device, "pkv_kv_gather_fp8", stream, *pools, ctypes.byref(desc),
+             _dev(block_tables, "block_tables", i32), W, _dev(seq_lens, "seq_lens", i32),
+             _dev(cu_seq_lens, "cu_seq_lens", i32), B, int(total_tokens), code,
+             _dev(k_out, "k_out", dtype), _dev(v_out, "v_out", dtype), _opt(err, "err", i32))
+    return k_out, v_out
+
+
+def decode_fp8_workspace_bytes(num_seqs, n_heads, head_dim, max_seq_len, max_ctas=0, block_size=16):
+    return int(_load().pkv_decode_fp8_workspace_bytes(num_seqs, n_heads, head_dim, max_seq_len,
+                                                      max_ctas, block_size))
+
+
+def _fp8_query(q, k_pool, out):
+    if q.dim() != 3 or q.shape[2] != k_pool.shape[3]:
+        raise ValueError("q must be [rows, n_heads, head_dim] with the pool's head_dim")
+    if out is None:
+        return torch.empty_like(q)
+    if out.shape != q.shape:
+        raise ValueError(f"out must be {tuple(q.shape)}")
+    return out
+
+
+def paged_attention_decode_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
+                               scale: float, max_seq_len: int | None = None, *, out=None,
+                               workspace=None, max_ctas: int = 0, err=None, stream=None):
+    """Decode attention [B, n_heads, head_dim] (float32 or bfloat16) over the
+    paged history of an 8-bit cache (see :func:`kv_write_fp8`).
+
+    ``max_seq_len`` and ``workspace`` are as for
+    :func:`paged_attention_decode`, with ``decode_fp8_workspace_bytes(...)``
+    bytes; calls that may run at the same time need a workspace each.
+    """
+    desc, pools = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
+    B, W = _batch(block_tables, seq_lens)
+    out = _fp8_query(q, k_pool, out)
+    if q.shape[0] != B:
+        raise ValueError("q must have one row per sequence")
+    H, hd = q.shape[1:]
+    if max_seq_len is None:
+        max_seq_len = int(seq_lens.max().item()) if B else 0
+    if workspace is None:
+        need = decode_fp8_workspace_bytes(B, H, hd, max_seq_len, max_ctas, desc.block_size)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _one_device(k_pool.device, v_pool=v_pool, k_scales=k_scales, v_scales=v_scales, q=q, out=out,
+                workspace=workspace, block_tables=block_tables, seq_lens=seq_lens, err=err)
+    i32 = torch.int32
+    _call_on(k_pool.device, "pkv_paged_attention_decode_fp8", stream, _dev(q, "q"),
+             _dtype_code(q.dtype), B, H, *pools, ctypes.byref(desc),
+             _dev(block_tables, "block_tables", i32), W, _dev(seq_lens, "seq_lens", i32),
+             int(max_seq_len), float(scale), int(max_ctas), _dev(out, "out", q.dtype),
+             _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+             _opt(err, "err", i32))
+    return out
+
+
+def paged_attention_prefill_fp8(q, cu_q_lens, k_pool, v_pool, k_scales, v_scales, block_tables,
+                                seq_lens, scale: float, max_q_len: int | None = None,
+                                max_seq_len: int | None = None, *, out=None, err=None,
+                                stream=None):
+    """Causal chunked-prefill attention [total_q, n_heads, head_dim] (float32
+    or bfloat16) over the paged history of an 8-bit cache."""
+    desc, pools = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
+    B, W = _batch(block_tables, seq_lens, cu_q_lens, "cu_q_lens")
+    out = _fp8_query(q, k_pool, out)
+    if max_q_len is None:
+        max_q_len = int((cu_q_lens[1:] - cu_q_lens[:-1]).max().item()) if B else 0
+    if max_seq_len is None:
+        max_seq_len = int(seq_lens.max().item()) if B else 0
+    _one_device(k_pool.device, v_pool=v_pool, k_scales=k_scales, v_scales=v_scales, q=q, out=out,
+                cu_q_lens=cu_q_lens, block_tables=block_tables, seq_lens=seq_lens, err=err)
+    i32 = torch.int32
+    _call_on(k_pool.device, "pkv_paged_attention_prefill_fp8", stream, _dev(q, "q"),
+             _dtype_code(q.dtype), _dev(cu_q_lens, "cu_q_lens", i32), B, q.shape[0],
+             int(max_q_len), q.shape[1], *pools, ctypes.byref(desc),
+             _dev(block_tables, "block_tables", i32), W, _dev(seq_lens, "seq_lens", i32),
+             int(max_seq_len), float(scale), _dev(out, "out", q.dtype), _opt(err, "err", i32))
     return out

@@ -1,0 +1,544 @@
+// Decode over the 8-bit cache: one query per sequence attends to the
+// sequence's pages (attention.cuh's decode over e4m3 pools with a scale per
+// block and KV head; mathematics and layouts of the tiles in fp8_rows.cuh).
+//
+// Bound by reading the cache: 2 x n_kv x head_dim bytes a token, 8 bytes of
+// scales per block and head.  The work split is that of the bf16 decode, since
+// what it is for is the same: a persistent grid over equal contiguous ranges
+// of (sequence, head group, block) units, a merge kernel for the groups that
+// several CTAs share, and one thread-block cluster per (sequence, head group)
+// for batches too small to stream.  A producer lane fetches whole blocks of the
+// group's heads with TMA (16 tokens x hg heads x head_dim bytes, K and V: 32 KB
+// a stage at 8 heads of 128); one consumer warp per KV head.  Block ids and
+// scales are gathered by the consumer warps, 32 blocks at a time and a batch
+// ahead of use, so their latency is off the path.
+#pragma once
+
+#include "attention.cuh"
+#include "fp8_rows.cuh"
+
+namespace pkv {
+namespace fp8 {
+
+using attn::Cursor;
+using attn::DecodeParams;
+using attn::DecodeWs;
+using attn::Ring;
+using attn::kBarrierBytes;
+using attn::kKernelPlanSeqs;
+using attn::kMaxCluster;
+using attn::kMaxRep;
+using attn::kMaxStages;
+
+struct Scales {
+  const float* k;
+  const float* v;
+};
+
+// Largest decode CTA: one producer warp and a warp per KV head of the group.
+constexpr int kMaxThreads = 9 * 32;
+
+// Heads per CTA: the largest divisor of n_kv that is at most 8 (a row of 8
+// heads is at most 1 KB).
+inline int head_group(int n_kv) {
+  int best = 1;
+  for (int h = 1; h <= 8 && h <= n_kv; ++h)
+    if (n_kv % h == 0) best = h;
+  return best;
+}
+
+// tc::tma_load_3d with an L2 cache policy for the copied lines.
+__device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* map, int x, int y,
+                                                 int z, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)),
+      "l"(policy)
+      : "memory");
+}
+
+// One lane: wait for stage `it` to be free, then fetch a block's K and V for
+// heads head0 .. (a slot past the pool's end reads zeros).  `policy`
+// (nonzero): an L2 cache policy for the copied lines.
+__device__ __forceinline__ bool fetch(const Ring& r, uint32_t it, const CUtensorMap* tm_k,
+                                      const CUtensorMap* tm_v, int slot, int head0, int32_t* err,
+                                      uint64_t policy) {
+  const int st = static_cast<int>(it % r.nstages);
+  const uint32_t use = it / r.nstages;
+  if (use > 0 && !mbar_wait(r.empty + st, (use - 1) & 1)) {
+    report(err, PKV_DEVERR_TIMEOUT);
+    return false;
+  }
+  mbar_arrive_expect_tx(r.full + st, static_cast<uint32_t>(r.stage_bytes));
+  if (policy != 0) {
+    tma_load_3d_hint(r.k_tile(st), tm_k, 0, slot, head0, r.full + st, policy);
+    tma_load_3d_hint(r.v_tile(st), tm_v, 0, slot, head0, r.full + st, policy);
+  } else {
+    tc::tma_load_3d(r.k_tile(st), tm_k, 0, slot, head0, r.full + st);
+    tc::tma_load_3d(r.v_tile(st), tm_v, 0, slot, head0, r.full + st);
+  }
+  return true;
+}
+
+// A consumer warp's block scales, one block per lane.
+struct ScaleBatch {
+  float ks, vs, lv;
+  // `id`: this lane's block (any value if it has none)
+  __device__ __forceinline__ void load(const Scales& sc, const DecodeParams& p, int id, int head) {
+    const bool ok = id >= 0 && id < p.num_blocks;  // others are read as zeros
+    const int64_t at = int64_t(ok ? id : 0) * p.n_kv + head;
+    ks = ok ? __ldg(sc.k + at) : 1.f;
+    vs = ok ? __ldg(sc.v + at) : 1.f;
+  }
+  __device__ __forceinline__ void settle() { lv = __log2f(vs); }
+};
+
+template <typename T, int HD, int NT>
+__global__ void __launch_bounds__(kMaxThreads, 1)
+    decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const DecodeParams p, const Scales sc) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int consumers = p.hg_size;
+  Ring ring = attn::make_tile_ring(smem, p.nstages, kBS * p.hg_size * HD);
+  attn::ring_init(ring, consumers);
+  attn::pdl_wait();               // inputs and workspace belong to the preceding kernel
+  attn::pdl_launch_dependents();  // the merge kernel may be scheduled (it waits for this grid)
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = gridDim.x;
+  int U;
+  int4 st = make_int4(0, 0, 0, 0);
+  if (p.plan_in_kernel) {
+    // scan the units per sequence in the (still unused) ring stages
+    int* cu_s = reinterpret_cast<int*>(ring.stages);  // [B + 1]
+    int* warp_tot = cu_s + p.B + 1;                   // [32]
+    const int nt = blockDim.x;
+    for (int b = threadIdx.x; b < p.B; b += nt) {
+      if (blockIdx.x == 0) attn::check_length(p, b);
+      cu_s[b] = attn::units_of(p, b);
+    }
+    __syncthreads();
+    const int chunk = (p.B + nt - 1) / nt;
+    const int b0 = min(p.B, int(threadIdx.x) * chunk);
+    const int b1 = min(p.B, b0 + chunk);
+    int local = 0;
+    for (int b = b0; b < b1; ++b) local += cu_s[b];
+    int run = attn::cta_exclusive_scan(local, warp_tot);
+    for (int b = b0; b < b1; ++b) {
+      const int n = cu_s[b];
+      cu_s[b] = run;
+      run += n;
+    }
+    if (threadIdx.x == nt - 1) cu_s[p.B] = run;
+    __syncthreads();
+    U = cu_s[p.B];
+    const int r0 = attn::range_begin(blockIdx.x, U, G);
+    if (r0 < attn::range_begin(blockIdx.x + 1, U, G)) {
+      const int b = attn::seq_of_unit(cu_s, p.B, r0);
+      const int nblk = attn::walked_blocks(p, attn::used_len(p, b));
+      const int grp = (r0 - cu_s[b]) / nblk;
+      st = make_int4(b, grp, (r0 - cu_s[b]) - grp * nblk, 0);
+    }
+    attn::zero_empty<T, HD>(p, blockIdx.x, G, [&](int b) { return cu_s[b + 1] == cu_s[b]; });
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      p.total_units[0] = U;
+      p.total_units[1] = -1;  // a call planning for itself replaces any kept plan
+    }
+    fence_proxy_async_smem();  // the scan's stores come before the ring's copies
+    __syncthreads();
+  } else {
+    U = __ldcg(p.total_units);
+    st = __ldcg(p.starts + blockIdx.x);
+  }
+  const int r0 = attn::range_begin(blockIdx.x, U, G);
+  const int r1 = attn::range_begin(blockIdx.x + 1, U, G);
+  const int rows_per_group = p.hg_size * p.rep;
+  Cursor cur;
+  if (r0 < r1) cur.load(p, st);
+
+  if (warp == consumers) {
+    // -------------------------------------------------------- producer
+    const uint64_t pol = tc::l2_evict_first_policy();  // each block is read once
+    uint32_t it = 0;
+    bool ok = true;
+    for (int u = r0; u < r1 && ok;) {
+      const int n = min(r1 - u, cur.nblk - cur.j);
+      const int32_t* row = p.bt + int64_t(cur.b) * p.W + cur.j;
+      for (int jj = 0; jj < n && ok; jj += 32) {
+        const int id = jj + lane < n ? __ldg(row + jj + lane) : 0;
+        const int n_here = min(32, n - jj);
+        for (int k = 0; k < n_here; ++k) {
+          if (*ring.abort_flag) { ok = false; break; }
+          const int blk = __shfl_sync(0xffffffffu, id, k);
+          const bool good = blk >= 0 && blk < p.num_blocks;
+          if (!good && lane == 0) report(p.err, PKV_DEVERR_BLOCK_ID);
+          bool filled = true;
+          if (lane == 0)
+            filled = fetch(ring, it, &tm_k, &tm_v, (good ? blk : p.num_blocks) * kBS,
+                           cur.grp * p.hg_size, p.err, pol);
+          if (!__shfl_sync(0xffffffffu, filled, 0)) {
+            *ring.abort_flag = 1;
+            ok = false;
+            break;
+          }
+          ++it;
+        }
+      }
+      u += n;
+      cur.advance(p, n);
+    }
+    if (!ok) attn::ring_drain(ring, it);
+    // the split group this CTA merges (read by the merge kernel)
+    if (lane == 0)
+      p.splits[blockIdx.x] =
+          r0 < r1 ? attn::split_entry(blockIdx.x, G, U, st.x, st.y, st.z,
+                                      attn::walked_blocks(p, attn::used_len(p, st.x)))
+                  : make_int4(-1, 0, 0, 0);
+  } else if (warp < consumers) {
+    // ------------------------------------------------------- consumers
+    Rows<T, HD, NT, false> rows;
+    uint32_t it = 0;
+    bool ok = true;
+    const T* q = static_cast<const T*>(p.q);
+    T* out = static_cast<T*>(p.out);
+    for (int u = r0; u < r1 && ok;) {
+      const int n = min(r1 - u, cur.nblk - cur.j);
+      const int b = cur.b;
+      const int kv_head = cur.grp * p.hg_size + warp;
+      const int head0 = kv_head * p.rep;
+      const int last = cur.L - 1;
+      // block ids a batch of 32 ahead of the scales, scales a batch ahead of use
+      const int32_t* row = p.bt + int64_t(b) * p.W + cur.j;
+      auto id_at = [&](int i) { return i < n ? __ldg(row + i) : -1; };
+      ScaleBatch now, next;
+      next.load(sc, p, id_at(lane), kv_head);
+      int ids = id_at(32 + lane);
+      rows.begin(
+          [&](int r) -> const T* {
+            return r < p.rep ? q + (int64_t(b) * p.n_heads + head0 + r) * HD : nullptr;
+          },
+          [&](int) { return last; }, p.scale_log2);
+      for (int k = 0; k < n; ++k) {
+        if ((k & 31) == 0) {
+          now = next;
+          now.settle();
+          next.load(sc, p, ids, kv_head);
+          ids = id_at(k + 64 + lane);
+        }
+        const float ks = __shfl_sync(0xffffffffu, now.ks, k & 31);
+        const float vs = __shfl_sync(0xffffffffu, now.vs, k & 31);
+        const float lv = __shfl_sync(0xffffffffu, now.lv, k & 31);
+        if (!attn::ring_wait_full(ring, it, p.err)) {
+          *ring.abort_flag = 1;
+          ok = false;
+          break;
+        }
+        const int stg = static_cast<int>(it % ring.nstages);
+        const int j0 = (cur.j + k) * kBS;
+        rows.block(ring.k_tile(stg) + warp * kBS * HD, ring.v_tile(stg) + warp * kBS * HD, j0,
+                   cur.L - j0, ks, vs, lv);
+        attn::ring_release(ring, it);
+        ++it;
+      }
+      if (!ok) break;
+      if (cur.j == 0 && n == cur.nblk) {
+        rows.store([&](int r) -> T* {
+          return r < p.rep ? out + (int64_t(b) * p.n_heads + head0 + r) * HD : nullptr;
+        });
+      } else {  // a group split over several CTAs
+        const int slot = 2 * blockIdx.x + (u == r0 ? 0 : 1);
+        const int64_t base = int64_t(slot) * rows_per_group + warp * p.rep;
+        rows.store_partial(
+            [&](int r) -> float* { return r < p.rep ? p.ws_o + (base + r) * HD : nullptr; },
+            [&](int r) -> float* { return p.ws_ml + (base + r) * 2; });
+      }
+      u += n;
+      cur.advance(p, n);
+    }
+  }
+}
+
+// Batches too small to stream: one cluster of C CTAs per (sequence, head
+// group), each a contiguous part of the sequence's at most 8 * C blocks, the
+// parts combined through distributed shared memory (as the bf16 decode's
+// cluster path; no workspace, no merge launch).
+template <typename T, int HD, int NT>
+__global__ void __launch_bounds__(kMaxThreads, 1)
+    decode_cluster_kernel(const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, const DecodeParams p,
+                          const Scales sc) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int consumers = p.hg_size;
+  Ring ring = attn::make_tile_ring(smem, p.nstages, kBS * p.hg_size * HD);
+  attn::ring_init(ring, consumers);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int C = p.cluster;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int seg = static_cast<int>(blockIdx.x) / C;  // (sequence, head group)
+  const int b = seg / p.n_groups;
+  const int grp = seg - b * p.n_groups;
+  const int rows_per_group = p.hg_size * p.rep;
+  float* part_o = reinterpret_cast<float*>(smem + p.part_off);  // [rows_per_group][HD]
+  float* part_ml = part_o + rows_per_group * HD;                // [rows_per_group][2]
+
+  attn::pdl_wait();
+  attn::pdl_launch_dependents();
+  // this path's sequences have at most 64 blocks: entries lane and 32 + lane
+  // of the table row are read along with the length
+  const int32_t* trow = p.bt + int64_t(b) * p.W;
+  int ids[2] = {-1, -1};
+  if (lane < p.W) ids[0] = __ldg(trow + lane);
+  if (lane + 32 < p.W) ids[1] = __ldg(trow + lane + 32);
+  const int L = attn::used_len(p, b);
+  const int nblk = (L + kBS - 1) / kBS;
+  const int j0 = rank * nblk / C, j1 = (rank + 1) * nblk / C;
+  if (blockIdx.x == 0 && threadIdx.x == 0)
+    p.total_units[1] = -1;  // a call planning for itself replaces any kept plan
+  if (rank == 0 && grp == 0 && threadIdx.x == 0) attn::check_length(p, b);
+
+  if (warp == consumers) {
+    const uint64_t pol = tc::l2_evict_first_policy();
+    uint32_t it = 0;
+    bool ok = true;
+    for (int j = j0; j < j1 && ok; ++j) {
+      if (*ring.abort_flag) { ok = false; break; }
+      const int blk = __shfl_sync(0xffffffffu, j < 32 ? ids[0] : ids[1], j & 31);
+      const bool good = blk >= 0 && blk < p.num_blocks;
+      if (!good && lane == 0) report(p.err, PKV_DEVERR_BLOCK_ID);
+      bool filled = true;
+      if (lane == 0)
+        filled = fetch(ring, it, &tm_k, &tm_v, (good ? blk : p.num_blocks) * kBS,
+                       grp * p.hg_size, p.err, pol);
+      if (!__shfl_sync(0xffffffffu, filled, 0)) {
+        *ring.abort_flag = 1;
+        ok = false;
+        break;
+      }
+      ++it;
+    }
+    if (!ok) attn::ring_drain(ring, it);
+  } else if (warp < consumers) {
+    const T* q = static_cast<const T*>(p.q);
+    const int kv_head = grp * p.hg_size + warp;
+    const int head0 = kv_head * p.rep;
+    // scales of blocks j0 + lane (j1 - j0 <= 8)
+    const int lo = __shfl_sync(0xffffffffu, ids[0], (j0 + lane) & 31);
+    const int hi = __shfl_sync(0xffffffffu, ids[1], (j0 + lane) & 31);
+    ScaleBatch now;
+    now.load(sc, p, j0 + lane < j1 ? (j0 + lane < 32 ? lo : hi) : -1, kv_head);
+    Rows<T, HD, NT, false> rows;
+    rows.begin(
+        [&](int r) -> const T* {
+          return r < p.rep ? q + (int64_t(b) * p.n_heads + head0 + r) * HD : nullptr;
+        },
+        [&](int) { return L - 1; }, p.scale_log2);
+    now.settle();
+    for (int j = j0; j < j1; ++j) {
+      const uint32_t it = j - j0;
+      const float ks = __shfl_sync(0xffffffffu, now.ks, it);
+      const float vs = __shfl_sync(0xffffffffu, now.vs, it);
+      const float lv = __shfl_sync(0xffffffffu, now.lv, it);
+      if (!attn::ring_wait_full(ring, it, p.err)) {
+        *ring.abort_flag = 1;
+        break;
+      }
+      const int stg = static_cast<int>(it % ring.nstages);
+      rows.block(ring.k_tile(stg) + warp * kBS * HD, ring.v_tile(stg) + warp * kBS * HD, j * kBS,
+                 L - j * kBS, ks, vs, lv);
+      attn::ring_release(ring, it);
+    }
+    // this CTA's part (also after an abort, so the barrier below is reached)
+    rows.store_partial(
+        [&](int r) -> float* { return r < p.rep ? part_o + (warp * p.rep + r) * HD : nullptr; },
+        [&](int r) -> float* { return part_ml + (warp * p.rep + r) * 2; });
+  }
+
+  cluster_sync();  // every CTA's partial is in its shared memory
+  // CTA `rank` combines elements [rank E / C, (rank + 1) E / C) of the group
+  const int E = rows_per_group * HD;
+  const int e0 = rank * E / C, e1 = (rank + 1) * E / C;
+  T* out = static_cast<T*>(p.out) + (int64_t(b) * p.n_heads + int64_t(grp) * rows_per_group) * HD;
+  for (int e = e0 + static_cast<int>(threadIdx.x); e < e1; e += static_cast<int>(blockDim.x)) {
+    const int r = e / HD;
+    float2 ml[kMaxCluster];
+    float oc[kMaxCluster];
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) {  // every peer's values in one round trip
+      ml[c] = make_float2(-INFINITY, 0.f);
+      oc[c] = 0.f;
+      if (c < C) {
+        ml[c] = ld_cluster_f32x2(cluster_map(part_ml + r * 2, c));
+        oc[c] = ld_cluster_f32(cluster_map(part_o + e, c));
+      }
+    }
+    float M = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c)
+      if (ml[c].y > 0.f) M = fmaxf(M, ml[c].x);  // a part that saw no key has no weight
+    float acc = 0.f, den = 0.f;
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) {
+      if (ml[c].y > 0.f) {
+        const float w = fast_exp2(ml[c].x - M) * ml[c].y;
+        den += w;
+        acc = fmaf(w, oc[c], acc);
+      }
+    }
+    out[e] = Elem<T>::from_f(den > 0.f ? acc * (1.f / den) : 0.f);
+  }
+  cluster_sync();  // the peers have read this CTA's partials
+}
+
+// --------------------------------------------------------------- host side
+
+template <typename T, int HD, int NT>
+struct DecodeFp8 {
+  static int stage_bytes(int hg) { return 2 * kBS * hg * HD; }
+  static size_t smem_for(int hg, int nstages) {
+    return kBarrierBytes + 1024 + size_t(nstages) * stage_bytes(hg);
+  }
+  // Ring depth: about 176 KB of stages per SM, shared by the CTAs of 8
+  // consumer warps in all (narrow groups: several CTAs per SM).
+  static int ring_stages(int hg) {
+    const int ctas = std::max(1, 8 / hg);
+    const int ns = 176 * 1024 / ctas / stage_bytes(hg);
+    return std::max(2, std::min(kMaxStages, ns));
+  }
+  static cudaError_t grid(const AttnArgs& a, int hg, int* G, size_t* smem, int* nstages, int* wave) {
+    *nstages = ring_stages(hg);
+    *smem = smem_for(hg, *nstages);
+    static KernelSetup setup;
+    int per_sm = 0;
+    const cudaError_t e = kernel_setup(setup, decode_kernel<T, HD, NT>, static_cast<int>(*smem),
+                                       (hg + 1) * 32, &per_sm);
+    if (e != cudaSuccess) return e;
+    per_sm = std::max(1, std::min(per_sm, 16));  // 16: what the workspace is sized for
+    *wave = *G = sm_count() * per_sm;
+    if (a.max_ctas > 0 && a.max_ctas < *G) *G = a.max_ctas;
+    const int64_t max_units = int64_t(a.num_seqs) * (a.pool.n_kv / hg) *
+                              ((std::min(a.max_seq_len, a.max_blocks_per_seq * kBS) + kBS - 1) / kBS);
+    if (max_units < *G) *G = static_cast<int>(std::max<int64_t>(1, max_units));
+    return cudaSuccess;
+  }
+  static constexpr int kClusterSmemMax = 226 * 1024;
+
+  static cudaError_t run(const AttnArgs& a, const Scales& sc, cudaStream_t stream) {
+    const PoolShape& pool = a.pool;
+    const int hg = head_group(pool.n_kv);
+    DecodeParams p{};
+    p.q = a.q;
+    p.out = a.out;
+    p.k_pool = static_cast<const uint8_t*>(a.k_pool);
+    p.v_pool = static_cast<const uint8_t*>(a.v_pool);
+    p.bt = a.block_tables;
+    p.seq_lens = a.seq_lens;
+    p.err = a.err;
+    p.B = a.num_seqs;
+    p.n_heads = a.n_heads;
+    p.n_kv = pool.n_kv;
+    p.rep = a.n_heads / pool.n_kv;
+    p.hg_size = hg;
+    p.n_groups = pool.n_kv / hg;
+    p.W = a.max_blocks_per_seq;
+    p.num_blocks = pool.num_blocks;
+    p.max_len = std::min(a.max_seq_len, a.max_blocks_per_seq * kBS);
+    p.max_seq_len = a.max_seq_len;
+    p.head_dim = HD;
+    p.elem_bytes = 1;
+    p.scale_log2 = a.scale * attn::kLog2e;
+    int G = 0, wave = 0;
+    size_t smem = 0;
+    cudaError_t e = grid(a, hg, &G, &smem, &p.nstages, &wave);
+    if (e != cudaSuccess) return e;
+    if (G > 65535) return cudaErrorInvalidValue;  // split entries pack CTA indices in 16 bits
+    p.grid = G;
+    const DecodeWs L(a.num_seqs, G, size_t(hg) * p.rep, HD);
+    if (L.total > a.workspace_bytes) return cudaErrorInvalidValue;
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    p.cu_units = reinterpret_cast<int32_t*>(ws + L.cu);
+    p.starts = reinterpret_cast<int4*>(ws + L.starts);
+    p.splits = reinterpret_cast<int4*>(ws + L.splits);
+    p.total_units = reinterpret_cast<int32_t*>(ws + L.total_units);
+    p.ws_ml = reinterpret_cast<float*>(ws + L.ml);
+    p.ws_o = reinterpret_cast<float*>(ws + L.o);
+    // the pools as (head_dim bytes, slot, KV head), read in boxes of one
+    // block's 16 slots x the group's heads
+    CUtensorMap tm_k{}, tm_v{};
+    const uint64_t slots = uint64_t(pool.num_blocks) * kBS;
+    const uint64_t dims[3] = {HD, slots, uint64_t(pool.n_kv)};
+    const uint64_t strides[2] = {uint64_t(pool.n_kv) * HD, HD};
+    const uint32_t box[3] = {HD, kBS, static_cast<uint32_t>(hg)};
+    if (!encode_u8(&tm_k, a.k_pool, dims, strides, box, Tile<HD>::kSwizzle) ||
+        !encode_u8(&tm_v, a.v_pool, dims, strides, box, Tile<HD>::kSwizzle))
+      return cudaErrorInvalidValue;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3((hg + 1) * 32);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+
+    // Latency-bound batches, by the rule of the bf16 decode: the longest
+    // sequence at most 64 blocks and the clusters within two waves.
+    const int nmax = (p.max_len + kBS - 1) / kBS;
+    const int C = std::max(1, std::min(kMaxCluster, (nmax + 3) / 4));
+    const int64_t ctas = int64_t(p.B) * p.n_groups * C;
+    if (a.max_ctas == 0 && nmax <= 8 * kMaxCluster && ctas <= 2 * int64_t(wave)) {
+      p.cluster = C;
+      p.nstages = std::max(2, std::min(p.nstages, (nmax + C - 1) / C));
+      const size_t rows = size_t(hg) * p.rep;
+      const size_t extra = rows * HD * 4 + (rows * 2 * 4 + 15) / 16 * 16;
+      while (p.nstages > 2 && smem_for(hg, p.nstages) + extra > size_t(kClusterSmemMax)) --p.nstages;
+      p.part_off = static_cast<int>(smem_for(hg, p.nstages));
+      static KernelSetup setup;
+      e = kernel_setup(setup, decode_cluster_kernel<T, HD, NT>, kClusterSmemMax, (hg + 1) * 32,
+                       nullptr);
+      if (e != cudaSuccess) return e;
+      attr[1].id = cudaLaunchAttributeClusterDimension;
+      attr[1].val.clusterDim.x = static_cast<unsigned>(C);
+      attr[1].val.clusterDim.y = 1;
+      attr[1].val.clusterDim.z = 1;
+      cfg.numAttrs = 2;
+      cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+      cfg.dynamicSmemBytes = p.part_off + extra;
+      e = cudaLaunchKernelEx(&cfg, decode_cluster_kernel<T, HD, NT>, tm_k, tm_v, p, sc);
+      return e != cudaSuccess ? e : cudaGetLastError();
+    }
+    // every CTA scans the lengths in its ring stages; larger batches have a
+    // plan kernel
+    p.plan_in_kernel = a.num_seqs <= kKernelPlanSeqs &&
+                       size_t(a.num_seqs + 1 + 32) * 4 <= size_t(p.nstages) * stage_bytes(hg);
+    if (!p.plan_in_kernel) {
+      attn::decode_plan_kernel<T, HD><<<1, 1024, 0, stream>>>(p);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    cfg.gridDim = dim3(G);
+    cfg.dynamicSmemBytes = smem;
+    e = cudaLaunchKernelEx(&cfg, decode_kernel<T, HD, NT>, tm_k, tm_v, p, sc);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(G);
+    e = attn::launch_merge<T, HD>(cfg, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+  }
+};
+
+template <typename T>
+cudaError_t decode_as(const AttnArgs& a, const Scales& sc, cudaStream_t s) {
+  const bool one = a.n_heads / a.pool.n_kv <= 8;
+  switch (a.pool.head_dim) {
+    case 16: return one ? DecodeFp8<T, 16, 1>::run(a, sc, s) : DecodeFp8<T, 16, 2>::run(a, sc, s);
+    case 32: return one ? DecodeFp8<T, 32, 1>::run(a, sc, s) : DecodeFp8<T, 32, 2>::run(a, sc, s);
+    case 64: return one ? DecodeFp8<T, 64, 1>::run(a, sc, s) : DecodeFp8<T, 64, 2>::run(a, sc, s);
+    default: return one ? DecodeFp8<T, 128, 1>::run(a, sc, s) : DecodeFp8<T, 128, 2>::run(a, sc, s);
+  }
+}
+
+// The two output types are compiled in their own translation units.
+cudaError_t decode_fp8_bf16(const AttnArgs& a, const Scales& sc, cudaStream_t s);
+cudaError_t decode_fp8_f32(const AttnArgs& a, const Scales& sc, cudaStream_t s);
+
+}  // namespace fp8
+}  // namespace pkv

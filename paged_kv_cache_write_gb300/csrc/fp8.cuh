@@ -1,0 +1,63 @@
+// Device helpers of the 8-bit cache: e4m3 values, their conversions and the
+// power-of-two scale of a (block, KV head).
+//
+// An element of an 8-bit pool stands for (e4m3 value) * (scale of its block
+// and KV head).  Scales are powers of two 2^e, kFp8MinExp <= e <= kFp8MaxExp:
+// e4m3 is a floating format, so a finer scale would not make its relative
+// error smaller, and with a power of two
+//   - x * 2^-e is exact, so e4m3's rounding is the only one of a write,
+//   - moving a block to a larger scale is exact but for values that become
+//     subnormal (below 2^-6 of the scale),
+//   - every value of the cache has 4 significand bits and an exponent far
+//     inside bf16's range: it is a bf16 number.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "device.cuh"
+
+namespace pkv {
+
+constexpr float kE4m3Max = 448.f;  // 1.75 * 2^8
+constexpr int kFp8MinExp = -60;
+constexpr int kFp8MaxExp = 60;
+
+// 2^e for an exponent of the normal range.
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
+
+// Scale for values of magnitude at most a (a >= 0, not NaN): 2^e with the
+// smallest e in range such that a <= 448 * 2^e.  a = m * 2^E with 1 <= m < 2
+// needs e = E - 8 if m <= 1.75, else E - 7; zero, subnormals and infinity
+// are settled by the clamp.
+__device__ __forceinline__ float fp8_scale_for(float a) {
+  const uint32_t bits = __float_as_uint(a);
+  const int E = static_cast<int>(bits >> 23) - 127;
+  int e = E - ((bits & 0x7fffffu) <= 0x600000u ? 8 : 7);
+  e = max(kFp8MinExp, min(kFp8MaxExp, e));
+  return pow2f(e);
+}
+
+// Two e4m3 bytes (lo in the low byte), round to nearest even; magnitudes
+// past 448 become 448, NaN stays NaN.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The two e4m3 bytes of `b` as f16 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(b));
+  return r;
+}
+
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t b) {
+  const uint32_t h = e4m3x2_to_f16x2(b);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+}  // namespace pkv

@@ -10,7 +10,7 @@ namespace pkv {
 
 struct PoolShape {
   int32_t num_blocks, block_size, n_kv, head_dim, dtype;
-  int32_t elem_bytes() const { return dtype == 0 ? 4 : 2; }
+  int32_t elem_bytes() const { return dtype == 0 ? 4 : dtype == 1 ? 2 : 1; }
   int64_t row_bytes() const { return int64_t(n_kv) * head_dim * elem_bytes(); }
 };
 
@@ -35,6 +35,21 @@ cudaError_t launch_kv_gather(const void* k_pool, const void* v_pool, const PoolS
                              const int32_t* seq_lens, const int32_t* cu_seq_lens, int32_t num_seqs,
                              int32_t total_tokens, void* k_out, void* v_out, int32_t* err,
                              cudaStream_t stream);
+
+// 8-bit cache: write (quantising) and read back.  dtype: of k, v and of the
+// read-back outputs.
+cudaError_t launch_kv_write_fp8(const void* k, const void* v, int32_t dtype,
+                                const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                const int32_t* seq_lens, const int32_t* cu_new_lens,
+                                int32_t num_seqs, int32_t num_tokens, void* k_pool, void* v_pool,
+                                float* k_scales, float* v_scales, const PoolShape& pool,
+                                int32_t* err, cudaStream_t stream);
+cudaError_t launch_kv_gather_fp8(const void* k_pool, const void* v_pool, const float* k_scales,
+                                 const float* v_scales, const PoolShape& pool,
+                                 const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                 const int32_t* seq_lens, const int32_t* cu_seq_lens,
+                                 int32_t num_seqs, int32_t total_tokens, int32_t dtype,
+                                 void* k_out, void* v_out, int32_t* err, cudaStream_t stream);
 
 // Attention problem shared by decode and prefill.
 struct AttnArgs {
@@ -82,5 +97,14 @@ cudaError_t launch_prefill(const AttnArgs& a, cudaStream_t stream);
 // tcgen05 prefill (bf16, head_dim 64/128, 1/2/4/8/16 query heads per KV head).
 bool prefill_tc_supported(const PoolShape& pool, int32_t n_heads);
 cudaError_t launch_prefill_tc(const AttnArgs& a, cudaStream_t stream);
+
+// Attention over the 8-bit cache; dtype: of q and out (a.pool describes the
+// 8-bit pool).
+bool fp8_attention_supported(const PoolShape& pool, int32_t n_heads);
+size_t decode_fp8_workspace_bytes(int32_t num_seqs, int32_t n_heads, int32_t head_dim);
+cudaError_t launch_decode_fp8(const AttnArgs& a, int32_t dtype, const float* k_scales,
+                              const float* v_scales, cudaStream_t stream);
+cudaError_t launch_prefill_fp8(const AttnArgs& a, int32_t dtype, const float* k_scales,
+                               const float* v_scales, cudaStream_t stream);
 
 }  // namespace pkv

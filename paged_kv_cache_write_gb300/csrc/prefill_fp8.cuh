@@ -1,0 +1,182 @@
+// Chunked prefill over the 8-bit cache on warp-level tensor cores: fp32
+// queries, and bf16 queries of narrow heads (mathematics and tile layouts in
+// fp8_rows.cuh).
+//
+// CTA = (query tile, KV head, sequence).  Eight consumer warps each own
+// 16 / rep consecutive queries x all rep query heads of the KV head; a producer
+// lane streams the head's blocks (16 tokens x head_dim bytes of K and V) into
+// a ring that all of them read, up to the tile's last visible key.  Bound by
+// the consumers' conversions and products: each warp turns the block's e4m3
+// values into f16 for itself.
+#pragma once
+
+#include "attention.cuh"
+#include "decode_fp8.cuh"
+
+namespace pkv {
+namespace fp8 {
+
+using attn::PrefillParams;
+
+constexpr int kPrefillWarps = 8;
+constexpr int kPrefillTiles = 2;  // row tiles of 8 per warp
+constexpr int kPrefillRows = 8 * kPrefillTiles;
+
+template <typename T, int HD>
+__global__ void __launch_bounds__((kPrefillWarps + 1) * 32, 1)
+    prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const PrefillParams p,
+                   const Scales sc) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int b = blockIdx.z;
+  const int g = blockIdx.y;
+  const int q0 = __ldg(p.cu_q + b);
+  const int c = __ldg(p.cu_q + b + 1) - q0;
+  const int tile_q = kPrefillWarps * p.queries_per_warp;
+  const int i0 = blockIdx.x * tile_q;
+  if (i0 >= c) return;  // whole CTA idle: exit before touching barriers
+  if (q0 < 0 || int64_t(q0) + c > p.total_q) {  // offsets disagree with the query count
+    if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0) report(p.err, PKV_DEVERR_LENGTH);
+    return;
+  }
+  int L = __ldg(p.seq_lens + b);
+  if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0) {
+    if (L < c || L < 0) report(p.err, PKV_DEVERR_LENGTH);
+    else if (L > p.max_len)
+      report(p.err, L > p.W * kBS ? PKV_DEVERR_TABLE_WIDTH : PKV_DEVERR_LENGTH);
+  }
+  if (L > p.max_len) L = p.max_len;
+  if (L < c) return;  // inconsistent chunk: reported above, nothing computed
+  const int i_end = min(c, i0 + tile_q);
+  const int n_blocks = (L - c + i_end - 1) / kBS + 1;  // up to the last key any row sees
+
+  Ring ring = attn::make_tile_ring(smem, p.nstages, kBS * HD);
+  attn::ring_init(ring, kPrefillWarps);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t* row = p.bt + int64_t(b) * p.W;
+
+  if (warp == kPrefillWarps) {
+    uint32_t it = 0;
+    bool ok = true;
+    for (int jj = 0; jj < n_blocks && ok; jj += 32) {
+      const int id = jj + lane < n_blocks ? __ldg(row + jj + lane) : 0;
+      const int n_here = min(32, n_blocks - jj);
+      for (int k = 0; k < n_here; ++k) {
+        if (*ring.abort_flag) { ok = false; break; }
+        const int blk = __shfl_sync(0xffffffffu, id, k);
+        const bool good = blk >= 0 && blk < p.num_blocks;
+        if (!good && lane == 0) report(p.err, PKV_DEVERR_BLOCK_ID);
+        bool filled = true;
+        if (lane == 0)  // the chunk's other tiles read the block again: no eviction hint
+          filled = fetch(ring, it, &tm_k, &tm_v, (good ? blk : p.num_blocks) * kBS, g, p.err, 0);
+        if (!__shfl_sync(0xffffffffu, filled, 0)) {
+          *ring.abort_flag = 1;
+          ok = false;
+          break;
+        }
+        ++it;
+      }
+    }
+    if (!ok) attn::ring_drain(ring, it);
+  } else {
+    Rows<T, HD, kPrefillTiles, true> rows;
+    const T* q = static_cast<const T*>(p.q);
+    const int qw = i0 + warp * p.queries_per_warp;  // first query of this warp
+    const int nrows = p.queries_per_warp * p.rep;
+    auto query_of = [&](int r) { return qw + r / p.rep; };
+    auto head_of = [&](int r) { return g * p.rep + r % p.rep; };
+    DecodeParams dp{};  // what a scale batch needs of the pool
+    dp.num_blocks = p.num_blocks;
+    dp.n_kv = p.n_kv;
+    auto id_at = [&](int i) { return i < n_blocks ? __ldg(row + i) : -1; };
+    ScaleBatch now, next;
+    next.load(sc, dp, id_at(lane), g);
+    int ids = id_at(32 + lane);
+    rows.begin(
+        [&](int r) -> const T* {
+          if (r >= nrows || query_of(r) >= c) return nullptr;
+          return q + (int64_t(q0 + query_of(r)) * p.n_heads + head_of(r)) * HD;
+        },
+        [&](int r) { return L - c + query_of(r); }, p.scale_log2);
+    // this warp's last visible key
+    const int my_last = qw < c ? L - c + min(c, qw + p.queries_per_warp) - 1 : -1;
+    for (int k = 0; k < n_blocks; ++k) {
+      if ((k & 31) == 0) {
+        now = next;
+        now.settle();
+        next.load(sc, dp, ids, g);
+        ids = id_at(k + 64 + lane);
+      }
+      const float ks = __shfl_sync(0xffffffffu, now.ks, k & 31);
+      const float vs = __shfl_sync(0xffffffffu, now.vs, k & 31);
+      const float lv = __shfl_sync(0xffffffffu, now.lv, k & 31);
+      if (!attn::ring_wait_full(ring, k, p.err)) {
+        *ring.abort_flag = 1;
+        return;
+      }
+      if (k * kBS <= my_last) {
+        const int st = k % ring.nstages;
+        rows.block(ring.k_tile(st), ring.v_tile(st), k * kBS, L - k * kBS, ks, vs, lv);
+      }
+      attn::ring_release(ring, k);
+    }
+    T* out = static_cast<T*>(p.out);
+    rows.store([&](int r) -> T* {
+      if (r >= nrows || query_of(r) >= c) return nullptr;
+      return out + (int64_t(q0 + query_of(r)) * p.n_heads + head_of(r)) * HD;
+    });
+  }
+}
+
+template <typename T, int HD>
+cudaError_t prefill_run(const AttnArgs& a, const Scales& sc, cudaStream_t stream) {
+  const PoolShape& pool = a.pool;
+  PrefillParams p{};
+  p.q = a.q;
+  p.out = a.out;
+  p.bt = a.block_tables;
+  p.seq_lens = a.seq_lens;
+  p.cu_q = a.cu_q_lens;
+  p.err = a.err;
+  p.B = a.num_seqs;
+  p.n_heads = a.n_heads;
+  p.n_kv = pool.n_kv;
+  p.rep = a.n_heads / pool.n_kv;
+  p.W = a.max_blocks_per_seq;
+  p.num_blocks = pool.num_blocks;
+  p.max_len = std::min(a.max_seq_len, a.max_blocks_per_seq * kBS);
+  p.total_q = a.total_q;
+  p.scale_log2 = a.scale * attn::kLog2e;
+  p.queries_per_warp = kPrefillRows / p.rep;
+  p.nstages = 12;
+  const size_t smem = kBarrierBytes + 1024 + size_t(p.nstages) * 2 * kBS * HD;
+  CUtensorMap tm_k{}, tm_v{};
+  const uint64_t dims[3] = {HD, uint64_t(pool.num_blocks) * kBS, uint64_t(pool.n_kv)};
+  const uint64_t strides[2] = {uint64_t(pool.n_kv) * HD, HD};
+  const uint32_t box[3] = {HD, kBS, 1};
+  if (!encode_u8(&tm_k, a.k_pool, dims, strides, box, Tile<HD>::kSwizzle) ||
+      !encode_u8(&tm_v, a.v_pool, dims, strides, box, Tile<HD>::kSwizzle))
+    return cudaErrorInvalidValue;
+  static KernelSetup setup;
+  const int threads = (kPrefillWarps + 1) * 32;
+  cudaError_t e = kernel_setup(setup, prefill_kernel<T, HD>, static_cast<int>(smem), threads, nullptr);
+  if (e != cudaSuccess) return e;
+  const int tile_q = kPrefillWarps * p.queries_per_warp;
+  const int64_t tiles = (int64_t(a.max_q_len) + tile_q - 1) / tile_q;
+  if (tiles == 0 || a.num_seqs == 0) return cudaSuccess;
+  // the grid's y and z extents are 16-bit: long batches go in slices
+  for (int s0 = 0; s0 < a.num_seqs; s0 += 65535) {
+    PrefillParams ps = p;
+    ps.B = std::min(65535, a.num_seqs - s0);
+    ps.cu_q += s0;
+    ps.seq_lens += s0;
+    ps.bt += int64_t(s0) * p.W;
+    const dim3 grid(static_cast<unsigned>(tiles), pool.n_kv, ps.B);
+    prefill_kernel<T, HD><<<grid, threads, smem, stream>>>(tm_k, tm_v, ps, sc);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace fp8
+}  // namespace pkv

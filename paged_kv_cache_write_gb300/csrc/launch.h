@@ -104,6 +104,9 @@ bool fp8_attention_supported(const PoolShape& pool, int32_t n_heads);
 size_t decode_fp8_workspace_bytes(int32_t num_seqs, int32_t n_heads, int32_t head_dim);
 cudaError_t launch_decode_fp8(const AttnArgs& a, int32_t dtype, const float* k_scales,
                               const float* v_scales, cudaStream_t stream);
+// its tcgen05 path: bf16, head_dim 64 / 128
+cudaError_t launch_prefill_fp8_tc(const AttnArgs& a, const float* k_scales, const float* v_scales,
+                                  cudaStream_t stream);
 cudaError_t launch_prefill_fp8(const AttnArgs& a, int32_t dtype, const float* k_scales,
                                const float* v_scales, cudaStream_t stream);
 

@@ -1,5 +1,6 @@
-// Prefill over the 8-bit cache: the warp path for bf16 queries and the
-// dispatch by type (kernels in prefill_fp8.cuh).
+// Prefill over the 8-bit cache: the warp path for bf16 queries of narrow
+// heads (kernels in prefill_fp8.cuh) and the dispatch: bf16 queries of
+// head_dim 64 and 128 go to the tcgen05 kernel (prefill_fp8_tc.cu).
 #include "prefill_fp8.cuh"
 
 namespace pkv {
@@ -17,8 +18,7 @@ cudaError_t launch_prefill_fp8(const AttnArgs& a, int32_t dtype, const float* k_
   switch (a.pool.head_dim) {
     case 16: return prefill_run<__nv_bfloat16, 16>(a, sc, s);
     case 32: return prefill_run<__nv_bfloat16, 32>(a, sc, s);
-    case 64: return prefill_run<__nv_bfloat16, 64>(a, sc, s);
-    default: return prefill_run<__nv_bfloat16, 128>(a, sc, s);
+    default: return launch_prefill_fp8_tc(a, k_scales, v_scales, s);
   }
 }
 

@@ -1,0 +1,725 @@
+// Chunked prefill over the 8-bit cache on the 5th-generation tensor cores:
+// bf16 queries, head_dim 64 / 128.
+//
+// What is computed: query i of a chunk of c queries at the end of an L-token
+// sequence attends keys 0 .. L - c + i of its KV head, with element = e4m3
+// value x scale of (block, head).  With the byte values k8, v8 of a block:
+//   x = (q . k8) * (scale * log2 e * ks),  w = 2^(x + log2 vs - M + 11),
+//   l += (sum of the block's w) / vs,  O += w v8,  out = O / l.
+// M is a running reference of x + log2 vs, moved only when the maximum has
+// passed it by 2^4, so weights stay below 2^15: an f16 operand, and scales cost
+// nothing per element: they are constants of a 16-key block.
+//
+// tcgen05 takes no f16 x e4m3 product, so the cache's bytes become f16 (exact)
+// on their way into shared memory.  Queries become f16 too, each row times
+// the power of two that brings its largest element to 2^14 .. 2^15 (exact for
+// bf16 within 2^28 of it; undone in the score's factor).
+//
+// One CTA per SM owns two 128-row tiles, A and B, of one (sequence, KV head);
+// a row is one (query, query head) pair.  Keys go in tiles of 128 (8 blocks).
+//  warps 0-7    softmax of tile A, 8-15 of tile B.  Two threads per row, 64 of
+//               the 128 scores each (warps w and w + 4 hold the same TMEM
+//               lanes), so a tile's softmax, which its next products wait for,
+//               takes half as long; they exchange their maxima in shared
+//               memory.  Weights go back to TMEM as f16 over the scores.
+//  warp 16      allocates TMEM (S_A, S_B, O_A, O_B: all 512 columns at
+//               head_dim 128) and one lane issues the MMAs in ping-pong order:
+//               S_A, S_B, then for each tile once its weights are there
+//               O_X += W_X V_j and at once S_X = Q_X K_{j+1}^T.
+//  warps 17-23  bring K and V, a block (16 tokens) at a time in turn: 16-byte
+//               loads straight from the pool, each warp's next two blocks on
+//               their way, e4m3 -> f16 in registers, 128-byte-swizzled tiles
+//               in two-stage rings.
+// 24 warps leave 80 registers a thread, and no loop may spill: with 200 KB of
+// shared memory little L1 is left, and a reload from local memory costs an
+// L2 round trip.
+//
+// Values past the sequence's end are stored as zeros.  A NaN value that some
+// row of the tile may not see is stored as zero too, and its dim and first
+// position noted: rows that do see it get NaN at the end.  Every wait is
+// bounded; a thread that gave up still takes part in the CTA's barriers.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+
+#include "device.cuh"
+#include "fp8.cuh"
+#include "host_cache.h"
+#include "launch.h"
+#include "tcgen05.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kTileKeys = 128;
+constexpr int kBlk = 16;
+constexpr int kBlocks = kTileKeys / kBlk;  // blocks per key tile
+constexpr int kHalfKeys = kTileKeys / 2;   // scores of a softmax thread
+constexpr int kMmaWarp = 16;
+constexpr int kLoadWarp0 = 17;
+constexpr int kLoadWarps = 7;
+constexpr int kAhead = 2;  // blocks in flight per load warp
+constexpr int kThreads = 24 * 32;
+constexpr int kStages = 2;
+constexpr int kScaleStages = 4;  // scales outlive their K stage (see the load warps)
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleLog2 = 4.f;  // move the reference when the maximum passes it by 2^4
+constexpr float kWeightLog2 = 11.f;  // weights below 2^(11 + 4)
+constexpr uint32_t kTmemCols = 512;
+
+struct TcParams {
+  const __nv_bfloat16* q;
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  const float* k_scales;
+  const float* v_scales;
+  const int32_t* bt;
+  const int32_t* seq_lens;
+  const int32_t* cu_q;
+  __nv_bfloat16* out;
+  int32_t* err;
+  int B, n_heads, n_kv, rep, W, num_blocks, max_len, total_q, q_per_tile;
+  int ordered;
+  float scale_log2;
+};
+
+template <int HD>
+struct Layout {
+  static constexpr int NH = HD / 64;              // 128-byte column halves
+  static constexpr int HALF = kTileKeys * 128;    // 16 KB
+  static constexpr int TILE = NH * HALF;
+  static constexpr int K_OFF = 2 * TILE;          // after Q_A, Q_B
+  static constexpr int V_OFF = K_OFF + kStages * TILE;
+  static constexpr int XM_OFF = V_OFF + kStages * TILE;         // [turn][tile][half][128]
+  static constexpr int SCALE_OFF = XM_OFF + 2 * 2 * 2 * kRows * 4;  // ks, lv, 1/vs [stages][8]
+  static constexpr int NAN_OFF = SCALE_OFF + 3 * kScaleStages * kBlocks * 4;  // [HD] + flag
+  static constexpr int BAR_OFF = (NAN_OFF + HD * 4 + 16 + 15) / 16 * 16;
+  static constexpr int BYTES = BAR_OFF + 256;
+  // + 1 KB alignment slack; at least 120 KB so only one CTA fits per SM (it
+  // takes all 512 TMEM columns)
+  static constexpr int REQUEST = (BYTES + 1024) > 120 * 1024 ? (BYTES + 1024) : 120 * 1024;
+};
+
+// Instruction descriptor of kind::f16 with f16 A and B (format bits 0), fp32
+// accumulator; b_mn: B stored MN-major.
+constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn) {
+  return (1u << 4) | (uint32_t(b_mn) << 16) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+
+// The two warps (64 threads) that share rows 32 (w % 4) .. of tile x.
+__device__ __forceinline__ void pair_barrier(int x, int w) {
+  asm volatile("bar.sync %0, 64;" ::"r"(1 + x * 4 + (w & 3)) : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity) {
+  const bool ok = mbar_wait(bar, parity);
+  return __all_sync(0xffffffffu, ok);
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_fp8_tc_kernel(const TcParams p) {
+  using Lay = Layout<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+
+  // Work order, as in the bf16 prefill: with at most blockDim.x sequences, x
+  // numbers the (sequence, KV head, tile pair) triples, sequences by
+  // descending work and each one's pairs from the last (most keys) down;
+  // otherwise z, y, x in the natural order.  Work values are staged in the
+  // (still unused) V stages.
+  __shared__ int order_s, pair_s, head_s, job_s[4];
+  int g = blockIdx.y;
+  int b = blockIdx.z, pair = blockIdx.x;
+  if (p.ordered) {
+    const int t = threadIdx.x;
+    int64_t* work_s = reinterpret_cast<int64_t*>(smem + Lay::V_OFF);
+    int* seq_s = reinterpret_cast<int*>(work_s + p.B);  // [B] sequence of each rank
+    int* pairs_s = seq_s + p.B;                         // [B] pairs of each rank
+    const int qpp = 2 * p.q_per_tile;
+    int64_t wt = 0;
+    int pt = 0;
+    if (t < p.B) {
+      const int64_t cs = int64_t(__ldg(p.cu_q + t + 1)) - __ldg(p.cu_q + t);
+      const int64_t Ls = min(__ldg(p.seq_lens + t), p.max_len);
+      wt = cs * (2 * Ls - cs + 1);
+      pt = cs > 0 ? static_cast<int>((cs + qpp - 1) / qpp) : 0;
+      work_s[t] = wt;
+    }
+    if (t == 0) order_s = -1;
+    __syncthreads();
+    int rank = 0;
+    if (t < p.B) {
+      for (int s = 0; s < p.B; ++s) {
+        const int64_t ws = work_s[s];
+        rank += (ws > wt) || (ws == wt && s < t);
+      }
+      seq_s[rank] = t;
+      pairs_s[rank] = pt;
+    }
+    __syncthreads();
+    if (t < p.B) {  // rank t's first slot: the (head, pair) slots of the heavier ranks
+      int64_t first = 0;
+      for (int r = 0; r < t; ++r) first += pairs_s[r];
+      const int64_t x = blockIdx.x;
+      const int64_t lo = first * p.n_kv, n = int64_t(pairs_s[t]) * p.n_kv;
+      if (x >= lo && x < lo + n) {
+        const int off = static_cast<int>(x - lo);
+        order_s = seq_s[t];
+        head_s = off / pairs_s[t];
+        pair_s = pairs_s[t] - 1 - (off - (off / pairs_s[t]) * pairs_s[t]);
+      }
+    }
+    __syncthreads();
+    if (order_s < 0) return;  // slot past the last pair
+    b = order_s;
+    g = head_s;
+    pair = pair_s;
+  }
+  const int q0 = __ldg(p.cu_q + b);
+  const int c = __ldg(p.cu_q + b + 1) - q0;
+  const int i0 = pair * 2 * p.q_per_tile;  // first query of tile A
+  if (i0 >= c) return;                     // idle CTA: leave before any barrier or TMEM use
+  if (q0 < 0 || int64_t(q0) + c > p.total_q) {
+    if (threadIdx.x == 0 && i0 == 0 && g == 0) report(p.err, PKV_DEVERR_LENGTH);
+    return;
+  }
+  int L = __ldg(p.seq_lens + b);
+  if (threadIdx.x == 0 && i0 == 0 && g == 0) {
+    if (L < c || L < 0) report(p.err, PKV_DEVERR_LENGTH);
+    else if (L > p.max_len)
+      report(p.err, L > p.W * kBlk ? PKV_DEVERR_TABLE_WIDTH : PKV_DEVERR_LENGTH);
+  }
+  if (L > p.max_len) L = p.max_len;
+  if (L < c) return;
+  const int i_end = min(c, i0 + 2 * p.q_per_tile);
+  const int n_tiles = (L - c + i_end - 1) / kTileKeys + 1;
+  const int n_blocks_seq = (L + kBlk - 1) / kBlk;
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::BAR_OFF);
+  uint64_t* q_full = bars + 0;    // [2] per tile A/B
+  uint64_t* k_full = bars + 2;    // [2] per stage
+  uint64_t* k_empty = bars + 4;   // [2]
+  uint64_t* v_full = bars + 6;    // [2]
+  uint64_t* v_empty = bars + 8;   // [2]
+  uint64_t* s_full = bars + 10;   // [2] per tile
+  uint64_t* p_ready = bars + 12;  // [2] per tile
+  uint64_t* o_done = bars + 14;   // [2] per tile, once
+  uint64_t* drain = bars + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 17);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* ks_s = reinterpret_cast<float*>(smem + Lay::SCALE_OFF);  // [kScaleStages][8]
+  float* lv_s = ks_s + kScaleStages * kBlocks;
+  float* iv_s = lv_s + kScaleStages * kBlocks;
+  float* xm_s = reinterpret_cast<float*>(smem + Lay::XM_OFF);  // [turn][tile][half][row]
+  int* nan_s = reinterpret_cast<int*>(smem + Lay::NAN_OFF);    // [HD] first NaN position
+  int* nan_any = nan_s + HD;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + i, 8);
+      mbar_init(k_full + i, kBlocks);
+      mbar_init(k_empty + i, 1);
+      mbar_init(v_full + i, kBlocks);
+      mbar_init(v_empty + i, 1);
+      mbar_init(s_full + i, 1);
+      mbar_init(p_ready + i, 8);
+      mbar_init(o_done + i, 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *nan_any = 0;
+    job_s[0] = i0;
+    job_s[1] = c;
+    job_s[2] = q0;
+    job_s[3] = g;
+    fence_barrier_init();
+  }
+  if (threadIdx.x < HD) nan_s[threadIdx.x] = INT_MAX;
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(tmem_slot, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  auto q_tile = [&](int x) { return smem + x * Lay::TILE; };
+  auto k_st = [&](int j) { return smem + Lay::K_OFF + (j % kStages) * Lay::TILE; };
+  auto v_st = [&](int j) { return smem + Lay::V_OFF + (j % kStages) * Lay::TILE; };
+  auto s_tm = [&](int x) { return tmem + uint32_t(x) * kTileKeys; };
+  auto o_tm = [&](int x) { return tmem + 256u + uint32_t(x) * 128u; };
+
+  if (warp >= kLoadWarp0) {
+    // ------------------------------------------------------ K and V tiles
+    // Unit 16 j + i is block i of K tile j, unit 16 j + 8 + i of V tile j; the
+    // warps take them in turn.  A step of the warp covers 32 / PR rows; lane:
+    // 16-byte piece lane % PR.  At head_dim 128 the lanes of a row's second
+    // half take their piece from the row's neighbour, so that the eight lanes
+    // of a store phase, whose pieces are then even ones of one row and odd ones
+    // of the other, touch each bank once.
+    constexpr int PR = HD / 16;    // pieces of a row
+    constexpr int RS = 32 / PR;    // rows per step: 4 or 8
+    constexpr int NV = kBlk / RS;  // steps: 4 or 2
+    const int piece = lane % PR, half = piece >> 2;
+    const int r0 = HD == 128 ? (lane / PR) ^ half : lane / PR;  // row of step 0
+    const int32_t* row = p.bt + int64_t(b) * p.W;
+    const int pitch = p.n_kv * HD;
+    const int lane_off = r0 * pitch + g * HD + piece * 16;
+    const int step_off = RS * pitch;
+    // where the lane's piece (16 dims: two 16-byte pieces of f16) goes in row
+    // r0 + RS i of a block: (r0 + RS i) % 8 is r0, and r0 + 4 in odd steps of 4
+    const int at = (piece & 3) * 2;
+    const int put_lo = half * Lay::HALF + r0 * 128 + ((at ^ r0) << 4);
+    const int put_hi = half * Lay::HALF + r0 * 128 + (((at + 1) ^ r0) << 4);
+    const int n_units = 2 * kBlocks * n_tiles;
+    // -1: nothing there, or a bad id
+    auto id_of = [&](int u) {
+      const int jb = (u >> 4) * kBlocks + (u & 7);
+      int id = -1;
+      if (u < n_units && jb < n_blocks_seq) id = __ldg(row + jb);
+      return id;
+    };
+    uint4 d[kAhead][NV];
+    float sk[kAhead], sv[kAhead];  // scales of a K unit's block (every lane alike)
+    int id_d[kAhead], id_next[kAhead];
+    // (unconditional loads, of block 0 where there is none, so that they stay
+    // in flight: a selected load is waited for where it is issued)
+    auto fetch = [&](uint4 (&x)[NV], float& ks, float& vs, int& id, int u) {
+      if (id >= p.num_blocks || id < -1) id = -2;  // reported when it is stored
+      const int blk = max(id, 0);
+      const uint8_t* src = ((u & 8) ? p.v_pool : p.k_pool) + int64_t(blk) * (kBlk * pitch) + lane_off;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) x[i] = __ldg(reinterpret_cast<const uint4*>(src + i * step_off));
+      if (!(u & 8)) {
+        ks = __ldg(p.k_scales + int64_t(blk) * p.n_kv + g);
+        vs = __ldg(p.v_scales + int64_t(blk) * p.n_kv + g);
+      }
+    };
+    const int w = warp - kLoadWarp0;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int u = w + k * kLoadWarps;
+      id_d[k] = id_of(u);
+      fetch(d[k], sk[k], sv[k], id_d[k], u);
+      id_next[k] = id_of(u + kAhead * kLoadWarps);
+    }
+    bool ok = true;
+    for (int u0 = w; u0 < n_units && ok; u0 += kAhead * kLoadWarps) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int u = u0 + k * kLoadWarps;
+        if (u >= n_units || !ok) break;
+        const int j = u >> 4, bi = u & 7;
+        const bool is_v = (u & 8) != 0;
+        const int st = j % kStages;
+        const uint32_t use = j / kStages;
+        if (use > 0 && !wait_all((is_v ? v_empty : k_empty) + st, (use - 1) & 1)) {
+          if (lane == 0) {
+            report(p.err, PKV_DEVERR_TIMEOUT);
+            *abort_flag = 1;
+          }
+          ok = false;
+          break;
+        }
+        const int pos0 = (j * kBlocks + bi) * kBlk;
+        if (!is_v && lane == 0) {
+          // The scales of tile j - 4 are no longer read: K stage j was free, so
+          // S_{j-2} is complete, so W_{j-3} was there, so softmax j - 4 is over.
+          const int o = (j % kScaleStages) * kBlocks + bi;
+          if (id_d[k] == -2) report(p.err, PKV_DEVERR_BLOCK_ID);
+          const bool good = id_d[k] >= 0;
+          ks_s[o] = good ? sk[k] : 1.f;
+          lv_s[o] = good ? __log2f(sv[k]) : 0.f;
+          iv_s[o] = good ? __fdividef(1.f, sv[k]) : 1.f;
+        }
+        if (id_d[k] < 0 || pos0 + kBlk > L) {
+          // what lies past the sequence's end, and a bad block, is zeros
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+            if (id_d[k] < 0 || pos0 + r0 + RS * i >= L) d[k][i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (is_v && pos0 + kBlk > L - c + i0 + 1) {
+          // some row may not see some key of this block: take out its NaNs
+          const int first_last = L - c + i0;  // the last key that the pair's first query sees
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            const int pos = pos0 + r0 + RS * i;
+            uint32_t v4[4] = {d[k][i].x, d[k][i].y, d[k][i].z, d[k][i].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t bad = __vcmpeq4(v4[q] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              if (bad != 0 && pos > first_last) {
+                for (int e = 0; e < 4; ++e)
+                  if ((bad >> (8 * e)) & 1u) atomicMin(nan_s + piece * 16 + 4 * q + e, pos);
+                v4[q] &= ~bad;
+                atomicOr(nan_any, 1);
+              }
+            }
+            d[k][i] = make_uint4(v4[0], v4[1], v4[2], v4[3]);
+          }
+        }
+        uint8_t* base = (is_v ? v_st(j) : k_st(j)) + bi * (kBlk * 128);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const uint32_t x[4] = {d[k][i].x, d[k][i].y, d[k][i].z, d[k][i].w};
+          uint32_t f[8];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            f[2 * q] = e4m3x2_to_f16x2(static_cast<uint16_t>(x[q]));
+            f[2 * q + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(x[q] >> 16));
+          }
+          // piece q of row r sits at q ^ (r % 8)
+          const int odd4 = (RS * i) & 4 ? 64 : 0;
+          uint8_t* dst = base + i * RS * 128;
+          *reinterpret_cast<uint4*>(dst + (put_lo ^ odd4)) = make_uint4(f[0], f[1], f[2], f[3]);
+          *reinterpret_cast<uint4*>(dst + (put_hi ^ odd4)) = make_uint4(f[4], f[5], f[6], f[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive((is_v ? v_full : k_full) + st);
+        const int un = u + kAhead * kLoadWarps;
+        id_d[k] = id_next[k];
+        fetch(d[k], sk[k], sv[k], id_d[k], un);
+        id_next[k] = id_of(un + kAhead * kLoadWarps);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ----------------------------------------------------------------- MMA
+    if (lane == 0) {
+      constexpr uint32_t idesc_qk = idesc_f16_f32(kRows, kTileKeys, false);
+      constexpr uint32_t idesc_pv = idesc_f16_f32(kRows, HD, true);
+      auto issue_qk = [&](int x, int j) {
+        const uint32_t q_addr = smem_addr(q_tile(x));
+        const uint32_t k_addr = smem_addr(k_st(j));
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * Lay::HALF + (kk & 3) * 32;
+          tc::mma_ss(s_tm(x), tc::sw128_desc(q_addr + off, 16, 1024),
+                     tc::sw128_desc(k_addr + off, 16, 1024), idesc_qk, kk > 0);
+        }
+        tc::commit(s_full + x);
+      };
+      auto issue_pv = [&](int x, int j) {
+        const uint32_t v_addr = smem_addr(v_st(j));
+#pragma unroll
+        for (int kk = 0; kk < kTileKeys / 16; ++kk) {
+          // W: the softmax halves' 32 columns at columns 0 and 64 of S
+          const uint32_t w_col = (kk >> 2) * 64 + (kk & 3) * 8;
+          tc::mma_ts(o_tm(x), s_tm(x) + w_col,
+                     tc::sw128_desc(v_addr + kk * 2048, Lay::HALF, 1024), idesc_pv,
+                     j > 0 || kk > 0);
+        }
+      };
+      bool ok = mbar_wait(k_full, 0);
+      for (int x = 0; x < 2 && ok; ++x) {
+        if (!(ok = mbar_wait(q_full + x, 0))) break;
+        tc::fence_after_sync();
+        issue_qk(x, 0);
+      }
+      if (ok) tc::commit(k_empty);  // K_0 is no longer read
+      for (int j = 0; j < n_tiles && ok; ++j) {
+        const bool more = j + 1 < n_tiles;
+        const int kn = (j + 1) % kStages;
+        for (int x = 0; x < 2 && ok; ++x) {
+          if (!(ok = mbar_wait(p_ready + x, j & 1))) break;
+          if (x == 0 && !(ok = mbar_wait(v_full + (j % kStages), (j / kStages) & 1))) break;
+          if (x == 0 && more && !(ok = mbar_wait(k_full + kn, ((j + 1) / kStages) & 1))) break;
+          tc::fence_after_sync();
+          issue_pv(x, j);
+          if (x == 1) tc::commit(v_empty + (j % kStages));  // V_j is no longer read
+          if (more) issue_qk(x, j + 1);
+          else tc::commit(o_done + x);
+          if (x == 1 && more) tc::commit(k_empty + kn);  // K_{j+1} is no longer read
+        }
+      }
+      if (!ok) {
+        report(p.err, PKV_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // every MMA issued above has finished before TMEM is released
+      tc::commit(drain);
+      mbar_wait(drain, 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- softmax
+    const int x = warp >> 3;               // tile A or B
+    const int hf = (warp >> 2) & 1;        // half of the keys (and of the dims)
+    const int r = (warp & 3) * 32 + lane;  // TMEM lane = row of the tile
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    // the thread's row (its query, or -1) and where its half of it lies in q
+    // and out; what this needs is read back from shared memory at the end, so
+    // that it takes no registers in between
+    struct Row {
+      int qi;
+      int64_t off;
+    };
+    auto my_row = [&]() {
+      const volatile int* job = job_s;
+      const int q = r / p.rep;
+      const int qi = job[0] + x * p.q_per_tile + q;  // i0 + ...
+      const bool active = q < p.q_per_tile && qi < job[1];
+      return Row{active ? qi : -1,
+                 (int64_t(job[2] + qi) * p.n_heads + job[3] * p.rep + (r - q * p.rep)) * HD +
+                     hf * (HD / 2)};
+    };
+    int last;
+    // exchange with the row's other thread; the two places take turns, so one
+    // barrier per exchange is enough (a place is written again only after the
+    // next exchange's barrier, which the other thread passes having read it)
+    auto exchange = [&](float v, int turn) {
+      const int mine = ((turn & 1) * 4 + x * 2 + hf) * kRows + r;
+      xm_s[mine] = v;
+      pair_barrier(x, warp);
+      return xm_s[mine ^ kRows];
+    };
+    float rs;  // undoes the row's power of two; times scale * log2 e
+    {
+      const Row me = my_row();
+      last = me.qi >= 0 ? L - c + me.qi : -1;
+      uint4 u[HD / 16];
+      float a = 0.f;
+#pragma unroll
+      for (int i = 0; i < HD / 16; ++i) {
+        u[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (me.qi >= 0) u[i] = __ldg(reinterpret_cast<const uint4*>(p.q + me.off) + i);
+        const uint32_t e[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          a = fmaxf(a, fmaxf(fabsf(__uint_as_float(e[k] << 16)),
+                             fabsf(__uint_as_float(e[k] & 0xffff0000u))));
+      }
+      a = fmaxf(a, exchange(a, 0));
+      const int up = min(126, 14 + 127 - static_cast<int>(__float_as_uint(a) >> 23));
+      const float f = pow2f(up);
+      rs = pow2f(-up) * p.scale_log2;
+#pragma unroll
+      for (int i = 0; i < HD / 16; ++i) {
+        const uint32_t e[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          o[k] = pack_f16x2(__uint_as_float(e[k] << 16) * f, __uint_as_float(e[k] & 0xffff0000u) * f);
+        const int d16 = hf * (HD / 16) + i;  // 16-byte piece of the row
+        *reinterpret_cast<uint4*>(q_tile(x) + (d16 >> 3) * Lay::HALF + r * 128 +
+                                  (((d16 & 7) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full + x);
+    }
+    float m_used = -INFINITY, l_sum = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n_tiles; ++j) {
+      // (every thread passes the same barriers whatever happens to its waits)
+      if (ok && !(ok = wait_all(s_full + x, j & 1)) && lane == 0) {
+        report(p.err, PKV_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      tc::fence_after_sync();
+      const uint32_t s_addr = s_tm(x) + lane_base + hf * kHalfKeys;
+      const int pos0 = j * kTileKeys + hf * kHalfKeys;
+      // 32 scores; keys past this row's causal limit are -inf
+      auto load = [&](uint32_t (&v)[32], int ch) {
+        tc::tmem_ld32(s_addr + ch * 32, v);
+        tc::tmem_wait_ld();
+        if (pos0 + ch * 32 + 31 > last) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (pos0 + ch * 32 + k > last) v[k] = __float_as_uint(-INFINITY);
+        }
+      };
+      const float* ks = ks_s + (j % kScaleStages) * kBlocks + hf * 4;
+      // (factors are > 0; none is zero: -inf stays -inf)
+      auto factor = [&](int bk) { return fmaxf(rs * ks[bk], 1.2e-38f); };
+      auto shift = [&](int bk) { return ks[kScaleStages * kBlocks + bk]; };  // log2 vs
+      auto inv_vs = [&](int bk) { return ks[2 * kScaleStages * kBlocks + bk]; };
+      // maximum of x + log2 vs, block by block
+      auto top = [&](const uint32_t (&v)[32], int ch) {
+        float t = -INFINITY;
+#pragma unroll
+        for (int bb = 0; bb < 2; ++bb) {
+          float mb = __uint_as_float(v[bb * 16]);
+#pragma unroll
+          for (int k = 1; k < 16; ++k) mb = fmaxf(mb, __uint_as_float(v[bb * 16 + k]));
+          t = fmaxf(t, fmaf(mb, factor(ch * 2 + bb), shift(ch * 2 + bb)));
+        }
+        return t;
+      };
+      // Two chunks of 32 scores.  Both at once would not fit the registers; the
+      // second is read from TMEM twice (weights overwrite the first one's place).
+      uint32_t v[32];
+      load(v, 1);
+      float mx = top(v, 1);
+      load(v, 0);
+      mx = fmaxf(mx, top(v, 0));
+      mx = fmaxf(mx, exchange(mx, j + 1));
+      const float m_new = fmaxf(m_used, mx);
+      const bool grow = m_new > m_used + kRescaleLog2;
+      const float alpha = grow ? fast_exp2(m_used - m_new) : 1.f;
+      if (grow) m_used = m_new;
+      const float mref = (m_used == -INFINITY ? 0.f : m_used) - kWeightLog2;
+      float add = 0.f;
+#pragma unroll
+      for (int ch = 0; ch < 2; ++ch) {
+        if (ch == 1) load(v, 1);
+        uint32_t pk[16];
+#pragma unroll
+        for (int bb = 0; bb < 2; ++bb) {
+          const int bk = ch * 2 + bb;
+          const float f = factor(bk), cst = shift(bk) - mref;
+          const float2 f2 = make_float2(f, f), c2 = make_float2(cst, cst);
+          float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int e = bb * 16 + 2 * k;
+            const float2 t2 =
+                __ffma2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), f2, c2);
+            const float2 pe = make_float2(fast_exp2(t2.x), fast_exp2(t2.y));
+            acc = __fadd2_rn(acc, pe);
+            pk[bb * 8 + k] = pack_f16x2(pe.x, pe.y);
+          }
+          add = fmaf(acc.x + acc.y, inv_vs(bk), add);
+        }
+        tc::tmem_st16(s_addr + ch * 16, pk);
+      }
+      l_sum = l_sum * alpha + add;
+      // (S_j complete implies the products W_{j-1} V_{j-1} before it are)
+      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll 1
+        for (int ch = 0; ch < HD / 64; ++ch) {
+          const uint32_t o_addr = o_tm(x) + lane_base + hf * (HD / 2) + ch * 32;
+          uint32_t ov[32];
+          tc::tmem_ld32(o_addr, ov);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float2 o2 = __fmul2_rn(
+                make_float2(__uint_as_float(ov[2 * k]), __uint_as_float(ov[2 * k + 1])), a2);
+            ov[2 * k] = __float_as_uint(o2.x);
+            ov[2 * k + 1] = __float_as_uint(o2.y);
+          }
+          tc::tmem_st32(o_addr, ov);
+        }
+      }
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_ready + x);
+    }
+    l_sum += exchange(l_sum, n_tiles + 1);
+    if (ok && !(ok = wait_all(o_done + x, 0)) && lane == 0) {
+      report(p.err, PKV_DEVERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+    if (ok) {
+      tc::fence_after_sync();
+      const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
+      const bool nans = *static_cast<volatile int*>(nan_any) != 0;
+      const Row me = my_row();
+      __nv_bfloat16* orow = p.out + me.off;
+#pragma unroll 1
+      for (int ch = 0; ch < HD / 64; ++ch) {
+        uint32_t ov[32];
+        tc::tmem_ld32(o_tm(x) + lane_base + hf * (HD / 2) + ch * 32, ov);
+        tc::tmem_wait_ld();
+        if (nans) {
+          const volatile int* first = nan_s + hf * (HD / 2) + ch * 32;
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (first[k] <= last) ov[k] = 0x7fc00000u;
+        }
+        if (me.qi >= 0) {
+          uint4* dst = reinterpret_cast<uint4*>(orow + ch * 32);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[e] = pack_bf16x2(__uint_as_float(ov[8 * k + 2 * e]) * inv,
+                                 __uint_as_float(ov[8 * k + 2 * e + 1]) * inv);
+            dst[k] = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+      }
+    }
+  }
+  // ------------------------------------------------------------ teardown
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int HD>
+cudaError_t run_tc(const AttnArgs& a, const float* k_scales, const float* v_scales,
+                   cudaStream_t stream) {
+  using Lay = Layout<HD>;
+  const PoolShape& pool = a.pool;
+  const int rep = a.n_heads / pool.n_kv;
+  TcParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.k_pool = static_cast<const uint8_t*>(a.k_pool);
+  p.v_pool = static_cast<const uint8_t*>(a.v_pool);
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.err = a.err;
+  p.n_heads = a.n_heads;
+  p.n_kv = pool.n_kv;
+  p.rep = rep;
+  p.W = a.max_blocks_per_seq;
+  p.num_blocks = pool.num_blocks;
+  p.max_len = std::min(a.max_seq_len, a.max_blocks_per_seq * kBlk);
+  p.total_q = a.total_q;
+  p.q_per_tile = kRows / rep;
+  p.scale_log2 = a.scale * kLog2e;
+  auto kern = prefill_fp8_tc_kernel<HD>;
+  static KernelSetup setup;
+  cudaError_t e = kernel_setup(setup, kern, Lay::REQUEST, kThreads, nullptr);
+  if (e != cudaSuccess) return e;
+  const int qpp = 2 * p.q_per_tile;
+  // ordered: one slot per (sequence, KV head, pair); the pairs number at most
+  // total_q / qpp + one partial pair per sequence
+  const int64_t slots = ((int64_t(a.total_q) + qpp - 1) / qpp + a.num_seqs) * pool.n_kv;
+  p.ordered = a.num_seqs <= kThreads && slots <= INT_MAX;
+  // natural order: the grid's z extent is 16-bit, so long batches go in slices
+  const int slice = p.ordered ? a.num_seqs : 65535;
+  for (int s0 = 0; s0 < a.num_seqs; s0 += slice) {
+    p.B = std::min(slice, a.num_seqs - s0);
+    p.bt = a.block_tables + int64_t(s0) * p.W;
+    p.seq_lens = a.seq_lens + s0;
+    p.cu_q = a.cu_q_lens + s0;
+    const dim3 grid = p.ordered ? dim3(static_cast<unsigned>(slots), 1, 1)
+                                : dim3((a.max_q_len + qpp - 1) / qpp, pool.n_kv, p.B);
+    kern<<<grid, kThreads, Lay::REQUEST, stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_fp8_tc(const AttnArgs& a, const float* k_scales, const float* v_scales,
+                                  cudaStream_t stream) {
+  return a.pool.head_dim == 64 ? run_tc<64>(a, k_scales, v_scales, stream)
+                               : run_tc<128>(a, k_scales, v_scales, stream);
+}
+
+}  // namespace pkv

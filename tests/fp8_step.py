@@ -88,7 +88,7 @@ class Batch:
         return tuple(paged_fp8.values(p[blocks], s[blocks]).reshape(-1, self.n_kv, self.hd)[:n]
                      for p, s in ((self.kp, self.ks), (self.vp, self.vs)))
 
-    def reference(self, q, b, last):
+    def reference(self, q, b, last, held=15):
         """(output, tolerance) [H, hd] in float64 of one query over keys 0..last.
 
         Tolerance, to first order.  The output is sum(w v) / sum(p).  Scores
@@ -103,9 +103,9 @@ class Batch:
 
         f16 has an absolute floor besides: a value below 2^-14 is rounded by up
         to 2^-25.  Weights times value scale (p vs) are held with their
-        largest at 2^15, so the numerator is off by at most 2^-25 sum |v / vs|
-        where its largest p vs is 2^15, which is 2^-40 max(p vs) sum |v / vs|
-        with p normalised (parts and earlier blocks, whose largest is smaller,
+        largest at 2^held or more, so the numerator is off by at most
+        2^-25 sum |v / vs| where its largest p vs is 2^held, which is
+        2^-(25 + held) max(p vs) sum |v / vs| with p normalised (parts and earlier blocks, whose largest is smaller,
         are off by less).  A query row is held with its largest element at
         2^14 or more: a score is off by at most 2^-39 max |q| sum |k|.
         """
@@ -131,15 +131,16 @@ class Batch:
                    + 2.0 ** -20 * max(1.0, S / 8) + own)
             vs = vs_of[:, h // rep]
             tol[h] = (half * np.abs(out[h]) + 2 * rel * (p @ np.abs(v))
-                      + 2.0 ** -40 * (p * vs).max() * (np.abs(v) / vs[:, None]).sum(axis=0) + 1e-30)
+                      + 2.0 ** -(25 + held) * (p * vs).max() * (np.abs(v) / vs[:, None]).sum(axis=0) + 1e-30)
         return out, tol
 
-    def check(self, got, q, which, last):
-        """got, q [rows, H, hd]; row i is sequence which[i]'s, over keys 0..last[i]."""
+    def check(self, got, q, which, last, held=15):
+        """got, q [rows, H, hd]; row i is sequence which[i]'s, over keys 0..last[i].
+        held: 15, or 11 for the prefill, whose reference may lag its maximum by 2^4."""
         got, q = f64(got), f64(q)
         worst = 0.0
         for i, (b, n) in enumerate(zip(which, last)):
-            ref, tol = self.reference(q[i], b, n)
+            ref, tol = self.reference(q[i], b, n, held)
             assert np.all(np.isfinite(got[i])), (i, b, n)
             worst = max(worst, float(np.max(np.abs(got[i] - ref) / tol)) if n >= 0
                         else float(np.abs(got[i]).max()))

@@ -16,20 +16,21 @@
 // bf16 within 2^28 of it; undone in the score's factor).
 //
 // One CTA per SM owns two 128-row tiles, A and B, of one (sequence, KV head);
-// a row is one (query, query head) pair.  Keys go in tiles of 128 (8 blocks).
-//  warps 0-7    softmax of tile A, 8-15 of tile B.  Two threads per row, 64 of
-//               the 128 scores each (warps w and w + 4 hold the same TMEM
-//               lanes), so a tile's softmax, which its next products wait for,
-//               takes half as long; they exchange their maxima in shared
-//               memory.  Weights go back to TMEM as f16 over the scores.
-//  warp 16      allocates TMEM (S_A, S_B, O_A, O_B: all 512 columns at
-//               head_dim 128) and one lane issues the MMAs in ping-pong order:
-//               S_A, S_B, then for each tile once its weights are there
-//               O_X += W_X V_j and at once S_X = Q_X K_{j+1}^T.
+// a row is one (query, query head) pair.  Keys go in tiles of 64 (4 blocks), so
+// that scores have two buffers per row tile in TMEM: while a tile's softmax
+// runs, its next scores are computed, and neither waits for the other.
+//  warps 0-7    softmax of tile A, 8-15 of tile B.  Two threads per row, 32 of
+//               the 64 scores each (warps w and w + 4 hold the same TMEM
+//               lanes); they exchange their maxima in shared memory.  Weights
+//               go back to TMEM as f16 over the scores.
+//  warp 16      allocates TMEM (2 S_A, 2 S_B, O_A, O_B: all 512 columns at
+//               head_dim 128) and one lane issues the MMAs: S_X of the first
+//               two key tiles, then for each key tile j and row tile X, once
+//               its weights are there, O_X += W_X V_j and S_X = Q_X K_{j+2}^T.
 //  warps 17-23  bring K and V, a block (16 tokens) at a time in turn: 16-byte
 //               loads straight from the pool, each warp's next two blocks on
 //               their way, e4m3 -> f16 in registers, 128-byte-swizzled tiles
-//               in two-stage rings.
+//               in four-stage rings.
 // 24 warps leave 80 registers a thread, and no loop may spill: with 200 KB of
 // shared memory little L1 is left, and a reload from local memory costs an
 // L2 round trip.
@@ -56,17 +57,18 @@ namespace pkv {
 namespace {
 
 constexpr int kRows = 128;
-constexpr int kTileKeys = 128;
+constexpr int kTileKeys = 64;
 constexpr int kBlk = 16;
 constexpr int kBlocks = kTileKeys / kBlk;  // blocks per key tile
 constexpr int kHalfKeys = kTileKeys / 2;   // scores of a softmax thread
+static_assert(kBlocks == 4 && kHalfKeys == 32, "units and chunks below");
 constexpr int kMmaWarp = 16;
 constexpr int kLoadWarp0 = 17;
 constexpr int kLoadWarps = 7;
 constexpr int kAhead = 2;  // blocks in flight per load warp
 constexpr int kThreads = 24 * 32;
-constexpr int kStages = 2;
-constexpr int kScaleStages = 4;  // scales outlive their K stage (see the load warps)
+constexpr int kStages = 4;
+constexpr int kScaleStages = 8;  // scales outlive their K stage (see the load warps)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 4.f;  // move the reference when the maximum passes it by 2^4
 constexpr float kWeightLog2 = 11.f;  // weights below 2^(11 + 4)
@@ -90,16 +92,18 @@ struct TcParams {
 
 template <int HD>
 struct Layout {
-  static constexpr int NH = HD / 64;              // 128-byte column halves
-  static constexpr int HALF = kTileKeys * 128;    // 16 KB
-  static constexpr int TILE = NH * HALF;
-  static constexpr int K_OFF = 2 * TILE;          // after Q_A, Q_B
-  static constexpr int V_OFF = K_OFF + kStages * TILE;
-  static constexpr int XM_OFF = V_OFF + kStages * TILE;         // [turn][tile][half][128]
-  static constexpr int SCALE_OFF = XM_OFF + 2 * 2 * 2 * kRows * 4;  // ks, lv, 1/vs [stages][8]
+  static constexpr int NH = HD / 64;               // 128-byte column halves
+  static constexpr int Q_HALF = kRows * 128;       // 16 KB
+  static constexpr int KV_HALF = kTileKeys * 128;  // 8 KB
+  static constexpr int Q_TILE = NH * Q_HALF;
+  static constexpr int KV_TILE = NH * KV_HALF;
+  static constexpr int K_OFF = 2 * Q_TILE;  // after Q_A, Q_B
+  static constexpr int V_OFF = K_OFF + kStages * KV_TILE;
+  static constexpr int XM_OFF = V_OFF + kStages * KV_TILE;          // [turn][tile][half][128]
+  static constexpr int SCALE_OFF = XM_OFF + 2 * 2 * 2 * kRows * 4;  // ks, lv, 1/vs [stages][4]
   static constexpr int NAN_OFF = SCALE_OFF + 3 * kScaleStages * kBlocks * 4;  // [HD] + flag
   static constexpr int BAR_OFF = (NAN_OFF + HD * 4 + 16 + 15) / 16 * 16;
-  static constexpr int BYTES = BAR_OFF + 256;
+  static constexpr int BYTES = BAR_OFF + 512;
   // + 1 KB alignment slack; at least 120 KB so only one CTA fits per SM (it
   // takes all 512 TMEM columns)
   static constexpr int REQUEST = (BYTES + 1024) > 120 * 1024 ? (BYTES + 1024) : 120 * 1024;
@@ -114,6 +118,12 @@ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn) {
 // The two warps (64 threads) that share rows 32 (w % 4) .. of tile x.
 __device__ __forceinline__ void pair_barrier(int x, int w) {
   asm volatile("bar.sync %0, 64;" ::"r"(1 + x * 4 + (w & 3)) : "memory");
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -207,18 +217,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_blocks_seq = (L + kBlk - 1) / kBlk;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::BAR_OFF);
-  uint64_t* q_full = bars + 0;    // [2] per tile A/B
-  uint64_t* k_full = bars + 2;    // [2] per stage
-  uint64_t* k_empty = bars + 4;   // [2]
-  uint64_t* v_full = bars + 6;    // [2]
-  uint64_t* v_empty = bars + 8;   // [2]
-  uint64_t* s_full = bars + 10;   // [2] per tile
-  uint64_t* p_ready = bars + 12;  // [2] per tile
-  uint64_t* o_done = bars + 14;   // [2] per tile, once
-  uint64_t* drain = bars + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 17);
+  uint64_t* q_full = bars + 0;         // [2] per row tile
+  uint64_t* k_full = bars + 2;         // [4] per stage
+  uint64_t* k_empty = bars + 6;        // [4]
+  uint64_t* v_full = bars + 10;        // [4]
+  uint64_t* v_empty = bars + 14;       // [4]
+  uint64_t* s_full = bars + 18;        // [row tile][buffer]
+  uint64_t* w_ready = bars + 22;       // [row tile][buffer]
+  uint64_t* o_done = bars + 26;        // [row tile][key tile % 2]
+  uint64_t* drain = bars + 30;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 31);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* ks_s = reinterpret_cast<float*>(smem + Lay::SCALE_OFF);  // [kScaleStages][8]
+  float* ks_s = reinterpret_cast<float*>(smem + Lay::SCALE_OFF);  // [kScaleStages][4]
   float* lv_s = ks_s + kScaleStages * kBlocks;
   float* iv_s = lv_s + kScaleStages * kBlocks;
   float* xm_s = reinterpret_cast<float*>(smem + Lay::XM_OFF);  // [turn][tile][half][row]
@@ -228,15 +238,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + i, 8);
+    for (int i = 0; i < 2; ++i) mbar_init(q_full + i, 8);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(w_ready + i, 8);
+      mbar_init(o_done + i, 1);
+    }
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(k_full + i, kBlocks);
       mbar_init(k_empty + i, 1);
       mbar_init(v_full + i, kBlocks);
       mbar_init(v_empty + i, 1);
-      mbar_init(s_full + i, 1);
-      mbar_init(p_ready + i, 8);
-      mbar_init(o_done + i, 1);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -256,15 +268,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  auto q_tile = [&](int x) { return smem + x * Lay::TILE; };
-  auto k_st = [&](int j) { return smem + Lay::K_OFF + (j % kStages) * Lay::TILE; };
-  auto v_st = [&](int j) { return smem + Lay::V_OFF + (j % kStages) * Lay::TILE; };
-  auto s_tm = [&](int x) { return tmem + uint32_t(x) * kTileKeys; };
+  auto q_tile = [&](int x) { return smem + x * Lay::Q_TILE; };
+  auto k_st = [&](int j) { return smem + Lay::K_OFF + (j % kStages) * Lay::KV_TILE; };
+  auto v_st = [&](int j) { return smem + Lay::V_OFF + (j % kStages) * Lay::KV_TILE; };
+  auto s_tm = [&](int x, int j) { return tmem + uint32_t(x * 2 + (j & 1)) * kTileKeys; };
   auto o_tm = [&](int x) { return tmem + 256u + uint32_t(x) * 128u; };
 
   if (warp >= kLoadWarp0) {
     // ------------------------------------------------------ K and V tiles
-    // Unit 16 j + i is block i of K tile j, unit 16 j + 8 + i of V tile j; the
+    // Unit 8 j + i is block i of K tile j, unit 8 j + 4 + i of V tile j; the
     // warps take them in turn.  A step of the warp covers 32 / PR rows; lane:
     // 16-byte piece lane % PR.  At head_dim 128 the lanes of a row's second
     // half take their piece from the row's neighbour, so that the eight lanes
@@ -282,12 +294,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // where the lane's piece (16 dims: two 16-byte pieces of f16) goes in row
     // r0 + RS i of a block: (r0 + RS i) % 8 is r0, and r0 + 4 in odd steps of 4
     const int at = (piece & 3) * 2;
-    const int put_lo = half * Lay::HALF + r0 * 128 + ((at ^ r0) << 4);
-    const int put_hi = half * Lay::HALF + r0 * 128 + (((at + 1) ^ r0) << 4);
+    const int put_lo = half * Lay::KV_HALF + r0 * 128 + ((at ^ r0) << 4);
+    const int put_hi = half * Lay::KV_HALF + r0 * 128 + (((at + 1) ^ r0) << 4);
     const int n_units = 2 * kBlocks * n_tiles;
     // -1: nothing there, or a bad id
     auto id_of = [&](int u) {
-      const int jb = (u >> 4) * kBlocks + (u & 7);
+      const int jb = (u >> 3) * kBlocks + (u & 3);
       int id = -1;
       if (u < n_units && jb < n_blocks_seq) id = __ldg(row + jb);
       return id;
@@ -300,10 +312,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto fetch = [&](uint4 (&x)[NV], float& ks, float& vs, int& id, int u) {
       if (id >= p.num_blocks || id < -1) id = -2;  // reported when it is stored
       const int blk = max(id, 0);
-      const uint8_t* src = ((u & 8) ? p.v_pool : p.k_pool) + int64_t(blk) * (kBlk * pitch) + lane_off;
+      const uint8_t* src = ((u & 4) ? p.v_pool : p.k_pool) + int64_t(blk) * (kBlk * pitch) + lane_off;
 #pragma unroll
       for (int i = 0; i < NV; ++i) x[i] = __ldg(reinterpret_cast<const uint4*>(src + i * step_off));
-      if (!(u & 8)) {
+      if (!(u & 4)) {
         ks = __ldg(p.k_scales + int64_t(blk) * p.n_kv + g);
         vs = __ldg(p.v_scales + int64_t(blk) * p.n_kv + g);
       }
@@ -322,8 +334,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < kAhead; ++k) {
         const int u = u0 + k * kLoadWarps;
         if (u >= n_units || !ok) break;
-        const int j = u >> 4, bi = u & 7;
-        const bool is_v = (u & 8) != 0;
+        const int j = u >> 3, bi = u & 3;
+        const bool is_v = (u & 4) != 0;
         const int st = j % kStages;
         const uint32_t use = j / kStages;
         if (use > 0 && !wait_all((is_v ? v_empty : k_empty) + st, (use - 1) & 1)) {
@@ -336,8 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int pos0 = (j * kBlocks + bi) * kBlk;
         if (!is_v && lane == 0) {
-          // The scales of tile j - 4 are no longer read: K stage j was free, so
-          // S_{j-2} is complete, so W_{j-3} was there, so softmax j - 4 is over.
+          // The scales of tile j - 8 are no longer read: K stage j was free, so
+          // S_{j-4} is complete, which was issued once W_{j-6} was there.
           const int o = (j % kScaleStages) * kBlocks + bi;
           if (id_d[k] == -2) report(p.err, PKV_DEVERR_BLOCK_ID);
           const bool good = id_d[k] >= 0;
@@ -398,51 +410,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ----------------------------------------------------------------- MMA
-    if (lane == 0) {
+    // One elected lane.  (elect.sync, not a test of the lane: the compiler then
+    // keeps descriptors in uniform registers, and an MMA takes some 30 cycles
+    // to issue instead of 45.)
+    if (elect_one()) {
       constexpr uint32_t idesc_qk = idesc_f16_f32(kRows, kTileKeys, false);
       constexpr uint32_t idesc_pv = idesc_f16_f32(kRows, HD, true);
+      // descriptors of the tiles' starts; a step within a tile adds its byte
+      // offset / 16 to the address field, which does not overflow
+      const uint64_t q_desc = tc::sw128_desc(smem_addr(q_tile(0)), 16, 1024);
+      const uint64_t k_desc = tc::sw128_desc(smem_addr(k_st(0)), 16, 1024);
+      const uint64_t v_desc = tc::sw128_desc(smem_addr(v_st(0)), Lay::KV_HALF, 1024);
       auto issue_qk = [&](int x, int j) {
-        const uint32_t q_addr = smem_addr(q_tile(x));
-        const uint32_t k_addr = smem_addr(k_st(j));
+        const uint64_t qd = q_desc + uint32_t(x * Lay::Q_TILE) / 16;
+        const uint64_t kd = k_desc + uint32_t((j % kStages) * Lay::KV_TILE) / 16;
 #pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * Lay::HALF + (kk & 3) * 32;
-          tc::mma_ss(s_tm(x), tc::sw128_desc(q_addr + off, 16, 1024),
-                     tc::sw128_desc(k_addr + off, 16, 1024), idesc_qk, kk > 0);
-        }
-        tc::commit(s_full + x);
+        for (int kk = 0; kk < HD / 16; ++kk)
+          tc::mma_ss(s_tm(x, j), qd + ((kk >> 2) * Lay::Q_HALF + (kk & 3) * 32) / 16,
+                     kd + ((kk >> 2) * Lay::KV_HALF + (kk & 3) * 32) / 16, idesc_qk, kk > 0);
+        tc::commit(s_full + x * 2 + (j & 1));
       };
       auto issue_pv = [&](int x, int j) {
-        const uint32_t v_addr = smem_addr(v_st(j));
+        const uint64_t vd = v_desc + uint32_t((j % kStages) * Lay::KV_TILE) / 16;
 #pragma unroll
-        for (int kk = 0; kk < kTileKeys / 16; ++kk) {
-          // W: the softmax halves' 32 columns at columns 0 and 64 of S
-          const uint32_t w_col = (kk >> 2) * 64 + (kk & 3) * 8;
-          tc::mma_ts(o_tm(x), s_tm(x) + w_col,
-                     tc::sw128_desc(v_addr + kk * 2048, Lay::HALF, 1024), idesc_pv,
-                     j > 0 || kk > 0);
-        }
+        for (int kk = 0; kk < kTileKeys / 16; ++kk)
+          // W: the softmax halves' 16 columns at columns 0 and 32 of S
+          tc::mma_ts(o_tm(x), s_tm(x, j) + (kk >> 1) * 32 + (kk & 1) * 8, vd + kk * 2048 / 16,
+                     idesc_pv, j > 0 || kk > 0);
+        tc::commit(o_done + x * 2 + (j & 1));
       };
-      bool ok = mbar_wait(k_full, 0);
-      for (int x = 0; x < 2 && ok; ++x) {
-        if (!(ok = mbar_wait(q_full + x, 0))) break;
-        tc::fence_after_sync();
-        issue_qk(x, 0);
-      }
-      if (ok) tc::commit(k_empty);  // K_0 is no longer read
-      for (int j = 0; j < n_tiles && ok; ++j) {
-        const bool more = j + 1 < n_tiles;
-        const int kn = (j + 1) % kStages;
+      bool ok = true;
+      for (int j = 0; j < 2 && j < n_tiles && ok; ++j) {
+        if (!(ok = mbar_wait(k_full + j, 0))) break;
         for (int x = 0; x < 2 && ok; ++x) {
-          if (!(ok = mbar_wait(p_ready + x, j & 1))) break;
+          if (j == 0 && !(ok = mbar_wait(q_full + x, 0))) break;
+          tc::fence_after_sync();
+          issue_qk(x, j);
+        }
+        tc::commit(k_empty + j);  // K_j is no longer read
+      }
+      for (int j = 0; j < n_tiles && ok; ++j) {
+        const bool more = j + 2 < n_tiles;
+        const int kn = (j + 2) % kStages;
+        for (int x = 0; x < 2 && ok; ++x) {
+          if (!(ok = mbar_wait(w_ready + x * 2 + (j & 1), (j >> 1) & 1))) break;
           if (x == 0 && !(ok = mbar_wait(v_full + (j % kStages), (j / kStages) & 1))) break;
-          if (x == 0 && more && !(ok = mbar_wait(k_full + kn, ((j + 1) / kStages) & 1))) break;
           tc::fence_after_sync();
           issue_pv(x, j);
           if (x == 1) tc::commit(v_empty + (j % kStages));  // V_j is no longer read
-          if (more) issue_qk(x, j + 1);
-          else tc::commit(o_done + x);
-          if (x == 1 && more) tc::commit(k_empty + kn);  // K_{j+1} is no longer read
+          if (!more) continue;
+          if (x == 0) {
+            if (!(ok = mbar_wait(k_full + kn, ((j + 2) / kStages) & 1))) break;
+            tc::fence_after_sync();
+          }
+          issue_qk(x, j + 2);
+          if (x == 1) tc::commit(k_empty + kn);  // K_{j+2} is no longer read
         }
       }
       if (!ok) {
@@ -514,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 4; ++k)
           o[k] = pack_f16x2(__uint_as_float(e[k] << 16) * f, __uint_as_float(e[k] & 0xffff0000u) * f);
         const int d16 = hf * (HD / 16) + i;  // 16-byte piece of the row
-        *reinterpret_cast<uint4*>(q_tile(x) + (d16 >> 3) * Lay::HALF + r * 128 +
+        *reinterpret_cast<uint4*>(q_tile(x) + (d16 >> 3) * Lay::Q_HALF + r * 128 +
                                   (((d16 & 7) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
       fence_proxy_async_smem();
@@ -525,47 +547,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int j = 0; j < n_tiles; ++j) {
       // (every thread passes the same barriers whatever happens to its waits)
-      if (ok && !(ok = wait_all(s_full + x, j & 1)) && lane == 0) {
+      if (ok && !(ok = wait_all(s_full + x * 2 + (j & 1), (j >> 1) & 1)) && lane == 0) {
         report(p.err, PKV_DEVERR_TIMEOUT);
         *abort_flag = 1;
       }
       tc::fence_after_sync();
-      const uint32_t s_addr = s_tm(x) + lane_base + hf * kHalfKeys;
-      const int pos0 = j * kTileKeys + hf * kHalfKeys;
-      // 32 scores; keys past this row's causal limit are -inf
-      auto load = [&](uint32_t (&v)[32], int ch) {
-        tc::tmem_ld32(s_addr + ch * 32, v);
-        tc::tmem_wait_ld();
-        if (pos0 + ch * 32 + 31 > last) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (pos0 + ch * 32 + k > last) v[k] = __float_as_uint(-INFINITY);
-        }
-      };
-      const float* ks = ks_s + (j % kScaleStages) * kBlocks + hf * 4;
+      const uint32_t s_addr = s_tm(x, j) + lane_base + hf * kHalfKeys;
+      uint32_t v[kHalfKeys];
+      tc::tmem_ld32(s_addr, v);
+      const float* ks = ks_s + (j % kScaleStages) * kBlocks + hf * 2;
+      const float2 ks2 = *reinterpret_cast<const float2*>(ks);
+      const float2 lv2 = *reinterpret_cast<const float2*>(ks + kScaleStages * kBlocks);
+      const float2 iv2 = *reinterpret_cast<const float2*>(ks + 2 * kScaleStages * kBlocks);
       // (factors are > 0; none is zero: -inf stays -inf)
-      auto factor = [&](int bk) { return fmaxf(rs * ks[bk], 1.2e-38f); };
-      auto shift = [&](int bk) { return ks[kScaleStages * kBlocks + bk]; };  // log2 vs
-      auto inv_vs = [&](int bk) { return ks[2 * kScaleStages * kBlocks + bk]; };
+      const float f[2] = {fmaxf(rs * ks2.x, 1.2e-38f), fmaxf(rs * ks2.y, 1.2e-38f)};
+      const float lv[2] = {lv2.x, lv2.y}, iv[2] = {iv2.x, iv2.y};
+      const int pos0 = j * kTileKeys + hf * kHalfKeys;
+      tc::tmem_wait_ld();
+      if (pos0 + kHalfKeys - 1 > last) {  // keys past this row's causal limit
+#pragma unroll
+        for (int k = 0; k < kHalfKeys; ++k)
+          if (pos0 + k > last) v[k] = __float_as_uint(-INFINITY);
+      }
       // maximum of x + log2 vs, block by block
-      auto top = [&](const uint32_t (&v)[32], int ch) {
-        float t = -INFINITY;
+      float mx = -INFINITY;
 #pragma unroll
-        for (int bb = 0; bb < 2; ++bb) {
-          float mb = __uint_as_float(v[bb * 16]);
+      for (int bk = 0; bk < 2; ++bk) {
+        float mb = __uint_as_float(v[bk * 16]);
 #pragma unroll
-          for (int k = 1; k < 16; ++k) mb = fmaxf(mb, __uint_as_float(v[bb * 16 + k]));
-          t = fmaxf(t, fmaf(mb, factor(ch * 2 + bb), shift(ch * 2 + bb)));
-        }
-        return t;
-      };
-      // Two chunks of 32 scores.  Both at once would not fit the registers; the
-      // second is read from TMEM twice (weights overwrite the first one's place).
-      uint32_t v[32];
-      load(v, 1);
-      float mx = top(v, 1);
-      load(v, 0);
-      mx = fmaxf(mx, top(v, 0));
+        for (int k = 1; k < 16; ++k) mb = fmaxf(mb, __uint_as_float(v[bk * 16 + k]));
+        mx = fmaxf(mx, fmaf(mb, f[bk], lv[bk]));
+      }
       mx = fmaxf(mx, exchange(mx, j + 1));
       const float m_new = fmaxf(m_used, mx);
       const bool grow = m_new > m_used + kRescaleLog2;
@@ -573,32 +585,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (grow) m_used = m_new;
       const float mref = (m_used == -INFINITY ? 0.f : m_used) - kWeightLog2;
       float add = 0.f;
+      uint32_t pk[16];
 #pragma unroll
-      for (int ch = 0; ch < 2; ++ch) {
-        if (ch == 1) load(v, 1);
-        uint32_t pk[16];
+      for (int bk = 0; bk < 2; ++bk) {
+        const float cst = lv[bk] - mref;
+        const float2 f2 = make_float2(f[bk], f[bk]), c2 = make_float2(cst, cst);
+        float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int bb = 0; bb < 2; ++bb) {
-          const int bk = ch * 2 + bb;
-          const float f = factor(bk), cst = shift(bk) - mref;
-          const float2 f2 = make_float2(f, f), c2 = make_float2(cst, cst);
-          float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int e = bb * 16 + 2 * k;
-            const float2 t2 =
-                __ffma2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), f2, c2);
-            const float2 pe = make_float2(fast_exp2(t2.x), fast_exp2(t2.y));
-            acc = __fadd2_rn(acc, pe);
-            pk[bb * 8 + k] = pack_f16x2(pe.x, pe.y);
-          }
-          add = fmaf(acc.x + acc.y, inv_vs(bk), add);
+        for (int k = 0; k < 8; ++k) {
+          const int e = bk * 16 + 2 * k;
+          const float2 t2 =
+              __ffma2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), f2, c2);
+          const float2 pe = make_float2(fast_exp2(t2.x), fast_exp2(t2.y));
+          acc = __fadd2_rn(acc, pe);
+          pk[bk * 8 + k] = pack_f16x2(pe.x, pe.y);
         }
-        tc::tmem_st16(s_addr + ch * 16, pk);
+        add = fmaf(acc.x + acc.y, iv[bk], add);
       }
+      tc::tmem_st16(s_addr, pk);
       l_sum = l_sum * alpha + add;
-      // (S_j complete implies the products W_{j-1} V_{j-1} before it are)
       if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        // O_X has to hold all products before this tile's.  (W_j is not there
+        // yet, so no later phase of the barrier can have completed.)
+        if (ok && !(ok = wait_all(o_done + x * 2 + ((j - 1) & 1), ((j - 1) >> 1) & 1)) && lane == 0) {
+          report(p.err, PKV_DEVERR_TIMEOUT);
+          *abort_flag = 1;
+        }
+        tc::fence_after_sync();
         const float2 a2 = make_float2(alpha, alpha);
 #pragma unroll 1
         for (int ch = 0; ch < HD / 64; ++ch) {
@@ -619,10 +632,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_ready + x);
+      if (lane == 0) mbar_arrive(w_ready + x * 2 + (j & 1));
     }
     l_sum += exchange(l_sum, n_tiles + 1);
-    if (ok && !(ok = wait_all(o_done + x, 0)) && lane == 0) {
+    if (ok && !(ok = wait_all(o_done + x * 2 + ((n_tiles - 1) & 1), ((n_tiles - 1) >> 1) & 1)) && lane == 0) {
       report(p.err, PKV_DEVERR_TIMEOUT);
       *abort_flag = 1;
     }

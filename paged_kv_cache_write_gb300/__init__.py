@@ -462,49 +462,76 @@ def paged_attention_decode_noalloc(q, k_pool, v_pool, block_tables, seq_lens, sc
 
 
 # ------------------------------------------------------------ 8-bit cache
+#
+# A decode step's kernels take 3-5 us, so what a call costs on the host counts:
+# each tensor is checked in one pass (device, type, layout), and the current
+# stream is asked for as a bare handle.
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+_f8 = torch.float8_e4m3fn
+_f32 = torch.float32
+_int = torch.int32
 
 
-def _call_on(device, name, stream, *args):
-    """Call entry point ``name`` with ``device`` current; its stream comes last."""
+def _ptr(t, name, dtype, index):
+    """Address of a contiguous tensor of ``dtype`` on CUDA device ``index``."""
+    try:
+        if t.get_device() == index and t.dtype is dtype and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if isinstance(t, torch.Tensor) and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{index}")
+    return _dev(t, name, dtype)  # raises: it is not the type or layout asked for
+
+
+def _call_on(index, name, stream, *args):
+    """Call entry point ``name`` with device ``index`` current; its stream comes last."""
     fn = getattr(_lib or _load(), name)
-    if device.index == torch.cuda.current_device():
-        _check(name, fn(*args, _stream(stream)))
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
     else:
-        with torch.cuda.device(device):
-            _check(name, fn(*args, _stream(stream)))
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
+    if status:
+        _check(name, status)
 
 
 def _fp8_pool(k_pool, v_pool, k_scales, v_scales):
-    """Descriptor and pointers of an 8-bit cache, its four tensors checked."""
-    if k_pool.dim() != 4:
+    """Device, descriptor and addresses of an 8-bit cache, its four tensors checked."""
+    shape = k_pool.shape
+    if len(shape) != 4:
         raise ValueError("pool must be [num_blocks, block_size, n_kv, head_dim]")
-    if v_pool.shape != k_pool.shape:
+    if v_pool.shape != shape:
         raise ValueError("k_pool and v_pool must have the same shape")
-    nb, bs, nkv, hd = k_pool.shape
-    if tuple(k_scales.shape) != (nb, nkv) or tuple(v_scales.shape) != (nb, nkv):
-        raise ValueError(f"k_scales and v_scales must be {(nb, nkv)}: one per block and KV head")
-    f8, f32 = torch.float8_e4m3fn, torch.float32
+    nb, bs, nkv, hd = shape
+    per = (nb, nkv)
+    if k_scales.shape != per or v_scales.shape != per:
+        raise ValueError(f"k_scales and v_scales must be {per}: one per block and KV head")
+    index = k_pool.get_device()
+    if index < 0:
+        raise ValueError("k_pool must be a CUDA tensor (the library has no CPU path)")
     desc = PoolDesc(nb, bs, nkv, hd, PKV_FP8_E4M3)
-    return desc, (_dev(k_pool, "k_pool", f8), _dev(v_pool, "v_pool", f8),
-                  _dev(k_scales, "k_scales", f32), _dev(v_scales, "v_scales", f32))
+    return index, desc, (_ptr(k_pool, "k_pool", _f8, index), _ptr(v_pool, "v_pool", _f8, index),
+                         _ptr(k_scales, "k_scales", _f32, index),
+                         _ptr(v_scales, "v_scales", _f32, index))
 
 
-def _batch(block_tables, seq_lens, cu=None, cu_name=""):
-    """(num_seqs, table width) of a batch's tables, lengths and offsets."""
-    if block_tables.dim() != 2:
+def _batch(block_tables, seq_lens):
+    """(num_seqs, table width) of a batch's tables and lengths."""
+    shape = block_tables.shape
+    if len(shape) != 2:
         raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
-    B, W = block_tables.shape
-    if tuple(seq_lens.shape) != (B,):
-        raise ValueError(f"seq_lens must be {(B,)}: one per row of block_tables")
-    if cu is not None and tuple(cu.shape) != (B + 1,):
-        raise ValueError(f"{cu_name} must be {(B + 1,)}")
-    return B, W
+    if seq_lens.shape != shape[:1]:
+        raise ValueError(f"seq_lens must be {tuple(shape[:1])}: one per row of block_tables")
+    return shape
 
 
-def _one_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+def _offsets(cu, name, B, index):
+    if cu.shape != (B + 1,):
+        raise ValueError(f"{name} must be {(B + 1,)}")
+    return _ptr(cu, name, _int, index)
 
 
 def kv_write_fp8(k, v, block_tables, seq_lens, cu_new_lens, k_pool, v_pool, k_scales, v_scales, *,
@@ -518,17 +545,17 @@ def kv_write_fp8(k, v, block_tables, seq_lens, cu_new_lens, k_pool, v_pool, k_sc
     keeps at least its scale; where a new token needs a larger one the earlier
     rows are moved to it.
     """
-    desc, pools = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
-    B, W = _batch(block_tables, seq_lens, cu_new_lens, "cu_new_lens")
-    if k.dim() != 3 or k.shape[1:] != k_pool.shape[2:] or v.shape != k.shape:
+    i, desc, pools = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
+    B, W = _batch(block_tables, seq_lens)
+    shape = k.shape
+    if len(shape) != 3 or shape != (shape[0], desc.n_kv, desc.head_dim) or v.shape != shape:
         raise ValueError("k, v must be [T, n_kv, head_dim] matching the pool")
-    _one_device(k_pool.device, v_pool=v_pool, k_scales=k_scales, v_scales=v_scales, k=k, v=v,
-                block_tables=block_tables, seq_lens=seq_lens, cu_new_lens=cu_new_lens, err=err)
-    i32 = torch.int32
-    _call_on(k_pool.device, "pkv_kv_write_fp8", stream, _dev(k, "k"), _dev(v, "v", k.dtype),
-             _dtype_code(k.dtype), _dev(block_tables, "block_tables", i32), W,
-             _dev(seq_lens, "seq_lens", i32), _dev(cu_new_lens, "cu_new_lens", i32), B, k.shape[0],
-             *pools, ctypes.byref(desc), _opt(err, "err", i32))
+    dt = k.dtype
+    _call_on(i, "pkv_kv_write_fp8", stream, _ptr(k, "k", dt, i), _ptr(v, "v", dt, i),
+             _dtype_code(dt), _ptr(block_tables, "block_tables", _int, i), W,
+             _ptr(seq_lens, "seq_lens", _int, i), _offsets(cu_new_lens, "cu_new_lens", B, i), B,
+             shape[0], *pools, ctypes.byref(desc),
+             None if err is None else _ptr(err, "err", _int, i))
 
 
 def kv_gather_fp8(k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, cu_seq_lens,
@@ -537,25 +564,22 @@ def kv_gather_fp8(k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, cu
     """Contiguous [total_tokens, n_kv, head_dim] K and V of an 8-bit cache in
     logical order, each value times its scale, in ``dtype`` (float32 or
     bfloat16; that of ``k_out`` / ``v_out`` where given)."""
-    desc, pools = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
-    B, W = _batch(block_tables, seq_lens, cu_seq_lens, "cu_seq_lens")
-    dtype = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else dtype
-    code = _dtype_code(dtype)
+    i, desc, pools = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
+    B, W = _batch(block_tables, seq_lens)
+    dt = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else dtype
+    code = _dtype_code(dt)
     shape = (int(total_tokens), desc.n_kv, desc.head_dim)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=k_pool.device)
+        k_out = torch.empty(shape, dtype=dt, device=k_pool.device)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=k_pool.device)
-    if tuple(k_out.shape) != shape or tuple(v_out.shape) != shape:
+        v_out = torch.empty(shape, dtype=dt, device=k_pool.device)
+    if k_out.shape != shape or v_out.shape != shape:
         raise ValueError(f"k_out, v_out must be {shape}")
-    _one_device(k_pool.device, v_pool=v_pool, k_scales=k_scales, v_scales=v_scales, k_out=k_out,
-                v_out=v_out, block_tables=block_tables, seq_lens=seq_lens,
-                cu_seq_lens=cu_seq_lens, err=err)
-    i32 = torch.int32
-    _call_on(k_pool.device, "pkv_kv_gather_fp8", stream, *pools, ctypes.byref(desc),
-             _dev(block_tables, "block_tables", i32), W, _dev(seq_lens, "seq_lens", i32),
-             _dev(cu_seq_lens, "cu_seq_lens", i32), B, int(total_tokens), code,
-             _dev(k_out, "k_out", dtype), _dev(v_out, "v_out", dtype), _opt(err, "err", i32))
+    _call_on(i, "pkv_kv_gather_fp8", stream, *pools, ctypes.byref(desc),
+             _ptr(block_tables, "block_tables", _int, i), W, _ptr(seq_lens, "seq_lens", _int, i),
+             _offsets(cu_seq_lens, "cu_seq_lens", B, i), B, shape[0], code,
+             _ptr(k_out, "k_out", dt, i), _ptr(v_out, "v_out", dt, i),
+             None if err is None else _ptr(err, "err", _int, i))
     return k_out, v_out
 
 
@@ -564,14 +588,16 @@ def decode_fp8_workspace_bytes(num_seqs, n_heads, head_dim, max_seq_len, max_cta
                                                       max_ctas, block_size))
 
 
-def _fp8_query(q, k_pool, out):
-    if q.dim() != 3 or q.shape[2] != k_pool.shape[3]:
+def _fp8_query(q, head_dim, out):
+    """(out, rows, heads) of an attention call."""
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != head_dim:
         raise ValueError("q must be [rows, n_heads, head_dim] with the pool's head_dim")
     if out is None:
-        return torch.empty_like(q)
-    if out.shape != q.shape:
-        raise ValueError(f"out must be {tuple(q.shape)}")
-    return out
+        out = torch.empty_like(q)
+    elif out.shape != shape:
+        raise ValueError(f"out must be {tuple(shape)}")
+    return out, shape[0], shape[1]
 
 
 def paged_attention_decode_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
@@ -584,26 +610,22 @@ def paged_attention_decode_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tabl
     :func:`paged_attention_decode`, with ``decode_fp8_workspace_bytes(...)``
     bytes; calls that may run at the same time need a workspace each.
     """
-    desc, pools = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
+    i, desc, pools = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
     B, W = _batch(block_tables, seq_lens)
-    out = _fp8_query(q, k_pool, out)
-    if q.shape[0] != B:
+    out, rows, H = _fp8_query(q, desc.head_dim, out)
+    if rows != B:
         raise ValueError("q must have one row per sequence")
-    H, hd = q.shape[1:]
     if max_seq_len is None:
         max_seq_len = int(seq_lens.max().item()) if B else 0
     if workspace is None:
-        need = decode_fp8_workspace_bytes(B, H, hd, max_seq_len, max_ctas, desc.block_size)
+        need = decode_fp8_workspace_bytes(B, H, desc.head_dim, max_seq_len, max_ctas)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _one_device(k_pool.device, v_pool=v_pool, k_scales=k_scales, v_scales=v_scales, q=q, out=out,
-                workspace=workspace, block_tables=block_tables, seq_lens=seq_lens, err=err)
-    i32 = torch.int32
-    _call_on(k_pool.device, "pkv_paged_attention_decode_fp8", stream, _dev(q, "q"),
-             _dtype_code(q.dtype), B, H, *pools, ctypes.byref(desc),
-             _dev(block_tables, "block_tables", i32), W, _dev(seq_lens, "seq_lens", i32),
-             int(max_seq_len), float(scale), int(max_ctas), _dev(out, "out", q.dtype),
-             _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-             _opt(err, "err", i32))
+    dt = q.dtype
+    _call_on(i, "pkv_paged_attention_decode_fp8", stream, _ptr(q, "q", dt, i), _dtype_code(dt), B,
+             H, *pools, ctypes.byref(desc), _ptr(block_tables, "block_tables", _int, i), W,
+             _ptr(seq_lens, "seq_lens", _int, i), int(max_seq_len), float(scale), int(max_ctas),
+             _ptr(out, "out", dt, i), _ptr(workspace, "workspace", workspace.dtype, i),
+             workspace.nbytes, None if err is None else _ptr(err, "err", _int, i))
     return out
 
 
@@ -613,19 +635,17 @@ def paged_attention_prefill_fp8(q, cu_q_lens, k_pool, v_pool, k_scales, v_scales
                                 stream=None):
     """Causal chunked-prefill attention [total_q, n_heads, head_dim] (float32
     or bfloat16) over the paged history of an 8-bit cache."""
-    desc, pools = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
-    B, W = _batch(block_tables, seq_lens, cu_q_lens, "cu_q_lens")
-    out = _fp8_query(q, k_pool, out)
+    i, desc, pools = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
+    B, W = _batch(block_tables, seq_lens)
+    out, rows, H = _fp8_query(q, desc.head_dim, out)
     if max_q_len is None:
         max_q_len = int((cu_q_lens[1:] - cu_q_lens[:-1]).max().item()) if B else 0
     if max_seq_len is None:
         max_seq_len = int(seq_lens.max().item()) if B else 0
-    _one_device(k_pool.device, v_pool=v_pool, k_scales=k_scales, v_scales=v_scales, q=q, out=out,
-                cu_q_lens=cu_q_lens, block_tables=block_tables, seq_lens=seq_lens, err=err)
-    i32 = torch.int32
-    _call_on(k_pool.device, "pkv_paged_attention_prefill_fp8", stream, _dev(q, "q"),
-             _dtype_code(q.dtype), _dev(cu_q_lens, "cu_q_lens", i32), B, q.shape[0],
-             int(max_q_len), q.shape[1], *pools, ctypes.byref(desc),
-             _dev(block_tables, "block_tables", i32), W, _dev(seq_lens, "seq_lens", i32),
-             int(max_seq_len), float(scale), _dev(out, "out", q.dtype), _opt(err, "err", i32))
+    dt = q.dtype
+    _call_on(i, "pkv_paged_attention_prefill_fp8", stream, _ptr(q, "q", dt, i), _dtype_code(dt),
+             _offsets(cu_q_lens, "cu_q_lens", B, i), B, rows, int(max_q_len), H, *pools,
+             ctypes.byref(desc), _ptr(block_tables, "block_tables", _int, i), W,
+             _ptr(seq_lens, "seq_lens", _int, i), int(max_seq_len), float(scale),
+             _ptr(out, "out", dt, i), None if err is None else _ptr(err, "err", _int, i))
     return out

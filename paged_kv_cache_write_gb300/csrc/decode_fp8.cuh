@@ -58,27 +58,115 @@ __device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* m
       : "memory");
 }
 
-// One lane: wait for stage `it` to be free, then fetch a block's K and V for
-// heads head0 .. (a slot past the pool's end reads zeros).  `policy`
-// (nonzero): an L2 cache policy for the copied lines.
-__device__ __forceinline__ bool fetch(const Ring& r, uint32_t it, const CUtensorMap* tm_k,
-                                      const CUtensorMap* tm_v, int slot, int head0, int32_t* err,
-                                      uint64_t policy) {
-  const int st = static_cast<int>(it % r.nstages);
-  const uint32_t use = it / r.nstages;
-  if (use > 0 && !mbar_wait(r.empty + st, (use - 1) & 1)) {
-    report(err, PKV_DEVERR_TIMEOUT);
-    return false;
+// A place in the ring: its stage and how often the ring has been gone round
+// (kept as counters: a division per block would cost as much as its copies).
+struct RingPos {
+  int st = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ void next(const Ring& r) {
+    if (++st == r.nstages) {
+      st = 0;
+      ++round;
+    }
   }
-  mbar_arrive_expect_tx(r.full + st, static_cast<uint32_t>(r.stage_bytes));
-  if (policy != 0) {
-    tma_load_3d_hint(r.k_tile(st), tm_k, 0, slot, head0, r.full + st, policy);
-    tma_load_3d_hint(r.v_tile(st), tm_v, 0, slot, head0, r.full + st, policy);
-  } else {
-    tc::tma_load_3d(r.k_tile(st), tm_k, 0, slot, head0, r.full + st);
-    tc::tma_load_3d(r.v_tile(st), tm_v, 0, slot, head0, r.full + st);
+};
+
+// Producer, one lane (elect_one): fetches blocks into the ring one after the
+// other.  A block takes it about 200 cycles, and a stage of 8 heads x 64 dims
+// should leave HBM every 700.
+struct Producer {
+  const Ring& ring;
+  const CUtensorMap* tm_k;
+  const CUtensorMap* tm_v;
+  int num_blocks;
+  int32_t* err;
+  uint64_t policy;  // nonzero: an L2 cache policy for the copied lines
+  RingPos pos;
+  uint32_t issued = 0;
+
+  // Block `id` (a bad one reads the zeros past the pool's end), from run
+  // run0 of the tile map on (a run: `width` bytes of a row).  False on timeout.
+  __device__ __forceinline__ bool fetch(int id, int run0) {
+    const bool good = id >= 0 && id < num_blocks;
+    if (!good) report(err, PKV_DEVERR_BLOCK_ID);
+    if (pos.round > 0 && !mbar_wait(ring.empty + pos.st, (pos.round - 1) & 1)) {
+      report(err, PKV_DEVERR_TIMEOUT);
+      return false;
+    }
+    const int slot = (good ? id : num_blocks) * kBS;
+    uint64_t* full = ring.full + pos.st;
+    mbar_arrive_expect_tx(full, static_cast<uint32_t>(ring.stage_bytes));
+    if (policy != 0) {
+      tma_load_3d_hint(ring.k_tile(pos.st), tm_k, 0, slot, run0, full, policy);
+      tma_load_3d_hint(ring.v_tile(pos.st), tm_v, 0, slot, run0, full, policy);
+    } else {
+      tc::tma_load_3d(ring.k_tile(pos.st), tm_k, 0, slot, run0, full);
+      tc::tma_load_3d(ring.v_tile(pos.st), tm_v, 0, slot, run0, full);
+    }
+    pos.next(ring);
+    ++issued;
+    return true;
   }
-  return true;
+
+  // Blocks row[0 .. n), ids read a group ahead.  False: gave up (and told the
+  // consumers).
+  __device__ __forceinline__ bool fetch_row(const int32_t* row, int n, int run0) {
+    constexpr int kGroup = 8;
+    int id[kGroup], next[kGroup];
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) next[i] = i < n ? __ldg(row + i) : 0;
+    for (int k0 = 0; k0 < n; k0 += kGroup) {
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) id[i] = next[i];
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i)
+        next[i] = k0 + kGroup + i < n ? __ldg(row + k0 + kGroup + i) : 0;
+      if (*ring.abort_flag) return false;
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        if (k0 + i >= n) break;
+        if (!fetch(id[i], run0)) {
+          *ring.abort_flag = 1;
+          return false;
+        }
+      }
+    }
+    return true;
+  }
+
+  // After giving up: wait (bounded) for the copies still in flight, so that
+  // none lands after the CTA has left.
+  __device__ __forceinline__ void drain() const { attn::ring_drain(ring, issued); }
+};
+
+// Consumer warp: wait for its next tile; false if the producer gave up or the
+// wait timed out.
+__device__ __forceinline__ bool wait_tile(const Ring& r, const RingPos& pos, int32_t* err) {
+  uint64_t* full = r.full + pos.st;
+  const uint32_t parity = pos.round & 1;
+  if (mbar_try_wait(full, parity)) return true;
+  for (uint32_t i = 0; i < kMaxPolls; ++i) {
+    if (*r.abort_flag) return false;
+    if (mbar_try_wait(full, parity)) return true;
+  }
+  if ((threadIdx.x & 31) == 0) report(err, PKV_DEVERR_TIMEOUT);
+  return false;
+}
+
+__device__ __forceinline__ void release_tile(const Ring& r, const RingPos& pos) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(r.empty + pos.st);
+}
+
+// Tile map of an 8-bit pool: (width bytes, slot, run), read in boxes of one
+// block's 16 slots x the runs of `heads` heads.
+inline bool encode_tiles(CUtensorMap* map, const void* base, const PoolShape& pool, int width,
+                         int heads) {
+  const int row = pool.n_kv * pool.head_dim;
+  const uint64_t dims[3] = {uint64_t(width), uint64_t(pool.num_blocks) * kBS, uint64_t(row / width)};
+  const uint64_t strides[2] = {uint64_t(row), uint64_t(width)};
+  const uint32_t box[3] = {uint32_t(width), kBS, uint32_t(heads * pool.head_dim / width)};
+  return encode_u8(map, base, dims, strides, box, TileView::swizzle(width));
 }
 
 // A consumer warp's block scales, one block per lane.
@@ -94,10 +182,39 @@ struct ScaleBatch {
   __device__ __forceinline__ void settle() { lv = __log2f(vs); }
 };
 
+// Consumer warp: its next NB tiles of the ring, blocks k .. k + NB - 1 of the
+// batch in `sc`.  False: gave up (and told the others).
+template <int NB, typename RowsT>
+__device__ __forceinline__ bool take_tiles(RowsT& rows, const Ring& ring, RingPos& pos,
+                                           const ScaleBatch& sc, int k, int j0, int valid,
+                                           bool use, int32_t* err) {
+  float ks[NB], vs[NB], lv[NB];
+  const uint8_t *kt[NB], *vt[NB];
+  RingPos at[NB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    ks[i] = __shfl_sync(0xffffffffu, sc.ks, (k + i) & 31);
+    vs[i] = __shfl_sync(0xffffffffu, sc.vs, (k + i) & 31);
+    lv[i] = __shfl_sync(0xffffffffu, sc.lv, (k + i) & 31);
+    at[i] = pos;
+    kt[i] = ring.k_tile(pos.st);
+    vt[i] = ring.v_tile(pos.st);
+    if (!wait_tile(ring, pos, err)) {
+      *ring.abort_flag = 1;
+      return false;
+    }
+    pos.next(ring);
+  }
+  if (use) rows.template blocks<NB>(kt, vt, j0, valid, ks, vs, lv);
+#pragma unroll
+  for (int i = 0; i < NB; ++i) release_tile(ring, at[i]);
+  return true;
+}
+
 template <typename T, int HD, int NT>
 __global__ void __launch_bounds__(kMaxThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  const DecodeParams p, const Scales sc) {
+                  const DecodeParams p, const Scales sc, const int width) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int consumers = p.hg_size;
   Ring ring = attn::make_tile_ring(smem, p.nstages, kBS * p.hg_size * HD);
@@ -159,46 +276,28 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 
   if (warp == consumers) {
     // -------------------------------------------------------- producer
-    const uint64_t pol = tc::l2_evict_first_policy();  // each block is read once
-    uint32_t it = 0;
-    bool ok = true;
-    for (int u = r0; u < r1 && ok;) {
-      const int n = min(r1 - u, cur.nblk - cur.j);
-      const int32_t* row = p.bt + int64_t(cur.b) * p.W + cur.j;
-      for (int jj = 0; jj < n && ok; jj += 32) {
-        const int id = jj + lane < n ? __ldg(row + jj + lane) : 0;
-        const int n_here = min(32, n - jj);
-        for (int k = 0; k < n_here; ++k) {
-          if (*ring.abort_flag) { ok = false; break; }
-          const int blk = __shfl_sync(0xffffffffu, id, k);
-          const bool good = blk >= 0 && blk < p.num_blocks;
-          if (!good && lane == 0) report(p.err, PKV_DEVERR_BLOCK_ID);
-          bool filled = true;
-          if (lane == 0)
-            filled = fetch(ring, it, &tm_k, &tm_v, (good ? blk : p.num_blocks) * kBS,
-                           cur.grp * p.hg_size, p.err, pol);
-          if (!__shfl_sync(0xffffffffu, filled, 0)) {
-            *ring.abort_flag = 1;
-            ok = false;
-            break;
-          }
-          ++it;
-        }
+    if (elect_one()) {
+      // (each block is read once: its lines leave L2 first)
+      Producer pr{ring, &tm_k, &tm_v, p.num_blocks, p.err, tc::l2_evict_first_policy()};
+      bool ok = true;
+      for (int u = r0; u < r1 && ok;) {
+        const int n = min(r1 - u, cur.nblk - cur.j);
+        ok = pr.fetch_row(p.bt + int64_t(cur.b) * p.W + cur.j, n, cur.grp * p.hg_size * HD / width);
+        u += n;
+        cur.advance(p, n);
       }
-      u += n;
-      cur.advance(p, n);
-    }
-    if (!ok) attn::ring_drain(ring, it);
-    // the split group this CTA merges (read by the merge kernel)
-    if (lane == 0)
+      if (!ok) pr.drain();
+      // the split group this CTA merges (read by the merge kernel)
       p.splits[blockIdx.x] =
           r0 < r1 ? attn::split_entry(blockIdx.x, G, U, st.x, st.y, st.z,
                                       attn::walked_blocks(p, attn::used_len(p, st.x)))
                   : make_int4(-1, 0, 0, 0);
+    }
   } else if (warp < consumers) {
     // ------------------------------------------------------- consumers
     Rows<T, HD, NT, false> rows;
-    uint32_t it = 0;
+    rows.place(width, warp);
+    RingPos pos;
     bool ok = true;
     const T* q = static_cast<const T*>(p.q);
     T* out = static_cast<T*>(p.out);
@@ -219,27 +318,22 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
             return r < p.rep ? q + (int64_t(b) * p.n_heads + head0 + r) * HD : nullptr;
           },
           [&](int) { return last; }, p.scale_log2);
-      for (int k = 0; k < n; ++k) {
+      constexpr int PAIR = Rows<T, HD, NT, false>::PAIR;
+      for (int k = 0; k < n && ok;) {
         if ((k & 31) == 0) {
           now = next;
           now.settle();
           next.load(sc, p, ids, kv_head);
           ids = id_at(k + 64 + lane);
         }
-        const float ks = __shfl_sync(0xffffffffu, now.ks, k & 31);
-        const float vs = __shfl_sync(0xffffffffu, now.vs, k & 31);
-        const float lv = __shfl_sync(0xffffffffu, now.lv, k & 31);
-        if (!attn::ring_wait_full(ring, it, p.err)) {
-          *ring.abort_flag = 1;
-          ok = false;
-          break;
-        }
-        const int stg = static_cast<int>(it % ring.nstages);
         const int j0 = (cur.j + k) * kBS;
-        rows.block(ring.k_tile(stg) + warp * kBS * HD, ring.v_tile(stg) + warp * kBS * HD, j0,
-                   cur.L - j0, ks, vs, lv);
-        attn::ring_release(ring, it);
-        ++it;
+        if (PAIR == 2 && k + 1 < n) {
+          ok = take_tiles<PAIR>(rows, ring, pos, now, k, j0, cur.L - j0, true, p.err);
+          k += PAIR;
+        } else {
+          ok = take_tiles<1>(rows, ring, pos, now, k, j0, cur.L - j0, true, p.err);
+          ++k;
+        }
       }
       if (!ok) break;
       if (cur.j == 0 && n == cur.nblk) {
@@ -267,7 +361,7 @@ template <typename T, int HD, int NT>
 __global__ void __launch_bounds__(kMaxThreads, 1)
     decode_cluster_kernel(const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const DecodeParams p,
-                          const Scales sc) {
+                          const Scales sc, const int width) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int consumers = p.hg_size;
   Ring ring = attn::make_tile_ring(smem, p.nstages, kBS * p.hg_size * HD);
@@ -284,12 +378,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 
   attn::pdl_wait();
   attn::pdl_launch_dependents();
-  // this path's sequences have at most 64 blocks: entries lane and 32 + lane
-  // of the table row are read along with the length
   const int32_t* trow = p.bt + int64_t(b) * p.W;
-  int ids[2] = {-1, -1};
-  if (lane < p.W) ids[0] = __ldg(trow + lane);
-  if (lane + 32 < p.W) ids[1] = __ldg(trow + lane + 32);
   const int L = attn::used_len(p, b);
   const int nblk = (L + kBS - 1) / kBS;
   const int j0 = rank * nblk / C, j1 = (rank + 1) * nblk / C;
@@ -298,55 +387,36 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
   if (rank == 0 && grp == 0 && threadIdx.x == 0) attn::check_length(p, b);
 
   if (warp == consumers) {
-    const uint64_t pol = tc::l2_evict_first_policy();
-    uint32_t it = 0;
-    bool ok = true;
-    for (int j = j0; j < j1 && ok; ++j) {
-      if (*ring.abort_flag) { ok = false; break; }
-      const int blk = __shfl_sync(0xffffffffu, j < 32 ? ids[0] : ids[1], j & 31);
-      const bool good = blk >= 0 && blk < p.num_blocks;
-      if (!good && lane == 0) report(p.err, PKV_DEVERR_BLOCK_ID);
-      bool filled = true;
-      if (lane == 0)
-        filled = fetch(ring, it, &tm_k, &tm_v, (good ? blk : p.num_blocks) * kBS,
-                       grp * p.hg_size, p.err, pol);
-      if (!__shfl_sync(0xffffffffu, filled, 0)) {
-        *ring.abort_flag = 1;
-        ok = false;
-        break;
-      }
-      ++it;
+    if (elect_one()) {
+      Producer pr{ring, &tm_k, &tm_v, p.num_blocks, p.err, tc::l2_evict_first_policy()};
+      if (!pr.fetch_row(trow + j0, j1 - j0, grp * p.hg_size * HD / width)) pr.drain();
     }
-    if (!ok) attn::ring_drain(ring, it);
   } else if (warp < consumers) {
     const T* q = static_cast<const T*>(p.q);
     const int kv_head = grp * p.hg_size + warp;
     const int head0 = kv_head * p.rep;
     // scales of blocks j0 + lane (j1 - j0 <= 8)
-    const int lo = __shfl_sync(0xffffffffu, ids[0], (j0 + lane) & 31);
-    const int hi = __shfl_sync(0xffffffffu, ids[1], (j0 + lane) & 31);
     ScaleBatch now;
-    now.load(sc, p, j0 + lane < j1 ? (j0 + lane < 32 ? lo : hi) : -1, kv_head);
+    now.load(sc, p, j0 + lane < j1 ? __ldg(trow + j0 + lane) : -1, kv_head);
     Rows<T, HD, NT, false> rows;
+    rows.place(width, warp);
     rows.begin(
         [&](int r) -> const T* {
           return r < p.rep ? q + (int64_t(b) * p.n_heads + head0 + r) * HD : nullptr;
         },
         [&](int) { return L - 1; }, p.scale_log2);
     now.settle();
-    for (int j = j0; j < j1; ++j) {
-      const uint32_t it = j - j0;
-      const float ks = __shfl_sync(0xffffffffu, now.ks, it);
-      const float vs = __shfl_sync(0xffffffffu, now.vs, it);
-      const float lv = __shfl_sync(0xffffffffu, now.lv, it);
-      if (!attn::ring_wait_full(ring, it, p.err)) {
-        *ring.abort_flag = 1;
-        break;
+    RingPos pos;
+    constexpr int PAIR = Rows<T, HD, NT, false>::PAIR;
+    for (int j = j0; j < j1;) {
+      const int jp = j * kBS;
+      if (PAIR == 2 && j + 1 < j1) {
+        if (!take_tiles<PAIR>(rows, ring, pos, now, j - j0, jp, L - jp, true, p.err)) break;
+        j += PAIR;
+      } else {
+        if (!take_tiles<1>(rows, ring, pos, now, j - j0, jp, L - jp, true, p.err)) break;
+        ++j;
       }
-      const int stg = static_cast<int>(it % ring.nstages);
-      rows.block(ring.k_tile(stg) + warp * kBS * HD, ring.v_tile(stg) + warp * kBS * HD, j * kBS,
-                 L - j * kBS, ks, vs, lv);
-      attn::ring_release(ring, it);
     }
     // this CTA's part (also after an abort, so the barrier below is reached)
     rows.store_partial(
@@ -462,15 +532,10 @@ struct DecodeFp8 {
     p.total_units = reinterpret_cast<int32_t*>(ws + L.total_units);
     p.ws_ml = reinterpret_cast<float*>(ws + L.ml);
     p.ws_o = reinterpret_cast<float*>(ws + L.o);
-    // the pools as (head_dim bytes, slot, KV head), read in boxes of one
-    // block's 16 slots x the group's heads
     CUtensorMap tm_k{}, tm_v{};
-    const uint64_t slots = uint64_t(pool.num_blocks) * kBS;
-    const uint64_t dims[3] = {HD, slots, uint64_t(pool.n_kv)};
-    const uint64_t strides[2] = {uint64_t(pool.n_kv) * HD, HD};
-    const uint32_t box[3] = {HD, kBS, static_cast<uint32_t>(hg)};
-    if (!encode_u8(&tm_k, a.k_pool, dims, strides, box, Tile<HD>::kSwizzle) ||
-        !encode_u8(&tm_v, a.v_pool, dims, strides, box, Tile<HD>::kSwizzle))
+    const int width = tile_width(hg, HD);
+    if (!encode_tiles(&tm_k, a.k_pool, pool, width, hg) ||
+        !encode_tiles(&tm_v, a.v_pool, pool, width, hg))
       return cudaErrorInvalidValue;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -504,7 +569,7 @@ struct DecodeFp8 {
       cfg.numAttrs = 2;
       cfg.gridDim = dim3(static_cast<unsigned>(ctas));
       cfg.dynamicSmemBytes = p.part_off + extra;
-      e = cudaLaunchKernelEx(&cfg, decode_cluster_kernel<T, HD, NT>, tm_k, tm_v, p, sc);
+      e = cudaLaunchKernelEx(&cfg, decode_cluster_kernel<T, HD, NT>, tm_k, tm_v, p, sc, width);
       return e != cudaSuccess ? e : cudaGetLastError();
     }
     // every CTA scans the lengths in its ring stages; larger batches have a
@@ -517,7 +582,7 @@ struct DecodeFp8 {
     }
     cfg.gridDim = dim3(G);
     cfg.dynamicSmemBytes = smem;
-    e = cudaLaunchKernelEx(&cfg, decode_kernel<T, HD, NT>, tm_k, tm_v, p, sc);
+    e = cudaLaunchKernelEx(&cfg, decode_kernel<T, HD, NT>, tm_k, tm_v, p, sc, width);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(G);
     e = attn::launch_merge<T, HD>(cfg, p);

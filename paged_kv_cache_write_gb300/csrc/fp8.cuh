@@ -60,4 +60,13 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t b) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// True in one lane of a converged warp.  Unlike a test of the lane id this
+// lets the compiler keep what the lane issues asynchronous operations with
+// (descriptors, shared-memory addresses) in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 }  // namespace pkv

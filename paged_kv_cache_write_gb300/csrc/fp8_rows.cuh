@@ -25,7 +25,8 @@
 //   O^T [16 dims x 8 rows] += V^T P^T.  Lane (g, c) holds HD / 8 consecutive
 //     dims of tokens 2c, 2c + 1, 2c + 8, 2c + 9; byte permutes pair the tokens.
 // The token order within a block is free too (kTok): it is chosen so that
-// both loads touch each bank once in the tile's swizzled layout.
+// both loads touch each bank once in the tile's swizzled layout (heads of 64
+// and 128; narrower ones at worst twice).
 #pragma once
 
 #include <climits>
@@ -63,28 +64,40 @@ __device__ __forceinline__ float2 unpack_f16x2(uint32_t u) {
   return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 
-// Tile of one KV head: 16 rows (tokens) of HD bytes, swizzled over spans of
-// kSwizzle bytes: the 16-byte piece i of token t sits at piece i ^ swz(t).
-template <int HD>
-struct Tile {
-  static constexpr int kSwizzle = HD == 128 ? 128 : HD == 64 ? 64 : 0;
-  static __device__ __forceinline__ int swz(int t) {
-    return HD == 128 ? (t & 7) : HD == 64 ? ((t >> 1) & 3) : 0;
+// A block's tile in shared memory: rows of `width` bytes (the TMA box's inner
+// extent), 16 rows (tokens) for each run of `width` bytes of the group's heads.
+// Rows are as wide as they can be, up to 128 bytes, since TMA moves about one
+// row in four cycles whatever its width: at head_dim 64 two heads share one.
+// The 16-byte piece i of token t sits at piece i ^ swz(t) (the hardware's
+// swizzle of that width).
+struct TileView {
+  int width;
+
+  static __host__ __device__ int swizzle(int width) { return width >= 64 ? width : 0; }
+  __device__ __forceinline__ int swz(int t) const {
+    return width == 128 ? (t & 7) : width == 64 ? ((t >> 1) & 3) : 0;
   }
-  // Byte of the tile holding dim d of token t.
-  static __device__ __forceinline__ int at(int t, int d) {
-    return t * HD + (((d >> 4) ^ swz(t)) << 4) + (d & 15);
+  // Byte, within the tile, of byte b of the group's row of token t.
+  __device__ __forceinline__ int at(int t, int b) const {
+    const int run = b / width, o = b - run * width;
+    return (run * kBS + t) * width + (((o >> 4) ^ swz(t)) << 4) + (o & 15);
   }
-  // Token of MMA row i (rows i + 8: token + 8).
-  static __device__ __forceinline__ int tok(int i) {
-    // eight 4-bit entries, row 0 in the lowest
-    constexpr uint32_t order = HD == 128 ? 0x37156240u   // 0 4 2 6 5 1 7 3
-                               : HD == 64 ? 0x65742130u  // 0 3 1 2 4 7 5 6
-                               : HD == 32 ? 0x57463120u  // 0 2 1 3 6 4 7 5
-                                          : 0x76543210u;
+  // Token of MMA row i (rows i + 8: token + 8), eight 4-bit entries.
+  __device__ __forceinline__ int tok(int i) const {
+    const uint32_t order = width == 128  ? 0x37156240u   // 0 4 2 6 5 1 7 3
+                           : width == 64 ? 0x65742130u   // 0 3 1 2 4 7 5 6
+                           : width == 32 ? 0x57463120u   // 0 2 1 3 6 4 7 5
+                                         : 0x76543210u;
     return static_cast<int>((order >> (4 * i)) & 15u);
   }
 };
+
+// Widest row that whole rows of `heads` heads divide into.
+inline int tile_width(int heads, int head_dim) {
+  int w = 128;
+  while ((heads * head_dim) % w != 0) w /= 2;
+  return w;
+}
 
 template <typename T>
 __device__ __forceinline__ void load4(const T* p, float (&x)[4]);
@@ -110,13 +123,34 @@ struct Rows {
   static constexpr int NK = HD / 4 / KB;              // K pieces of a token per lane
   static constexpr int DB = HD / 8;                   // dims of V^T a lane holds
   static constexpr int VW = DB / 4 > 0 ? DB / 4 : 1;  // 32-bit words of them
+  // blocks taken together, as the registers allow
+  static constexpr int PAIR = HD * NT * PARTS <= 128 ? 2 : 1;
 
   uint32_t qb[NT][PARTS][KK][2];
   float o[NT][KK][4];
   float m[NT][2], l[NT][2], rs[NT][2];
   int last[NT][2];
   int cut;  // least last key over the active rows
-  int koff[NK], voff[2];
+  TileView tile;
+  int head_off;             // the head's first byte in the group's row
+  int koff[NK], voff[2];    // this lane's pieces of K and V in a tile
+  int tok_k, tok_v[2];      // their tokens
+
+  // Where the warp's head lies in the tiles.
+  __device__ __forceinline__ void place(int width, int head) {
+    const int lane = threadIdx.x & 31;
+    const int g = lane >> 2, c = lane & 3;
+    tile.width = width;
+    head_off = head * HD;
+    tok_k = tile.tok(g);
+#pragma unroll
+    for (int i = 0; i < NK; ++i) koff[i] = tile.at(tok_k, head_off + i * 64 + c * KB);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      tok_v[i] = tile.tok(2 * c + i);
+      voff[i] = tile.at(tok_v[i], head_off + g * DB);
+    }
+  }
 
   // q_row(r): row r's query (null: no such row); last_key(r): the last key
   // it sees (-1: none).
@@ -124,15 +158,6 @@ struct Rows {
   __device__ __forceinline__ void begin(QRow q_row, LastKey last_key, float scale_log2) {
     const int lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
-    const int t = Tile<HD>::tok(g);
-#pragma unroll
-    for (int i = 0; i < NK; ++i)
-      koff[i] = KB == 16 ? Tile<HD>::at(t, i * 64 + c * 16) : t * HD + c * KB;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int tv = Tile<HD>::tok(2 * c + i);
-      voff[i] = DB >= 8 ? Tile<HD>::at(tv, g * DB) : tv * HD + g * DB;
-    }
     int least = INT_MAX;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -181,102 +206,118 @@ struct Rows {
     cut = __reduce_min_sync(0xffffffffu, least);
   }
 
-  // One block: the head's K and V tiles, the position j0 of its first token,
-  // the sequence's tokens in it (valid: V rows past it are not used), its
-  // scales and lv = log2 vs.
-  __device__ __forceinline__ void block(const uint8_t* kt, const uint8_t* vt, int j0, int valid,
-                                        float ks, float vs, float lv) {
-    const int lane = threadIdx.x & 31;
-    const int g = lane >> 2, c = lane & 3;
+  // NB consecutive blocks: their K and V tiles, the position j0 of the first
+  // token, the sequence's tokens from there on (valid: V rows past them are not
+  // used), the blocks' scales and lv = log2 vs.  Two at a time share one
+  // maximum, one rescaling and the latency of each step.
+  template <int NB>
+  __device__ __forceinline__ void blocks(const uint8_t* const (&kt)[NB],
+                                         const uint8_t* const (&vt)[NB], int j0, int valid,
+                                         const float (&ks)[NB], const float (&vs)[NB],
+                                         const float (&lv)[NB]) {
     // ---- S^T = K Q^T, two chains of products
-    uint32_t kw[2][KK];  // [token g | g + 8]: words of 4 dims
+    uint32_t vw[NB][4][VW];  // tokens tok(2c), tok(2c + 1), and those + 8
+    float w[NB][NT][4];      // scores, then weights
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int nb = 0; nb < NB; ++nb) {
+      uint32_t kw[2][KK];  // [token g | g + 8]: words of 4 dims
 #pragma unroll
-      for (int i = 0; i < NK; ++i) {
-        const uint8_t* p = kt + koff[i] + h * 8 * HD;
-        if constexpr (KB == 16) {
-          const uint4 w = *reinterpret_cast<const uint4*>(p);
-          kw[h][4 * i] = w.x, kw[h][4 * i + 1] = w.y, kw[h][4 * i + 2] = w.z, kw[h][4 * i + 3] = w.w;
-        } else if constexpr (KB == 8) {
-          const uint2 w = *reinterpret_cast<const uint2*>(p);
-          kw[h][0] = w.x, kw[h][1] = w.y;
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+          const uint8_t* p = kt[nb] + koff[i] + h * 8 * tile.width;
+          if constexpr (KB == 16) {
+            const uint4 x = *reinterpret_cast<const uint4*>(p);
+            kw[h][4 * i] = x.x, kw[h][4 * i + 1] = x.y, kw[h][4 * i + 2] = x.z, kw[h][4 * i + 3] = x.w;
+          } else if constexpr (KB == 8) {
+            const uint2 x = *reinterpret_cast<const uint2*>(p);
+            kw[h][0] = x.x, kw[h][1] = x.y;
+          } else {
+            kw[h][0] = *reinterpret_cast<const uint32_t*>(p);
+          }
+        }
+      // V's words too: in flight while the scores are computed
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const uint8_t* p = vt[nb] + voff[h & 1] + (h >> 1) * 8 * tile.width;
+        if constexpr (DB == 16) {
+          const uint4 x = *reinterpret_cast<const uint4*>(p);
+          vw[nb][h][0] = x.x, vw[nb][h][1] = x.y, vw[nb][h][2] = x.z, vw[nb][h][3] = x.w;
+        } else if constexpr (DB == 8) {
+          const uint2 x = *reinterpret_cast<const uint2*>(p);
+          vw[nb][h][0] = x.x, vw[nb][h][1] = x.y;
+        } else if constexpr (DB == 4) {
+          vw[nb][h][0] = *reinterpret_cast<const uint32_t*>(p);
         } else {
-          kw[h][0] = *reinterpret_cast<const uint32_t*>(p);
+          vw[nb][h][0] = *reinterpret_cast<const uint16_t*>(p);
         }
       }
-    // V's words too: in flight while the scores are computed
-    uint32_t vw[4][VW];  // tokens tok(2c), tok(2c + 1), and those + 8
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const uint8_t* p = vt + voff[h & 1] + (h >> 1) * 8 * HD;
-      if constexpr (DB == 16) {
-        const uint4 w = *reinterpret_cast<const uint4*>(p);
-        vw[h][0] = w.x, vw[h][1] = w.y, vw[h][2] = w.z, vw[h][3] = w.w;
-      } else if constexpr (DB == 8) {
-        const uint2 w = *reinterpret_cast<const uint2*>(p);
-        vw[h][0] = w.x, vw[h][1] = w.y;
-      } else if constexpr (DB == 4) {
-        vw[h][0] = *reinterpret_cast<const uint32_t*>(p);
-      } else {
-        vw[h][0] = *reinterpret_cast<const uint16_t*>(p);
-      }
-    }
-    constexpr int CH = KK >= 4 ? 2 : 1;
-    float s[NT][CH][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < CH; ++i) s[nt][i][0] = s[nt][i][1] = s[nt][i][2] = s[nt][i][3] = 0.f;
-#pragma unroll
-    for (int kk = 0; kk < KK; ++kk) {
-      const uint32_t a0 = e4m3x2_to_f16x2(static_cast<uint16_t>(kw[0][kk]));
-      const uint32_t a1 = e4m3x2_to_f16x2(static_cast<uint16_t>(kw[1][kk]));
-      const uint32_t a2 = e4m3x2_to_f16x2(static_cast<uint16_t>(kw[0][kk] >> 16));
-      const uint32_t a3 = e4m3x2_to_f16x2(static_cast<uint16_t>(kw[1][kk] >> 16));
+      constexpr int CH = KK >= 4 ? 2 : 1;
+      float s[NT][CH][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int pt = 0; pt < PARTS; ++pt)
-          mma_f16_16816(s[nt][kk % CH], a0, a1, a2, a3, qb[nt][pt][kk][0], qb[nt][pt][kk][1]);
+        for (int i = 0; i < CH; ++i) s[nt][i][0] = s[nt][i][1] = s[nt][i][2] = s[nt][i][3] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) {
+        const uint32_t a0 = e4m3x2_to_f16x2(static_cast<uint16_t>(kw[0][kk]));
+        const uint32_t a1 = e4m3x2_to_f16x2(static_cast<uint16_t>(kw[1][kk]));
+        const uint32_t a2 = e4m3x2_to_f16x2(static_cast<uint16_t>(kw[0][kk] >> 16));
+        const uint32_t a3 = e4m3x2_to_f16x2(static_cast<uint16_t>(kw[1][kk] >> 16));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int pt = 0; pt < PARTS; ++pt)
+            mma_f16_16816(s[nt][kk % CH], a0, a1, a2, a3, qb[nt][pt][kk][0], qb[nt][pt][kk][1]);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = s[nt][0][e];
+          if constexpr (CH == 2) x += s[nt][1][e];
+          w[nb][nt][e] = x * (rs[nt][e & 1] * ks[nb]);
+        }
     }
-    // ---- scores, mask, running maximum
-    const bool masked = j0 + kBS - 1 > cut;
-    float w[NT][4], alpha[NT][2];
+    // ---- mask, running maximum, weights
+    const bool masked = j0 + NB * kBS - 1 > cut;
+    if (masked) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j0 + nb * kBS + tok_k + (e >> 1) * 8 > last[nt][e & 1]) w[nb][nt][e] = -INFINITY;
+    }
+    float alpha[NT][2];
     bool moved = false;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float x[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float v = s[nt][0][e];
-        if constexpr (CH == 2) v += s[nt][1][e];
-        x[e] = v * (rs[nt][e & 1] * ks);
-      }
-      if (masked) {
-        const int pos = j0 + Tile<HD>::tok(g);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (pos + (e >> 1) * 8 > last[nt][e & 1]) x[e] = -INFINITY;
-      }
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float mx = fmaxf(x[j], x[2 + j]);
+        float mx = fmaxf(w[0][nt][j], w[0][nt][2 + j]) + lv[0];
+#pragma unroll
+        for (int nb = 1; nb < NB; ++nb) mx = fmaxf(mx, fmaxf(w[nb][nt][j], w[nb][nt][2 + j]) + lv[nb]);
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        const float mn = fmaxf(m[nt][j], mx + lv);
+        const float mn = fmaxf(m[nt][j], mx);
         const float ref = mn == -INFINITY ? 0.f : mn;  // nothing visible yet
         alpha[nt][j] = fast_exp2(m[nt][j] - ref);
         moved |= mn != m[nt][j];
         m[nt][j] = mn;
-        const float p0 = fast_exp2(x[j] - (ref - kWeightLog2));
-        const float p1 = fast_exp2(x[2 + j] - (ref - kWeightLog2));
-        l[nt][j] = l[nt][j] * alpha[nt][j] + (p0 + p1);
-        w[nt][j] = p0 * vs;
-        w[nt][2 + j] = p1 * vs;
+        float sum = 0.f;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const float p0 = fast_exp2(w[nb][nt][j] - (ref - kWeightLog2));
+          const float p1 = fast_exp2(w[nb][nt][2 + j] - (ref - kWeightLog2));
+          sum += p0 + p1;
+          w[nb][nt][j] = p0 * vs[nb];
+          w[nb][nt][2 + j] = p1 * vs[nb];
+        }
+        l[nt][j] = l[nt][j] * alpha[nt][j] + sum;
       }
-    }
     // the outputs are rescaled only when some row's maximum moved
     if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -290,69 +331,81 @@ struct Rows {
         }
     }
     // V rows past the sequence's end hold whatever the pool holds there
-    if (valid < kBS) {
+    if (valid < NB * kBS) {
 #pragma unroll
-      for (int h = 0; h < 4; ++h)
-        if (Tile<HD>::tok(2 * c + (h & 1)) + (h >> 1) * 8 >= valid)
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int i = 0; i < VW; ++i) vw[h][i] = 0u;
+        for (int h = 0; h < 4; ++h)
+          if (nb * kBS + tok_v[h & 1] + (h >> 1) * 8 >= valid)
+#pragma unroll
+            for (int i = 0; i < VW; ++i) vw[nb][h][i] = 0u;
     }
+    bool by_term = false;
     if constexpr (CAUSAL) {
       // a NaN among the values must not reach the rows that do not see its
-      // token, as it would through 0 * NaN in the product: such a block is
+      // token, as it would through 0 * NaN in the product: such blocks are
       // summed term by term
       bool nan = false;
       if (masked) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int i = 0; i < VW; ++i) nan |= __vcmpeq4(vw[h][i] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+          for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int i = 0; i < VW; ++i)
+              nan |= __vcmpeq4(vw[nb][h][i] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
       }
-      if (__any_sync(0xffffffffu, nan)) {
-        add_by_term(vt, w, j0, valid);
-        return;
-      }
+      by_term = __any_sync(0xffffffffu, nan);
     }
     // ---- O^T += V^T P^T
-    uint32_t pb[NT][PARTS][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nb = 0; nb < NB; ++nb) {
+      if (CAUSAL && by_term) {
+        add_by_term(vt[nb], w[nb], j0 + nb * kBS, valid - nb * kBS);
+        continue;
+      }
+      uint32_t pb[NT][PARTS][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t hi = pack_f16x2(w[nt][2 * h], w[nt][2 * h + 1]);
-        pb[nt][0][h] = transpose_8x8(hi);
-        if constexpr (HILO) {
-          const float2 f = unpack_f16x2(hi);
-          pb[nt][1][h] = transpose_8x8(pack_f16x2(w[nt][2 * h] - f.x, w[nt][2 * h + 1] - f.y));
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t hi = pack_f16x2(w[nb][nt][2 * h], w[nb][nt][2 * h + 1]);
+          pb[nt][0][h] = transpose_8x8(hi);
+          if constexpr (HILO) {
+            const float2 f = unpack_f16x2(hi);
+            pb[nt][1][h] =
+                transpose_8x8(pack_f16x2(w[nb][nt][2 * h] - f.x, w[nb][nt][2 * h + 1] - f.y));
+          }
         }
-      }
 #pragma unroll
-    for (int i = 0; i < VW; ++i)
+      for (int i = 0; i < VW; ++i)
 #pragma unroll
-      for (int half = 0; half < (DB >= 4 ? 2 : 1); ++half) {
-        const uint32_t sel = half == 0 ? 0x5140u : 0x7362u;
-        const uint32_t lo = __byte_perm(vw[0][i], vw[1][i], sel);
-        const uint32_t hi = __byte_perm(vw[2][i], vw[3][i], sel);
-        const uint32_t a0 = e4m3x2_to_f16x2(static_cast<uint16_t>(lo));
-        const uint32_t a1 = e4m3x2_to_f16x2(static_cast<uint16_t>(lo >> 16));
-        const uint32_t a2 = e4m3x2_to_f16x2(static_cast<uint16_t>(hi));
-        const uint32_t a3 = e4m3x2_to_f16x2(static_cast<uint16_t>(hi >> 16));
+        for (int half = 0; half < (DB >= 4 ? 2 : 1); ++half) {
+          const uint32_t sel = half == 0 ? 0x5140u : 0x7362u;
+          const uint32_t lo = __byte_perm(vw[nb][0][i], vw[nb][1][i], sel);
+          const uint32_t hi = __byte_perm(vw[nb][2][i], vw[nb][3][i], sel);
+          const uint32_t a0 = e4m3x2_to_f16x2(static_cast<uint16_t>(lo));
+          const uint32_t a1 = e4m3x2_to_f16x2(static_cast<uint16_t>(lo >> 16));
+          const uint32_t a2 = e4m3x2_to_f16x2(static_cast<uint16_t>(hi));
+          const uint32_t a3 = e4m3x2_to_f16x2(static_cast<uint16_t>(hi >> 16));
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int pt = 0; pt < PARTS; ++pt)
-            mma_f16_16816(o[nt][2 * i + half], a0, a1, a2, a3, pb[nt][pt][0], pb[nt][pt][1]);
-      }
+            for (int pt = 0; pt < PARTS; ++pt)
+              mma_f16_16816(o[nt][2 * i + half], a0, a1, a2, a3, pb[nt][pt][0], pb[nt][pt][1]);
+        }
+    }
   }
 
   // O += P V of a masked block term by term, the terms of hidden tokens left
   // out (w is 0 there but the value may be NaN).
-  __device__ __noinline__ void add_by_term(const uint8_t* vt, const float (&w)[NT][4], int j0,
+  __device__ __forceinline__ void add_by_term(const uint8_t* vt, const float (&w)[NT][4], int j0,
                                            int valid) {
     const int lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
+#pragma unroll 1
     for (int ti = 0; ti < kBS; ++ti) {
-      const int t = Tile<HD>::tok(ti & 7) + (ti & 8);
+      const int t = tile.tok(ti & 7) + (ti & 8);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -363,7 +416,7 @@ struct Rows {
 #pragma unroll
           for (int i = 0; i < KK; ++i) {
             const int d = g * DB + 2 * i;
-            const uint16_t v2 = *reinterpret_cast<const uint16_t*>(vt + Tile<HD>::at(t, d));
+            const uint16_t v2 = *reinterpret_cast<const uint16_t*>(vt + tile.at(t, head_off + d));
             const float2 v = e4m3x2_to_float2(v2);
             o[nt][i][j] = fmaf(wj, v.x, o[nt][i][j]);
             o[nt][i][2 + j] = fmaf(wj, v.y, o[nt][i][2 + j]);

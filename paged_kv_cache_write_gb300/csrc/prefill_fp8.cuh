@@ -56,30 +56,13 @@ __global__ void __launch_bounds__((kPrefillWarps + 1) * 32, 1)
   const int32_t* row = p.bt + int64_t(b) * p.W;
 
   if (warp == kPrefillWarps) {
-    uint32_t it = 0;
-    bool ok = true;
-    for (int jj = 0; jj < n_blocks && ok; jj += 32) {
-      const int id = jj + lane < n_blocks ? __ldg(row + jj + lane) : 0;
-      const int n_here = min(32, n_blocks - jj);
-      for (int k = 0; k < n_here; ++k) {
-        if (*ring.abort_flag) { ok = false; break; }
-        const int blk = __shfl_sync(0xffffffffu, id, k);
-        const bool good = blk >= 0 && blk < p.num_blocks;
-        if (!good && lane == 0) report(p.err, PKV_DEVERR_BLOCK_ID);
-        bool filled = true;
-        if (lane == 0)  // the chunk's other tiles read the block again: no eviction hint
-          filled = fetch(ring, it, &tm_k, &tm_v, (good ? blk : p.num_blocks) * kBS, g, p.err, 0);
-        if (!__shfl_sync(0xffffffffu, filled, 0)) {
-          *ring.abort_flag = 1;
-          ok = false;
-          break;
-        }
-        ++it;
-      }
+    if (elect_one()) {  // (the chunk's other tiles read the blocks again: no eviction hint)
+      Producer pr{ring, &tm_k, &tm_v, p.num_blocks, p.err, 0};
+      if (!pr.fetch_row(row, n_blocks, g)) pr.drain();
     }
-    if (!ok) attn::ring_drain(ring, it);
   } else {
     Rows<T, HD, kPrefillTiles, true> rows;
+    rows.place(HD, 0);
     const T* q = static_cast<const T*>(p.q);
     const int qw = i0 + warp * p.queries_per_warp;  // first query of this warp
     const int nrows = p.queries_per_warp * p.rep;
@@ -100,25 +83,24 @@ __global__ void __launch_bounds__((kPrefillWarps + 1) * 32, 1)
         [&](int r) { return L - c + query_of(r); }, p.scale_log2);
     // this warp's last visible key
     const int my_last = qw < c ? L - c + min(c, qw + p.queries_per_warp) - 1 : -1;
-    for (int k = 0; k < n_blocks; ++k) {
+    RingPos pos;
+    constexpr int PAIR = Rows<T, HD, kPrefillTiles, true>::PAIR;
+    for (int k = 0; k < n_blocks;) {
       if ((k & 31) == 0) {
         now = next;
         now.settle();
         next.load(sc, dp, ids, g);
         ids = id_at(k + 64 + lane);
       }
-      const float ks = __shfl_sync(0xffffffffu, now.ks, k & 31);
-      const float vs = __shfl_sync(0xffffffffu, now.vs, k & 31);
-      const float lv = __shfl_sync(0xffffffffu, now.lv, k & 31);
-      if (!attn::ring_wait_full(ring, k, p.err)) {
-        *ring.abort_flag = 1;
-        return;
+      const int j0 = k * kBS;
+      const bool use = j0 <= my_last;
+      if (PAIR == 2 && k + 1 < n_blocks) {
+        if (!take_tiles<PAIR>(rows, ring, pos, now, k, j0, L - j0, use, p.err)) return;
+        k += PAIR;
+      } else {
+        if (!take_tiles<1>(rows, ring, pos, now, k, j0, L - j0, use, p.err)) return;
+        ++k;
       }
-      if (k * kBS <= my_last) {
-        const int st = k % ring.nstages;
-        rows.block(ring.k_tile(st), ring.v_tile(st), k * kBS, L - k * kBS, ks, vs, lv);
-      }
-      attn::ring_release(ring, k);
     }
     T* out = static_cast<T*>(p.out);
     rows.store([&](int r) -> T* {
@@ -151,11 +133,7 @@ cudaError_t prefill_run(const AttnArgs& a, const Scales& sc, cudaStream_t stream
   p.nstages = 12;
   const size_t smem = kBarrierBytes + 1024 + size_t(p.nstages) * 2 * kBS * HD;
   CUtensorMap tm_k{}, tm_v{};
-  const uint64_t dims[3] = {HD, uint64_t(pool.num_blocks) * kBS, uint64_t(pool.n_kv)};
-  const uint64_t strides[2] = {uint64_t(pool.n_kv) * HD, HD};
-  const uint32_t box[3] = {HD, kBS, 1};
-  if (!encode_u8(&tm_k, a.k_pool, dims, strides, box, Tile<HD>::kSwizzle) ||
-      !encode_u8(&tm_v, a.v_pool, dims, strides, box, Tile<HD>::kSwizzle))
+  if (!encode_tiles(&tm_k, a.k_pool, pool, HD, 1) || !encode_tiles(&tm_v, a.v_pool, pool, HD, 1))
     return cudaErrorInvalidValue;
   static KernelSetup setup;
   const int threads = (kPrefillWarps + 1) * 32;

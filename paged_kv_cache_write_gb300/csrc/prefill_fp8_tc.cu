@@ -120,12 +120,6 @@ __device__ __forceinline__ void pair_barrier(int x, int w) {
   asm volatile("bar.sync %0, 64;" ::"r"(1 + x * 4 + (w & 3)) : "memory");
 }
 
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
-
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);

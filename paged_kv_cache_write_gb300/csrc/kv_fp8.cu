@@ -27,37 +27,39 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kWindow = 16;  // consecutive tokens whose runs one CTA column handles
-constexpr int kHeld = 8;     // 8-element vectors of a unit a lane holds
+constexpr int kWindow = 32;  // consecutive tokens whose runs one CTA column handles
+constexpr int kHeld = 8;     // 8-element vectors that a lane holds
 
-// Sequences of the tokens t0 .. t0 + n - 1 (n <= 32) of a ragged batch, by
-// the whole CTA: seq_s[i] = number of sequences that end at or before token
-// t0 + i, i.e. its sequence (num_seqs if it lies past the last).  One pass
-// over the offsets with every load in flight, not a chain of dependent ones.
-__device__ __forceinline__ void window_seqs(const int32_t* __restrict__ cu, int num_seqs, int t0,
-                                            int n, int* cnt_s, int* seq_s) {
+// Sequences of the tokens t0 .. t0 + N - 1 (N = 32 or 64) of a ragged batch,
+// by the whole CTA: thread i < N gets the number of sequences that end at or
+// before token t0 + i, i.e. its sequence (num_seqs if it lies past the last).
+// One pass over the offsets with every load in flight, not a chain of
+// dependent ones.
+template <int N>
+__device__ __forceinline__ int window_seq(const int32_t* __restrict__ cu, int num_seqs, int t0,
+                                          int* cnt_s) {
   const int tid = threadIdx.x;
-  if (tid <= n) cnt_s[tid] = 0;  // [0]: ends at or before t0; [i]: ends at t0 + i
+  if (tid < N) cnt_s[tid] = 0;  // [0]: ends at or before t0; [i]: ends at t0 + i
   __syncthreads();
   int before = 0;
 #pragma unroll 4
   for (int i = tid; i < num_seqs; i += kThreads) {
     const int end = __ldg(cu + i + 1);
     if (end <= t0) ++before;
-    else if (end < t0 + n) atomicAdd(cnt_s + (end - t0), 1);
+    else if (end < t0 + N) atomicAdd(cnt_s + (end - t0), 1);
   }
   before = __reduce_add_sync(0xffffffffu, before);
   if ((tid & 31) == 0 && before > 0) atomicAdd(cnt_s, before);
   __syncthreads();
-  if (tid < 32) {
-    int x = tid < n ? cnt_s[tid] : 0;
+  if (tid >= N) return 0;
+  int x = cnt_s[tid];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (tid >= o) x += y;
-    }
-    if (tid < n) seq_s[tid] = x;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if ((tid & 31) >= o) x += y;
   }
+  if (tid >= 32) x += __reduce_add_sync(0xffffffffu, cnt_s[tid & 31]);
+  return x;
 }
 
 struct WriteParams {
@@ -71,67 +73,149 @@ struct WriteParams {
   int W, num_seqs, num_tokens, bs, num_blocks, n_kv, hd;
 };
 
-// Eight consecutive elements of a row as loaded.
+// Eight consecutive elements of a row as loaded.  amax: the larger of `a` and
+// every |x| (NaN is passed over).
 template <typename T>
 struct Vec8;
 
 template <>
 struct Vec8<__nv_bfloat16> {
+  using Max = __nv_bfloat162;
   uint4 w;
   __device__ __forceinline__ void load(const uint8_t* p) {
     w = __ldg(reinterpret_cast<const uint4*>(p));
   }
-  __device__ __forceinline__ void zero() { w = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ uint32_t word(int i) const {
+    return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+  }
   __device__ __forceinline__ float2 pair(int i) const {
-    const uint32_t u = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+    const uint32_t u = word(i);
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
+  static __device__ __forceinline__ Max none() { return __float2bfloat162_rn(0.f); }
+  __device__ __forceinline__ Max amax(Max a) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = word(i);
+      a = __hmax2(a, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&u)));
+    }
+    return a;
+  }
+  static __device__ __forceinline__ float top(Max a) {
+    return fmaxf(__low2float(a), __high2float(a));
   }
 };
 
 template <>
 struct Vec8<float> {
+  using Max = float;
   float4 a, b;
   __device__ __forceinline__ void load(const uint8_t* p) {
     a = __ldg(reinterpret_cast<const float4*>(p));
     b = __ldg(reinterpret_cast<const float4*>(p) + 1);
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ float2 pair(int i) const {
     return i == 0 ? make_float2(a.x, a.y) : i == 1 ? make_float2(a.z, a.w)
          : i == 2 ? make_float2(b.x, b.y) : make_float2(b.z, b.w);
   }
+  static __device__ __forceinline__ Max none() { return 0.f; }
+  __device__ __forceinline__ Max amax(Max m) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = pair(i);
+      m = fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y)));
+    }
+    return m;
+  }
+  static __device__ __forceinline__ float top(Max m) { return m; }
 };
 
-// max(a, |x|) over the vector; fmaxf passes over NaN.
+// One warp's work on one unit: where it reads and writes, and its scale.
 template <typename T>
-__device__ __forceinline__ float vec_amax(const Vec8<T>& v, float a) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 x = v.pair(i);
-    a = fmaxf(a, fmaxf(fabsf(x.x), fabsf(x.y)));
-  }
-  return a;
-}
+struct Unit {
+  const uint8_t* src;  // the run's first row of the head
+  uint8_t* dst;        // row 0 of the block
+  float* scale;
+  float old;           // the block's scale (blocks with earlier tokens)
+  int off, nv;         // rows before the run; vectors of the run
 
-// VPR: 8-element vectors of a head's row (0: read from p.hd).
-template <typename T, int VPR>
-__global__ void __launch_bounds__(kThreads) kv_write_fp8_kernel(const WriteParams p) {
-  __shared__ int cnt_s[33], seq_s[32];
+  // unit u of the window: runs, then K / V, then heads
+  __device__ __forceinline__ void find(const WriteParams& p, const int4* run_s, int u, int vpr) {
+    const int ri = u / (2 * p.n_kv);
+    const int rem = u - ri * 2 * p.n_kv;
+    const bool is_v = rem >= p.n_kv;
+    const int h = is_v ? rem - p.n_kv : rem;
+    const int4 run = run_s[ri];
+    off = run.z;
+    nv = run.y * vpr;
+    scale = (is_v ? p.v_scales : p.k_scales) + int64_t(run.w) * p.n_kv + h;
+    src = (is_v ? p.v : p.k) + (int64_t(run.x) * p.n_kv + h) * p.hd * sizeof(T);
+    dst = (is_v ? p.v_pool : p.k_pool) + (int64_t(run.w) * p.bs * p.n_kv + h) * p.hd;
+  }
+  // the scale for magnitudes up to `a`
+  __device__ __forceinline__ float fit(float a) const {
+    // non-negative floats order as their bits
+    a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
+    const float f = fp8_scale_for(a);
+    return off > 0 ? fmaxf(old, f) : f;
+  }
+  __device__ __forceinline__ void put(const Vec8<T>& v, int e, int vpr, int64_t dst_row,
+                                      float inv) const {
+    uint32_t q[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = v.pair(j);
+      q[j] = e4m3x2(f.x * inv, f.y * inv);
+    }
+    const int r = e / vpr;
+    *reinterpret_cast<uint2*>(dst + (off + r) * dst_row + (e - r * vpr) * 8) =
+        make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+  }
+  // the new scale; earlier rows move to it if it is larger
+  __device__ __forceinline__ void finish(float s, float inv, int vpr, int64_t dst_row) const {
+    const int lane = threadIdx.x & 31;
+    if (off > 0 && s != old) {
+      const float ratio = old * inv;
+      for (int e = lane; e < off * vpr; e += 32) {
+        const int r = e / vpr;
+        uint2* at = reinterpret_cast<uint2*>(dst + r * dst_row + (e - r * vpr) * 8);
+        const uint2 w = *at;
+        auto moved = [&](uint32_t u4) {
+          const float2 lo = e4m3x2_to_float2(static_cast<uint16_t>(u4));
+          const float2 hi = e4m3x2_to_float2(static_cast<uint16_t>(u4 >> 16));
+          return e4m3x2(lo.x * ratio, lo.y * ratio) | (e4m3x2(hi.x * ratio, hi.y * ratio) << 16);
+        };
+        *at = make_uint2(moved(w.x), moved(w.y));
+      }
+    }
+    if (lane == 0 && (off == 0 || s != old)) *scale = s;
+  }
+};
+
+// VPR: 8-element vectors of a head's row (0: read from p.hd).  MU: units that
+// a warp takes at once, each with kHeld / MU vectors a lane (enough for 16
+// rows of VPR vectors); larger units are read twice.
+//
+// A CTA column (x) finds the runs of its window of tokens; the warps of its
+// grid.y CTAs share the units.  Four CTAs of 8 warps fit an SM (bf16), with
+// 2-4 KB in flight per warp.
+template <typename T, int VPR, int MU>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
+    kv_write_fp8_kernel(const WriteParams p) {
+  __shared__ int cnt_s[kWindow];
   __shared__ int4 run_s[kWindow];  // first token, tokens, offset in the block, block
   __shared__ int runs_s;
   const int t0 = blockIdx.x * kWindow;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  window_seqs(p.cu, p.num_seqs, t0, kWindow, cnt_s, seq_s);
+  const int b = window_seq<kWindow>(p.cu, p.num_seqs, t0, cnt_s);
   if (warp == 0) {
-    __syncwarp();
     // a run: the new tokens of one sequence in one block.  Lane i looks at
     // token t0 + i: it begins a run if it is its sequence's first new token
     // or the first of a block.
     const int t = t0 + lane;
     int4 run = make_int4(0, 0, 0, 0);
     bool begins = false;
-    if (lane < kWindow && t < p.num_tokens) {
-      const int b = seq_s[lane];
+    if (t < p.num_tokens) {
       if (b >= p.num_seqs) {
         report(p.err, PKV_DEVERR_LENGTH);  // offsets that stop short of the token count
       } else {
@@ -162,87 +246,61 @@ __global__ void __launch_bounds__(kThreads) kv_write_fp8_kernel(const WriteParam
   }
   __syncthreads();
 
+  constexpr int PU = kHeld / MU;  // vectors a lane holds of a unit
   const int vpr = VPR > 0 ? VPR : p.hd / 8;
   const int units = runs_s * 2 * p.n_kv;
   const int64_t src_row = int64_t(p.n_kv) * p.hd * sizeof(T);
   const int64_t dst_row = int64_t(p.n_kv) * p.hd;
-  for (int u = blockIdx.y * kWarps + warp; u < units; u += gridDim.y * kWarps) {
-    const int ri = u / (2 * p.n_kv);
-    const int rem = u - ri * 2 * p.n_kv;
-    const bool is_v = rem >= p.n_kv;
-    const int h = is_v ? rem - p.n_kv : rem;
-    const int4 run = run_s[ri];
-    const int off = run.z;
-    float* scale = (is_v ? p.v_scales : p.k_scales) + int64_t(run.w) * p.n_kv + h;
-    const float old = off > 0 ? *scale : 0.f;
-    const uint8_t* src = (is_v ? p.v : p.k) + (int64_t(run.x) * p.n_kv + h) * p.hd * sizeof(T);
-    // row 0 of the block
-    uint8_t* dst = (is_v ? p.v_pool : p.k_pool) + (int64_t(run.w) * p.bs * p.n_kv + h) * p.hd;
-    const int nv = run.y * vpr;
-    Vec8<T> v[kHeld];
-    auto load = [&](int base) {
+  for (int u = (blockIdx.y * kWarps + warp) * MU; u < units; u += gridDim.y * kWarps * MU) {
+    Unit<T> un[MU];
+    Vec8<T> v[MU][PU];
+    // (past the unit's end the last vector again, which changes no maximum: a
+    // load behind a condition is waited for where it is issued)
+    auto load = [&](int m, int base) {
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        const int e = base + i * 32 + lane;
-        if (e < nv) {
-          const int r = e / vpr;
-          v[i].load(src + r * src_row + (e - r * vpr) * 8 * sizeof(T));
-        } else {
-          v[i].zero();
-        }
+      for (int i = 0; i < PU; ++i) {
+        const int e = min(base + i * 32 + lane, un[m].nv - 1);
+        const int r = e / vpr;
+        v[m][i].load(un[m].src + r * src_row + (e - r * vpr) * 8 * sizeof(T));
       }
     };
-    float a = 0.f;
-    for (int base = 0; base < nv; base += kHeld * 32) {
-      load(base);
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i) a = vec_amax<T>(v[i], a);
+    for (int m = 0; m < MU; ++m) {
+      un[m].find(p, run_s, min(u + m, units - 1), vpr);
+      un[m].old = *un[m].scale;
+      load(m, 0);
     }
-    // non-negative floats order as their bits
-    a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
-    const float fit = fp8_scale_for(a);
-    const float s = off > 0 ? fmaxf(old, fit) : fit;
-    const float inv = 1.f / s;  // exact: s is a power of two
-    for (int base = 0; base < nv; base += kHeld * 32) {
-      if (nv > kHeld * 32) load(base);  // a unit too large to hold: read again
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        const int e = base + i * 32 + lane;
-        if (e < nv) {
-          uint32_t q[4];
+    for (int m = 0; m < MU; ++m) {
+      if (u + m >= units) break;
+      typename Vec8<T>::Max a = Vec8<T>::none();
+      for (int base = 0;;) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = v[i].pair(j);
-            q[j] = e4m3x2(f.x * inv, f.y * inv);
-          }
-          const int r = e / vpr;
-          *reinterpret_cast<uint2*>(dst + (off + r) * dst_row + (e - r * vpr) * 8) =
-              make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+        for (int i = 0; i < PU; ++i) a = v[m][i].amax(a);
+        if ((base += PU * 32) >= un[m].nv) break;
+        load(m, base);
+      }
+      const float s = un[m].fit(Vec8<T>::top(a));
+      const float inv = 1.f / s;  // exact: s is a power of two
+      const bool again = un[m].nv > PU * 32;  // too large to hold
+      for (int base = 0; base < un[m].nv; base += PU * 32) {
+        if (again) load(m, base);
+#pragma unroll
+        for (int i = 0; i < PU; ++i) {
+          const int e = base + i * 32 + lane;
+          if (e < un[m].nv) un[m].put(v[m][i], e, vpr, dst_row, inv);
         }
       }
+      un[m].finish(s, inv, vpr, dst_row);
     }
-    if (off > 0 && s != old) {  // the scale grew: the earlier rows move to it
-      const float ratio = old * inv;
-      for (int e = lane; e < off * vpr; e += 32) {
-        const int r = e / vpr;
-        uint2* at = reinterpret_cast<uint2*>(dst + r * dst_row + (e - r * vpr) * 8);
-        const uint2 w = *at;
-        auto moved = [&](uint32_t u4) {
-          const float2 lo = e4m3x2_to_float2(static_cast<uint16_t>(u4));
-          const float2 hi = e4m3x2_to_float2(static_cast<uint16_t>(u4 >> 16));
-          return e4m3x2(lo.x * ratio, lo.y * ratio) | (e4m3x2(hi.x * ratio, hi.y * ratio) << 16);
-        };
-        *at = make_uint2(moved(w.x), moved(w.y));
-      }
-    }
-    if (lane == 0 && (off == 0 || s != old)) *scale = s;
   }
 }
 
 // ------------------------------------------------------------------ gather
 
 constexpr int kGatherTokens = 32;
-constexpr int kGatherUnroll = 4;
+constexpr int kGatherRows = 4;   // rows a warp reads at once
+constexpr int kGatherSteps = 2;  // and steps of 32 items in each
 
 struct GatherParams {
   const uint8_t *k_pool, *v_pool;
@@ -255,53 +313,50 @@ struct GatherParams {
   int W, num_seqs, total, bs, num_blocks, n_kv, hd;
 };
 
-// 16 values of the cache in the output type (exact in both).
+// An item: as many elements as fill one 16-byte store, so that a warp's stores
+// are contiguous (16 elements an item would store them in strided pieces:
+// 3.5 TB/s for fp32).
 template <typename T>
-__device__ __forceinline__ void store16(uint8_t* dst, const uint4& w, float s);
+struct Item;
 
 template <>
-__device__ __forceinline__ void store16<float>(uint8_t* dst, const uint4& w, float s) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 a = e4m3x2_to_float2(static_cast<uint16_t>(u[i]));
-    const float2 b = e4m3x2_to_float2(static_cast<uint16_t>(u[i] >> 16));
-    __stcs(reinterpret_cast<float4*>(dst) + i, make_float4(a.x * s, a.y * s, b.x * s, b.y * s));
+struct Item<float> {
+  using Load = uint32_t;  // 4 elements
+  static __device__ __forceinline__ void store(uint8_t* dst, uint32_t u, float s) {
+    const float2 a = e4m3x2_to_float2(static_cast<uint16_t>(u));
+    const float2 b = e4m3x2_to_float2(static_cast<uint16_t>(u >> 16));
+    __stcs(reinterpret_cast<float4*>(dst), make_float4(a.x * s, a.y * s, b.x * s, b.y * s));
   }
-}
+};
 
 template <>
-__device__ __forceinline__ void store16<__nv_bfloat16>(uint8_t* dst, const uint4& w, float s) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t o[4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float2 a = e4m3x2_to_float2(static_cast<uint16_t>(u[2 * i + j]));
-      const float2 b = e4m3x2_to_float2(static_cast<uint16_t>(u[2 * i + j] >> 16));
-      o[2 * j] = pack_bf16x2(a.x * s, a.y * s);
-      o[2 * j + 1] = pack_bf16x2(b.x * s, b.y * s);
-    }
-    __stcs(reinterpret_cast<uint4*>(dst) + i, make_uint4(o[0], o[1], o[2], o[3]));
+struct Item<__nv_bfloat16> {
+  using Load = uint2;  // 8 elements (their values are bf16 numbers: nothing is rounded)
+  static __device__ __forceinline__ void store(uint8_t* dst, uint2 u, float s) {
+    const float2 a = e4m3x2_to_float2(static_cast<uint16_t>(u.x));
+    const float2 b = e4m3x2_to_float2(static_cast<uint16_t>(u.x >> 16));
+    const float2 c = e4m3x2_to_float2(static_cast<uint16_t>(u.y));
+    const float2 d = e4m3x2_to_float2(static_cast<uint16_t>(u.y >> 16));
+    __stcs(reinterpret_cast<uint4*>(dst),
+           make_uint4(pack_bf16x2(a.x * s, a.y * s), pack_bf16x2(b.x * s, b.y * s),
+                      pack_bf16x2(c.x * s, c.y * s), pack_bf16x2(d.x * s, d.y * s)));
   }
-}
+};
 
-// A CTA reads back kGatherTokens rows of K and of V; a thread handles 16
-// elements (one 16-byte load) at a time, kGatherUnroll loads in flight.
+// A CTA reads back kGatherTokens tokens: 2 x kGatherTokens rows of n_kv x hd
+// elements (K and V), kGatherRows rows of a warp at a time with
+// kGatherRows x kGatherSteps loads in flight per lane.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) kv_gather_fp8_kernel(const GatherParams p) {
-  __shared__ int cnt_s[33], seq_s[32];
+  __shared__ int cnt_s[kGatherTokens];
   __shared__ int blk_s[kGatherTokens], off_s[kGatherTokens];
   const int t0 = blockIdx.x * kGatherTokens;
   const int n = min(kGatherTokens, p.total - t0);
-  window_seqs(p.cu, p.num_seqs, t0, kGatherTokens, cnt_s, seq_s);
-  if (threadIdx.x < 32) {
-    __syncwarp();
+  const int b = window_seq<kGatherTokens>(p.cu, p.num_seqs, t0, cnt_s);
+  if (threadIdx.x < kGatherTokens) {
     const int i = threadIdx.x;
     int blk = -1, off = 0;  // -1: nothing to read, zeros
     if (i < n) {
-      const int b = seq_s[i];
       if (b >= p.num_seqs) {
         report(p.err, PKV_DEVERR_LENGTH);
       } else {
@@ -319,39 +374,57 @@ __global__ void __launch_bounds__(kThreads) kv_gather_fp8_kernel(const GatherPar
           }
         }
       }
-      blk_s[i] = blk;
-      off_s[i] = off;
     }
+    blk_s[i] = blk;
+    off_s[i] = off;
   }
   __syncthreads();
-  const int wpr = p.n_kv * p.hd / 16;  // 16-element words of a row
-  const int wph = p.hd / 16;
-  const int items = 2 * n * wpr;
-  for (int i0 = threadIdx.x; i0 < items; i0 += kThreads * kGatherUnroll) {
-    uint4 w[kGatherUnroll];
-    float s[kGatherUnroll];
+  using Load = typename Item<T>::Load;
+  constexpr int E = sizeof(Load);  // elements per item, one byte each
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ipr = p.n_kv * p.hd / E;  // items of a row
+  const int iph = p.hd / E;           // and of a head
+  const bool pow2 = (iph & (iph - 1)) == 0;
+  const int shift = 31 - __clz(iph);
+  // rows 0 .. n - 1 are K's, n .. 2 n - 1 V's
+  for (int r0 = warp * kGatherRows; r0 < 2 * n; r0 += kWarps * kGatherRows) {
+    const uint8_t* src[kGatherRows];
+    const float* scale[kGatherRows];
+    uint8_t* dst[kGatherRows];
+    bool have[kGatherRows];
 #pragma unroll
-    for (int k = 0; k < kGatherUnroll; ++k) {
-      const int i = i0 + k * kThreads;
-      w[k] = make_uint4(0u, 0u, 0u, 0u);
-      s[k] = 0.f;
-      if (i >= items) continue;
-      const bool is_v = i >= n * wpr;
-      const int j = is_v ? i - n * wpr : i;
-      const int t = j / wpr, c = j - t * wpr;
-      const int blk = blk_s[t];
-      if (blk < 0) continue;
-      w[k] = __ldcs(reinterpret_cast<const uint4*>(is_v ? p.v_pool : p.k_pool) +
-                    (int64_t(blk) * p.bs + off_s[t]) * wpr + c);
-      s[k] = __ldg((is_v ? p.v_scales : p.k_scales) + int64_t(blk) * p.n_kv + c / wph);
+    for (int k = 0; k < kGatherRows; ++k) {
+      const int r = min(r0 + k, 2 * n - 1);  // past the last row: it again
+      const bool is_v = r >= n;
+      const int t = is_v ? r - n : r;
+      have[k] = blk_s[t] >= 0;
+      const int64_t blk = max(blk_s[t], 0);
+      src[k] = (is_v ? p.v_pool : p.k_pool) + (blk * p.bs + off_s[t]) * ipr * E;
+      scale[k] = (is_v ? p.v_scales : p.k_scales) + blk * p.n_kv;
+      dst[k] = (is_v ? p.v_out : p.k_out) + int64_t(t0 + t) * ipr * 16;
     }
+    for (int c0 = lane; c0 < ipr; c0 += 32 * kGatherSteps) {
+      Load w[kGatherRows][kGatherSteps];
+      float s[kGatherRows][kGatherSteps];
 #pragma unroll
-    for (int k = 0; k < kGatherUnroll; ++k) {
-      const int i = i0 + k * kThreads;
-      if (i >= items) continue;
-      const bool is_v = i >= n * wpr;
-      const int j = is_v ? i - n * wpr : i;
-      store16<T>((is_v ? p.v_out : p.k_out) + (int64_t(t0) * wpr + j) * 16 * sizeof(T), w[k], s[k]);
+      for (int q = 0; q < kGatherSteps; ++q) {
+        const int c = min(c0 + 32 * q, ipr - 1);
+        const int h = pow2 ? c >> shift : c / iph;
+#pragma unroll
+        for (int k = 0; k < kGatherRows; ++k) {
+          w[k][q] = __ldcs(reinterpret_cast<const Load*>(src[k]) + c);
+          s[k][q] = __ldg(scale[k] + h);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kGatherSteps; ++q) {
+        const int c = c0 + 32 * q;
+        if (c < ipr) {
+#pragma unroll
+          for (int k = 0; k < kGatherRows; ++k)
+            if (r0 + k < 2 * n) Item<T>::store(dst[k] + int64_t(c) * 16, have[k] ? w[k][q] : Load{}, have[k] ? s[k][q] : 0.f);
+        }
+      }
     }
   }
 }
@@ -360,13 +433,13 @@ __global__ void __launch_bounds__(kThreads) kv_gather_fp8_kernel(const GatherPar
 
 template <typename T>
 static cudaError_t write_as(const WriteParams& p, dim3 grid, cudaStream_t stream) {
-  switch (p.hd) {
-    case 16: kv_write_fp8_kernel<T, 2><<<grid, kThreads, 0, stream>>>(p); break;
-    case 32: kv_write_fp8_kernel<T, 4><<<grid, kThreads, 0, stream>>>(p); break;
-    case 64: kv_write_fp8_kernel<T, 8><<<grid, kThreads, 0, stream>>>(p); break;
-    case 128: kv_write_fp8_kernel<T, 16><<<grid, kThreads, 0, stream>>>(p); break;
-    default: kv_write_fp8_kernel<T, 0><<<grid, kThreads, 0, stream>>>(p); break;
-  }
+  // two units at once where 16 rows of a head are at most half of what a warp
+  // holds, and blocks have no more rows than that
+  if (p.bs <= 16 && p.hd == 16) kv_write_fp8_kernel<T, 2, 2><<<grid, kThreads, 0, stream>>>(p);
+  else if (p.bs <= 16 && p.hd == 32) kv_write_fp8_kernel<T, 4, 2><<<grid, kThreads, 0, stream>>>(p);
+  else if (p.bs <= 16 && p.hd == 64) kv_write_fp8_kernel<T, 8, 2><<<grid, kThreads, 0, stream>>>(p);
+  else if (p.hd == 128) kv_write_fp8_kernel<T, 16, 1><<<grid, kThreads, 0, stream>>>(p);
+  else kv_write_fp8_kernel<T, 0, 1><<<grid, kThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -394,14 +467,19 @@ cudaError_t launch_kv_write_fp8(const void* k, const void* v, int32_t dtype, con
   p.num_blocks = pool.num_blocks;
   p.n_kv = pool.n_kv;
   p.hd = pool.head_dim;
-  // enough warps per window that each has about one unit: a window of 16
-  // tokens holds about 16 / block_size + 16 * num_seqs / num_tokens runs
+  // A window holds about kWindow / block_size + 1 + kWindow * num_seqs /
+  // num_tokens runs.  Few windows (a decode step): CTAs enough that each warp
+  // has about one unit.  Many (prompts): one CTA a window, so that what it
+  // takes to find the runs is paid once for all their units (31,722 tokens of
+  // 8 x 64: 63 us with four CTAs for each window of 16).
+  const int64_t windows = (int64_t(num_tokens) + kWindow - 1) / kWindow;
   const int64_t runs = std::min<int64_t>(
       std::min(kWindow, num_tokens),
       kWindow / pool.block_size + 1 + int64_t(kWindow) * num_seqs / num_tokens);
-  const int64_t per = (runs * 2 * pool.n_kv + kWarps - 1) / kWarps;
-  const dim3 grid(static_cast<unsigned>((int64_t(num_tokens) + kWindow - 1) / kWindow),
-                  static_cast<unsigned>(std::min<int64_t>(per, 1024)));
+  const int64_t most = (runs * 2 * pool.n_kv + kWarps - 1) / kWarps;
+  const int64_t want = (int64_t(sm_count()) * 4 + windows - 1) / windows;
+  const dim3 grid(static_cast<unsigned>(windows),
+                  static_cast<unsigned>(std::min<int64_t>(std::min(most, want), 1024)));
   return dtype == PKV_F32 ? write_as<float>(p, grid, stream)
                           : write_as<__nv_bfloat16>(p, grid, stream);
 }

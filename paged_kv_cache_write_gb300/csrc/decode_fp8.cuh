@@ -89,7 +89,7 @@ struct Producer {
   __device__ __forceinline__ bool fetch(int id, int run0) {
     const bool good = id >= 0 && id < num_blocks;
     if (!good) report(err, PKV_DEVERR_BLOCK_ID);
-    if (pos.round > 0 && !mbar_wait(ring.empty + pos.st, (pos.round - 1) & 1)) {
+    if (pos.round > 0 && !wait_or_abort(ring.empty + pos.st, (pos.round - 1) & 1, ring.abort_flag)) {
       report(err, PKV_DEVERR_TIMEOUT);
       return false;
     }
@@ -142,14 +142,9 @@ struct Producer {
 // Consumer warp: wait for its next tile; false if the producer gave up or the
 // wait timed out.
 __device__ __forceinline__ bool wait_tile(const Ring& r, const RingPos& pos, int32_t* err) {
-  uint64_t* full = r.full + pos.st;
-  const uint32_t parity = pos.round & 1;
-  if (mbar_try_wait(full, parity)) return true;
-  for (uint32_t i = 0; i < kMaxPolls; ++i) {
-    if (*r.abort_flag) return false;
-    if (mbar_try_wait(full, parity)) return true;
-  }
-  if ((threadIdx.x & 31) == 0) report(err, PKV_DEVERR_TIMEOUT);
+  if (wait_or_abort(r.full + pos.st, pos.round & 1, r.abort_flag)) return true;
+  // (the one that gives up first reports: the others see its flag)
+  if ((threadIdx.x & 31) == 0 && !*r.abort_flag) report(err, PKV_DEVERR_TIMEOUT);
   return false;
 }
 

@@ -69,4 +69,19 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
+// Polls after which a wait of the 8-bit kernels gives up: 0.1 s at least (a
+// failed poll takes some 50 cycles, or as long as the hardware parks the thread).
+constexpr uint32_t kFp8Polls = 1u << 22;
+
+// Bounded wait that also ends once some thread of the CTA has given up.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity,
+                                              volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  for (uint32_t i = 0; i < kFp8Polls; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+  }
+  return false;
+}
+
 }  // namespace pkv

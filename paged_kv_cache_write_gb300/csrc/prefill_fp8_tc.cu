@@ -4,10 +4,11 @@
 // What is computed: query i of a chunk of c queries at the end of an L-token
 // sequence attends keys 0 .. L - c + i of its KV head, with element = e4m3
 // value x scale of (block, head).  With the byte values k8, v8 of a block:
-//   x = (q . k8) * (scale * log2 e * ks),  w = 2^(x + log2 vs - M + 11),
+//   x = (q . k8) * (scale * log2 e * ks),  w = 2^(x + log2 vs - M + 4),
 //   l += (sum of the block's w) / vs,  O += w v8,  out = O / l.
-// M is a running reference of x + log2 vs, moved only when the maximum has
-// passed it by 2^4, so weights stay below 2^15: an f16 operand, and scales cost
+// M is a running reference of x + log2 vs, moved to the maximum when a weight
+// would pass f16's 65,504 (the maximum has grown 2^12-fold: seldom after
+// the first tile; f16 is normal down to 2^-18 of the reference's weight).  Scales cost
 // nothing per element: they are constants of a 16-key block.
 //
 // tcgen05 takes no f16 x e4m3 product, so the cache's bytes become f16 (exact)
@@ -19,21 +20,26 @@
 // a row is one (query, query head) pair.  Keys go in tiles of 64 (4 blocks), so
 // that scores have two buffers per row tile in TMEM: while a tile's softmax
 // runs, its next scores are computed, and neither waits for the other.
-//  warps 0-7    softmax of tile A, 8-15 of tile B.  Two threads per row, 32 of
-//               the 64 scores each (warps w and w + 4 hold the same TMEM
-//               lanes); they exchange their maxima in shared memory.  Weights
-//               go back to TMEM as f16 over the scores.
-//  warp 16      allocates TMEM (2 S_A, 2 S_B, O_A, O_B: all 512 columns at
-//               head_dim 128) and one lane issues the MMAs: S_X of the first
-//               two key tiles, then for each key tile j and row tile X, once
-//               its weights are there, O_X += W_X V_j and S_X = Q_X K_{j+2}^T.
-//  warps 17-23  bring K and V, a block (16 tokens) at a time in turn: 16-byte
+//  warps 0-3    softmax of tile A, 4-7 of tile B: one thread per row.  Weights
+//               are computed against the reference as it stands; only if some
+//               weight came out past f16's range (their partial sums tell) the
+//               maximum is taken, the reference moved to it and the tile done
+//               again, so that most tiles need no maximum at all.  Weights go
+//               back to TMEM as f16 over the scores.
+//  warps 8, 9   issue the MMAs of tiles A and B, one elected lane each: S_X of
+//               the first two key tiles, then for each key tile j, once its
+//               weights are there, O_X += W_X V_j and S_X = Q_X K_{j+2}^T.
+//               (A look at a barrier takes the issuing lane 120 cycles, a step's
+//               MMAs 600: one lane for both tiles left the tensor core idle
+//               half of the time.)  Warp 8 allocates TMEM: 2 S_A, 2 S_B, O_A,
+//               O_B, all 512 columns at head_dim 128.
+//  warps 10-15  bring K and V, a block (16 tokens) at a time in turn: 16-byte
 //               loads straight from the pool, each warp's next two blocks on
 //               their way, e4m3 -> f16 in registers, 128-byte-swizzled tiles
 //               in four-stage rings.
-// 24 warps leave 80 registers a thread, and no loop may spill: with 200 KB of
-// shared memory little L1 is left, and a reload from local memory costs an
-// L2 round trip.
+// 16 warps leave 128 registers a thread, and no loop may spill: with 200 KB of
+// shared memory little L1 is left, and a reload from local memory costs an L2
+// round trip.
 //
 // Values past the sequence's end are stored as zeros.  A NaN value that some
 // row of the tile may not see is stored as zero too, and its dim and first
@@ -60,18 +66,17 @@ constexpr int kRows = 128;
 constexpr int kTileKeys = 64;
 constexpr int kBlk = 16;
 constexpr int kBlocks = kTileKeys / kBlk;  // blocks per key tile
-constexpr int kHalfKeys = kTileKeys / 2;   // scores of a softmax thread
-static_assert(kBlocks == 4 && kHalfKeys == 32, "units and chunks below");
-constexpr int kMmaWarp = 16;
-constexpr int kLoadWarp0 = 17;
-constexpr int kLoadWarps = 7;
+static_assert(kBlocks == 4, "units and score chunks below");
+constexpr int kMmaWarp = 8;  // and 9, after eight of the softmax
+constexpr int kLoadWarp0 = 10;
+constexpr int kLoadWarps = 6;
 constexpr int kAhead = 2;  // blocks in flight per load warp
-constexpr int kThreads = 24 * 32;
+constexpr int kThreads = 16 * 32;
 constexpr int kStages = 4;
 constexpr int kScaleStages = 8;  // scales outlive their K stage (see the load warps)
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRescaleLog2 = 4.f;  // move the reference when the maximum passes it by 2^4
-constexpr float kWeightLog2 = 11.f;  // weights below 2^(11 + 4)
+constexpr float kWeightLog2 = 4.f;     // log2 of the reference's weight
+constexpr float kWeightMax = 65504.f;  // f16's largest
 constexpr uint32_t kTmemCols = 512;
 
 struct TcParams {
@@ -99,8 +104,7 @@ struct Layout {
   static constexpr int KV_TILE = NH * KV_HALF;
   static constexpr int K_OFF = 2 * Q_TILE;  // after Q_A, Q_B
   static constexpr int V_OFF = K_OFF + kStages * KV_TILE;
-  static constexpr int XM_OFF = V_OFF + kStages * KV_TILE;          // [turn][tile][half][128]
-  static constexpr int SCALE_OFF = XM_OFF + 2 * 2 * 2 * kRows * 4;  // ks, lv, 1/vs [stages][4]
+  static constexpr int SCALE_OFF = V_OFF + kStages * KV_TILE;  // ks, lv, 1/vs [stages][4]
   static constexpr int NAN_OFF = SCALE_OFF + 3 * kScaleStages * kBlocks * 4;  // [HD] + flag
   static constexpr int BAR_OFF = (NAN_OFF + HD * 4 + 16 + 15) / 16 * 16;
   static constexpr int BYTES = BAR_OFF + 512;
@@ -115,19 +119,23 @@ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn) {
   return (1u << 4) | (uint32_t(b_mn) << 16) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
 
-// The two warps (64 threads) that share rows 32 (w % 4) .. of tile x.
-__device__ __forceinline__ void pair_barrier(int x, int w) {
-  asm volatile("bar.sync %0, 64;" ::"r"(1 + x * 4 + (w & 3)) : "memory");
-}
-
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity) {
-  const bool ok = mbar_wait(bar, parity);
-  return __all_sync(0xffffffffu, ok);
+
+// Whether the barrier's phase of this parity is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
 }
 
 template <int HD>
@@ -218,33 +226,40 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_empty = bars + 14;       // [4]
   uint64_t* s_full = bars + 18;        // [row tile][buffer]
   uint64_t* w_ready = bars + 22;       // [row tile][buffer]
-  uint64_t* o_done = bars + 26;        // [row tile][key tile % 2]
-  uint64_t* drain = bars + 30;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 31);
+  uint64_t* o_done = bars + 26;        // [row tile][key tile % 2], the last two tiles
+  uint64_t* drain = bars + 30;         // [2] per row tile
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 32);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* ks_s = reinterpret_cast<float*>(smem + Lay::SCALE_OFF);  // [kScaleStages][4]
   float* lv_s = ks_s + kScaleStages * kBlocks;
   float* iv_s = lv_s + kScaleStages * kBlocks;
-  float* xm_s = reinterpret_cast<float*>(smem + Lay::XM_OFF);  // [turn][tile][half][row]
   int* nan_s = reinterpret_cast<int*>(smem + Lay::NAN_OFF);    // [HD] first NaN position
   int* nan_any = nan_s + HD;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  // every wait is one of these two: bounded, by a whole warp or by one lane
+  auto wait_one = [&](uint64_t* bar, uint32_t parity) {
+    return wait_or_abort(bar, parity, abort_flag);
+  };
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_one(bar, parity)) != 0;
+  };
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) mbar_init(q_full + i, 8);
+    for (int i = 0; i < 2; ++i) mbar_init(q_full + i, 4);
     for (int i = 0; i < 4; ++i) {
       mbar_init(s_full + i, 1);
-      mbar_init(w_ready + i, 8);
+      mbar_init(w_ready + i, 4);
       mbar_init(o_done + i, 1);
     }
     for (int i = 0; i < kStages; ++i) {
       mbar_init(k_full + i, kBlocks);
-      mbar_init(k_empty + i, 1);
+      mbar_init(k_empty + i, 2);  // left by both row tiles
       mbar_init(v_full + i, kBlocks);
-      mbar_init(v_empty + i, 1);
+      mbar_init(v_empty + i, 2);
     }
     mbar_init(drain, 1);
+    mbar_init(drain + 1, 1);
     *abort_flag = 0;
     *nan_any = 0;
     job_s[0] = i0;
@@ -402,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         id_next[k] = id_of(un + kAhead * kLoadWarps);
       }
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kMmaWarp) {
     // ----------------------------------------------------------------- MMA
     // One elected lane.  (elect.sync, not a test of the lane: the compiler then
     // keeps descriptors in uniform registers, and an MMA takes some 30 cycles
@@ -428,57 +443,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t vd = v_desc + uint32_t((j % kStages) * Lay::KV_TILE) / 16;
 #pragma unroll
         for (int kk = 0; kk < kTileKeys / 16; ++kk)
-          // W: the softmax halves' 16 columns at columns 0 and 32 of S
-          tc::mma_ts(o_tm(x), s_tm(x, j) + (kk >> 1) * 32 + (kk & 1) * 8, vd + kk * 2048 / 16,
-                     idesc_pv, j > 0 || kk > 0);
-        tc::commit(o_done + x * 2 + (j & 1));
+          // W: 16 f16 are 8 columns
+          tc::mma_ts(o_tm(x), s_tm(x, j) + kk * 8, vd + kk * 2048 / 16, idesc_pv, j > 0 || kk > 0);
+        if (j + 2 >= n_tiles) tc::commit(o_done + x * 2 + (j & 1));  // (see the softmax)
       };
-      bool ok = true;
+      const int x = warp - kMmaWarp;
+      bool ok = wait_one(q_full + x, 0);
       for (int j = 0; j < 2 && j < n_tiles && ok; ++j) {
-        if (!(ok = mbar_wait(k_full + j, 0))) break;
-        for (int x = 0; x < 2 && ok; ++x) {
-          if (j == 0 && !(ok = mbar_wait(q_full + x, 0))) break;
-          tc::fence_after_sync();
-          issue_qk(x, j);
-        }
-        tc::commit(k_empty + j);  // K_j is no longer read
+        if (!(ok = wait_one(k_full + j, 0))) break;
+        tc::fence_after_sync();
+        issue_qk(x, j);
+        tc::commit(k_empty + j);  // this row tile has read K_j
       }
       for (int j = 0; j < n_tiles && ok; ++j) {
-        const bool more = j + 2 < n_tiles;
-        const int kn = (j + 2) % kStages;
-        for (int x = 0; x < 2 && ok; ++x) {
-          if (!(ok = mbar_wait(w_ready + x * 2 + (j & 1), (j >> 1) & 1))) break;
-          if (x == 0 && !(ok = mbar_wait(v_full + (j % kStages), (j / kStages) & 1))) break;
-          tc::fence_after_sync();
-          issue_pv(x, j);
-          if (x == 1) tc::commit(v_empty + (j % kStages));  // V_j is no longer read
-          if (!more) continue;
-          if (x == 0) {
-            if (!(ok = mbar_wait(k_full + kn, ((j + 2) / kStages) & 1))) break;
-            tc::fence_after_sync();
-          }
-          issue_qk(x, j + 2);
-          if (x == 1) tc::commit(k_empty + kn);  // K_{j+2} is no longer read
-        }
+        const int st = j % kStages, kn = (j + 2) % kStages;
+        if (!(ok = wait_one(v_full + st, (j / kStages) & 1))) break;
+        if (!(ok = wait_one(w_ready + x * 2 + (j & 1), (j >> 1) & 1))) break;
+        tc::fence_after_sync();
+        issue_pv(x, j);
+        tc::commit(v_empty + st);
+        if (j + 2 >= n_tiles) continue;
+        if (!(ok = wait_one(k_full + kn, ((j + 2) / kStages) & 1))) break;
+        tc::fence_after_sync();
+        issue_qk(x, j + 2);
+        tc::commit(k_empty + kn);
       }
       if (!ok) {
         report(p.err, PKV_DEVERR_TIMEOUT);
         *abort_flag = 1;
       }
       // every MMA issued above has finished before TMEM is released
-      tc::commit(drain);
-      mbar_wait(drain, 0);
+      tc::commit(drain + x);
+      mbar_wait(drain + x, 0, kFp8Polls);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------- softmax
-    const int x = warp >> 3;               // tile A or B
-    const int hf = (warp >> 2) & 1;        // half of the keys (and of the dims)
+    const int x = warp >> 2;               // tile A or B
     const int r = (warp & 3) * 32 + lane;  // TMEM lane = row of the tile
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    // the thread's row (its query, or -1) and where its half of it lies in q
-    // and out; what this needs is read back from shared memory at the end, so
-    // that it takes no registers in between
+    // the thread's row: its query (or -1) and where it lies in q and out; what
+    // this needs is read back from shared memory at the end, so that it takes
+    // no registers in between
     struct Row {
       int qi;
       int64_t off;
@@ -489,49 +495,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int qi = job[0] + x * p.q_per_tile + q;  // i0 + ...
       const bool active = q < p.q_per_tile && qi < job[1];
       return Row{active ? qi : -1,
-                 (int64_t(job[2] + qi) * p.n_heads + job[3] * p.rep + (r - q * p.rep)) * HD +
-                     hf * (HD / 2)};
+                 (int64_t(job[2] + qi) * p.n_heads + job[3] * p.rep + (r - q * p.rep)) * HD};
     };
     int last;
-    // exchange with the row's other thread; the two places take turns, so one
-    // barrier per exchange is enough (a place is written again only after the
-    // next exchange's barrier, which the other thread passes having read it)
-    auto exchange = [&](float v, int turn) {
-      const int mine = ((turn & 1) * 4 + x * 2 + hf) * kRows + r;
-      xm_s[mine] = v;
-      pair_barrier(x, warp);
-      return xm_s[mine ^ kRows];
-    };
     float rs;  // undoes the row's power of two; times scale * log2 e
     {
       const Row me = my_row();
       last = me.qi >= 0 ? L - c + me.qi : -1;
-      uint4 u[HD / 16];
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + (me.qi >= 0 ? me.off : 0));
+      // two passes, eight vectors at a time: the row's maximum, then its values
       float a = 0.f;
+#pragma unroll 1
+      for (int i0 = 0; i0 < HD / 8; i0 += 8) {
+        uint4 u[8];
 #pragma unroll
-      for (int i = 0; i < HD / 16; ++i) {
-        u[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (me.qi >= 0) u[i] = __ldg(reinterpret_cast<const uint4*>(p.q + me.off) + i);
-        const uint32_t e[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+        for (int i = 0; i < 8; ++i) u[i] = __ldg(src + i0 + i);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          a = fmaxf(a, fmaxf(fabsf(__uint_as_float(e[k] << 16)),
-                             fabsf(__uint_as_float(e[k] & 0xffff0000u))));
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t e[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            a = fmaxf(a, fmaxf(fabsf(__uint_as_float(e[k] << 16)),
+                               fabsf(__uint_as_float(e[k] & 0xffff0000u))));
+        }
       }
-      a = fmaxf(a, exchange(a, 0));
       const int up = min(126, 14 + 127 - static_cast<int>(__float_as_uint(a) >> 23));
-      const float f = pow2f(up);
+      const float f = me.qi >= 0 ? pow2f(up) : 0.f;  // rows without a query hold zeros
       rs = pow2f(-up) * p.scale_log2;
+#pragma unroll 1
+      for (int i0 = 0; i0 < HD / 8; i0 += 8) {
+        uint4 u[8];
 #pragma unroll
-      for (int i = 0; i < HD / 16; ++i) {
-        const uint32_t e[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-        uint32_t o[4];
+        for (int i = 0; i < 8; ++i) u[i] = __ldg(src + i0 + i);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          o[k] = pack_f16x2(__uint_as_float(e[k] << 16) * f, __uint_as_float(e[k] & 0xffff0000u) * f);
-        const int d16 = hf * (HD / 16) + i;  // 16-byte piece of the row
-        *reinterpret_cast<uint4*>(q_tile(x) + (d16 >> 3) * Lay::Q_HALF + r * 128 +
-                                  (((d16 & 7) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t e[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            o[k] = pack_f16x2(__uint_as_float(e[k] << 16) * f,
+                              __uint_as_float(e[k] & 0xffff0000u) * f);
+          *reinterpret_cast<uint4*>(q_tile(x) + (i0 >> 3) * Lay::Q_HALF + r * 128 +
+                                    ((i ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -539,77 +545,101 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     float m_used = -INFINITY, l_sum = 0.f;
     bool ok = true;
-    for (int j = 0; j < n_tiles; ++j) {
-      // (every thread passes the same barriers whatever happens to its waits)
-      if (ok && !(ok = wait_all(s_full + x * 2 + (j & 1), (j >> 1) & 1)) && lane == 0) {
+    auto gave_up = [&]() {
+      if (lane == 0) {
         report(p.err, PKV_DEVERR_TIMEOUT);
         *abort_flag = 1;
       }
+      ok = false;
+    };
+    uint32_t v[kTileKeys];  // scores
+    auto request = [&](int j) {  // (there after tmem_wait_ld)
       tc::fence_after_sync();
-      const uint32_t s_addr = s_tm(x, j) + lane_base + hf * kHalfKeys;
-      uint32_t v[kHalfKeys];
-      tc::tmem_ld32(s_addr, v);
-      const float* ks = ks_s + (j % kScaleStages) * kBlocks + hf * 2;
-      const float2 ks2 = *reinterpret_cast<const float2*>(ks);
-      const float2 lv2 = *reinterpret_cast<const float2*>(ks + kScaleStages * kBlocks);
-      const float2 iv2 = *reinterpret_cast<const float2*>(ks + 2 * kScaleStages * kBlocks);
+      tc::tmem_ld32(s_tm(x, j) + lane_base, *reinterpret_cast<uint32_t(*)[32]>(v));
+      tc::tmem_ld32(s_tm(x, j) + lane_base + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+    };
+    auto s_bar = [&](int j) { return s_full + x * 2 + (j & 1); };
+    if (wait_all(s_bar(0), 0)) request(0);
+    else gave_up();
+    for (int j = 0; j < n_tiles && ok; ++j) {
+      const uint32_t s_addr = s_tm(x, j) + lane_base;
+      const float* sc = ks_s + (j % kScaleStages) * kBlocks;
+      const float4 k4 = *reinterpret_cast<const float4*>(sc);
+      const float4 l4 = *reinterpret_cast<const float4*>(sc + kScaleStages * kBlocks);
+      const float4 i4 = *reinterpret_cast<const float4*>(sc + 2 * kScaleStages * kBlocks);
       // (factors are > 0; none is zero: -inf stays -inf)
-      const float f[2] = {fmaxf(rs * ks2.x, 1.2e-38f), fmaxf(rs * ks2.y, 1.2e-38f)};
-      const float lv[2] = {lv2.x, lv2.y}, iv[2] = {iv2.x, iv2.y};
-      const int pos0 = j * kTileKeys + hf * kHalfKeys;
+      const float factor[4] = {fmaxf(rs * k4.x, 1.2e-38f), fmaxf(rs * k4.y, 1.2e-38f),
+                               fmaxf(rs * k4.z, 1.2e-38f), fmaxf(rs * k4.w, 1.2e-38f)};
+      const float shift[4] = {l4.x, l4.y, l4.z, l4.w}, inv_vs[4] = {i4.x, i4.y, i4.z, i4.w};
+      const int pos0 = j * kTileKeys;
       tc::tmem_wait_ld();
-      if (pos0 + kHalfKeys - 1 > last) {  // keys past this row's causal limit
+      if (pos0 + kTileKeys - 1 > last) {  // keys past this row's causal limit
 #pragma unroll
-        for (int k = 0; k < kHalfKeys; ++k)
+        for (int k = 0; k < kTileKeys; ++k)
           if (pos0 + k > last) v[k] = __float_as_uint(-INFINITY);
       }
-      // maximum of x + log2 vs, block by block
-      float mx = -INFINITY;
+      float alpha = 1.f, add = 0.f;
+      bool move = j == 0;  // set the reference to the maximum
+#pragma unroll 1
+      for (int pass = 0; pass < 2; ++pass) {
+        if (move) {
+          float mx = -INFINITY;  // of x + log2 vs
 #pragma unroll
-      for (int bk = 0; bk < 2; ++bk) {
-        float mb = __uint_as_float(v[bk * 16]);
+          for (int bk = 0; bk < kBlocks; ++bk) {
+            float mb = __uint_as_float(v[bk * 16]);
 #pragma unroll
-        for (int k = 1; k < 16; ++k) mb = fmaxf(mb, __uint_as_float(v[bk * 16 + k]));
-        mx = fmaxf(mx, fmaf(mb, f[bk], lv[bk]));
-      }
-      mx = fmaxf(mx, exchange(mx, j + 1));
-      const float m_new = fmaxf(m_used, mx);
-      const bool grow = m_new > m_used + kRescaleLog2;
-      const float alpha = grow ? fast_exp2(m_used - m_new) : 1.f;
-      if (grow) m_used = m_new;
-      const float mref = (m_used == -INFINITY ? 0.f : m_used) - kWeightLog2;
-      float add = 0.f;
-      uint32_t pk[16];
-#pragma unroll
-      for (int bk = 0; bk < 2; ++bk) {
-        const float cst = lv[bk] - mref;
-        const float2 f2 = make_float2(f[bk], f[bk]), c2 = make_float2(cst, cst);
-        float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int e = bk * 16 + 2 * k;
-          const float2 t2 =
-              __ffma2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), f2, c2);
-          const float2 pe = make_float2(fast_exp2(t2.x), fast_exp2(t2.y));
-          acc = __fadd2_rn(acc, pe);
-          pk[bk * 8 + k] = pack_f16x2(pe.x, pe.y);
+            for (int k = 1; k < 16; ++k) mb = fmaxf(mb, __uint_as_float(v[bk * 16 + k]));
+            mx = fmaxf(mx, fmaf(mb, factor[bk], shift[bk]));
+          }
+          const float m_new = fmaxf(m_used, mx);
+          alpha = m_new > m_used ? fast_exp2(m_used - m_new) : 1.f;
+          m_used = m_new;
         }
-        add = fmaf(acc.x + acc.y, iv[bk], add);
+        const float mref = (m_used == -INFINITY ? 0.f : m_used) - kWeightLog2;
+        float most = 0.f;
+        add = 0.f;
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int bb = 0; bb < 2; ++bb) {
+            const int bk = ch * 2 + bb;
+            const float f = factor[bk], cst = shift[bk] - mref;
+            const float2 f2 = make_float2(f, f), c2 = make_float2(cst, cst);
+            float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int e = bk * 16 + 2 * k;
+              const float2 t2 =
+                  __ffma2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), f2, c2);
+              const float2 pe = make_float2(fast_exp2(t2.x), fast_exp2(t2.y));
+              acc = __fadd2_rn(acc, pe);
+              pk[bb * 8 + k] = pack_f16x2(pe.x, pe.y);
+            }
+            add = fmaf(acc.x + acc.y, inv_vs[bk], add);
+            most = fmaxf(most, fmaxf(acc.x, acc.y));  // no weight is larger
+          }
+          tc::tmem_st16(s_addr + ch * 16, pk);
+        }
+        move = most > kWeightMax;
+        if (!__any_sync(0xffffffffu, move)) break;
       }
-      tc::tmem_st16(s_addr, pk);
       l_sum = l_sum * alpha + add;
       if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-        // O_X has to hold all products before this tile's.  (W_j is not there
-        // yet, so no later phase of the barrier can have completed.)
-        if (ok && !(ok = wait_all(o_done + x * 2 + ((j - 1) & 1), ((j - 1) >> 1) & 1)) && lane == 0) {
-          report(p.err, PKV_DEVERR_TIMEOUT);
-          *abort_flag = 1;
+        // O_X has to hold all products before this tile's.  S_{j+1} was computed
+        // after them; only the last tiles have a barrier for it of their own.
+        // (W_j is not there yet, so no later phase can have completed.)
+        const bool there = j + 1 < n_tiles ? wait_all(s_bar(j + 1), ((j + 1) >> 1) & 1)
+                                           : wait_all(o_done + x * 2 + ((j - 1) & 1), 0);
+        if (!there) {
+          gave_up();
+          break;
         }
         tc::fence_after_sync();
         const float2 a2 = make_float2(alpha, alpha);
 #pragma unroll 1
-        for (int ch = 0; ch < HD / 64; ++ch) {
-          const uint32_t o_addr = o_tm(x) + lane_base + hf * (HD / 2) + ch * 32;
+        for (int ch = 0; ch < HD / 32; ++ch) {
+          const uint32_t o_addr = o_tm(x) + lane_base + ch * 32;
           uint32_t ov[32];
           tc::tmem_ld32(o_addr, ov);
           tc::tmem_wait_ld();
@@ -623,16 +653,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::tmem_st32(o_addr, ov);
         }
       }
+      // The next scores are mostly there (their product was issued a tile ago):
+      // their load then overlaps the weights' store.
+      const bool more = j + 1 < n_tiles;
+      const bool early =
+          more && __all_sync(0xffffffffu, mbar_test(s_bar(j + 1), ((j + 1) >> 1) & 1));
+      if (early) request(j + 1);
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(w_ready + x * 2 + (j & 1));
+      if (more && !early) {
+        if (wait_all(s_bar(j + 1), ((j + 1) >> 1) & 1)) request(j + 1);
+        else gave_up();
+      }
     }
-    l_sum += exchange(l_sum, n_tiles + 1);
-    if (ok && !(ok = wait_all(o_done + x * 2 + ((n_tiles - 1) & 1), ((n_tiles - 1) >> 1) & 1)) && lane == 0) {
-      report(p.err, PKV_DEVERR_TIMEOUT);
-      *abort_flag = 1;
-    }
+    tc::tmem_wait_ld();  // (after giving up, a request may be in flight)
+    if (ok && !wait_all(o_done + x * 2 + ((n_tiles - 1) & 1), 0)) gave_up();
     if (ok) {
       tc::fence_after_sync();
       const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
@@ -640,12 +677,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Row me = my_row();
       __nv_bfloat16* orow = p.out + me.off;
 #pragma unroll 1
-      for (int ch = 0; ch < HD / 64; ++ch) {
+      for (int ch = 0; ch < HD / 32; ++ch) {
         uint32_t ov[32];
-        tc::tmem_ld32(o_tm(x) + lane_base + hf * (HD / 2) + ch * 32, ov);
+        tc::tmem_ld32(o_tm(x) + lane_base + ch * 32, ov);
         tc::tmem_wait_ld();
         if (nans) {
-          const volatile int* first = nan_s + hf * (HD / 2) + ch * 32;
+          const volatile int* first = nan_s + ch * 32;
 #pragma unroll
           for (int k = 0; k < 32; ++k)
             if (first[k] <= last) ov[k] = 0x7fc00000u;

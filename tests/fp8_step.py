@@ -136,7 +136,7 @@ class Batch:
 
     def check(self, got, q, which, last, held=15):
         """got, q [rows, H, hd]; row i is sequence which[i]'s, over keys 0..last[i].
-        held: 15, or 11 for the prefill, whose reference may lag its maximum by 2^4."""
+        held: 15, or 4 for the prefill, whose largest weight may be held at 2^4."""
         got, q = f64(got), f64(q)
         worst = 0.0
         for i, (b, n) in enumerate(zip(which, last)):

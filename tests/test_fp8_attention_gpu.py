@@ -204,7 +204,7 @@ def _prefill_case(heads, n_kv, head_dim, dtype, lens, new, seed=0):
     bt.no_error()
     which = [b for b, c in enumerate(new) for _ in range(c)]
     last = [n - c + i for n, c in zip(lens, new) for i in range(c)]
-    bt.check(out, q, which, last, held=11)
+    bt.check(out, q, which, last, held=4)
     return bt, q, out
 
 
@@ -237,7 +237,7 @@ def test_prefill_scales_far_apart(head_dim, dtype):
     q = bt.queries(300, 2)
     out = bt.prefill(q, lens, [300])
     bt.no_error()
-    bt.check(out, q, [0] * 300, range(300), held=11)
+    bt.check(out, q, [0] * 300, range(300), held=4)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -265,7 +265,7 @@ def test_prefill_hidden_nan_stays_hidden(head_dim, dtype):
         ck, cv = clean.draw(n), clean.draw(n)
         (ck if what == "k" else cv)[at, 0, 3] = 0.0
         clean.write([n], [n], ck, cv)
-        clean.check(out[:at], q[:at], [0] * at, range(at), held=11)
+        clean.check(out[:at], q[:at], [0] * at, range(at), held=4)
 
 
 def test_prefill_bad_device_data():
@@ -304,7 +304,7 @@ def test_prompts_then_decode_steps(heads, n_kv, head_dim, dtype):
         out = bt.prefill(q, have, new)
         which = [b for b, c in enumerate(new) for _ in range(c)]
         bt.check(out, q, which, [n - c + i for n, c in zip(have, new) for i in range(c)],
-                 held=11)
+                 held=4)
     for s in range(1, steps + 1):
         have = prompt + s
         bt.write(have, [1] * 4, bt.draw(4, 1.0 + s % 3), bt.draw(4, 1.0 + s % 4))

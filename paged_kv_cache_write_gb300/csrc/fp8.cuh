@@ -69,16 +69,30 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// Polls after which a wait of the 8-bit kernels gives up: 0.1 s at least (a
-// failed poll takes some 50 cycles, or as long as the hardware parks the thread).
-constexpr uint32_t kFp8Polls = 1u << 22;
+// Waits of the 8-bit kernels: the hardware parks the thread until the phase is
+// complete or, for a poll that fails, for up to kParkNs; after kFp8Polls of
+// those (2 s) the wait gives up.
+constexpr uint32_t kParkNs = 100000;
+constexpr uint32_t kFp8Polls = 20000;
+
+__device__ __forceinline__ bool mbar_park(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(kParkNs)
+      : "memory");
+  return done != 0;
+}
 
 // Bounded wait that also ends once some thread of the CTA has given up.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity,
                                               volatile int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_park(bar, parity)) return true;
   for (uint32_t i = 0; i < kFp8Polls; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_park(bar, parity)) return true;
     if (*abort_flag) return false;
   }
   return false;

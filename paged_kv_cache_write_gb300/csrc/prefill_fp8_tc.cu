@@ -457,14 +457,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int j = 0; j < n_tiles && ok; ++j) {
         const int st = j % kStages, kn = (j + 2) % kStages;
-        if (!(ok = wait_one(v_full + st, (j / kStages) & 1))) break;
-        if (!(ok = wait_one(w_ready + x * 2 + (j & 1), (j >> 1) & 1))) break;
+        const bool more = j + 2 < n_tiles;
+        // (the weights last: once they are there both products go at once)
+        ok = wait_one(v_full + st, (j / kStages) & 1) &&
+             (!more || wait_one(k_full + kn, ((j + 2) / kStages) & 1)) &&
+             wait_one(w_ready + x * 2 + (j & 1), (j >> 1) & 1);
+        if (!ok) break;
         tc::fence_after_sync();
         issue_pv(x, j);
         tc::commit(v_empty + st);
-        if (j + 2 >= n_tiles) continue;
-        if (!(ok = wait_one(k_full + kn, ((j + 2) / kStages) & 1))) break;
-        tc::fence_after_sync();
+        if (!more) continue;
         issue_qk(x, j + 2);
         tc::commit(k_empty + kn);
       }
@@ -474,7 +476,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // every MMA issued above has finished before TMEM is released
       tc::commit(drain + x);
-      mbar_wait(drain + x, 0, kFp8Polls);
+      for (uint32_t i = 0; i < kFp8Polls && !mbar_park(drain + x, 0); ++i) {
+      }
     }
     __syncwarp();
   } else {
@@ -497,11 +500,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       return Row{active ? qi : -1,
                  (int64_t(job[2] + qi) * p.n_heads + job[3] * p.rep + (r - q * p.rep)) * HD};
     };
-    int last;
+    int last, cut;  // last key that the row sees; the least of the warp's rows
     float rs;  // undoes the row's power of two; times scale * log2 e
     {
       const Row me = my_row();
-      last = me.qi >= 0 ? L - c + me.qi : -1;
+      last = me.qi >= 0 ? L - c + me.qi : INT_MAX;  // a row without a query is never masked
+      cut = __reduce_min_sync(0xffffffffu, last);
       const uint4* src = reinterpret_cast<const uint4*>(p.q + (me.qi >= 0 ? me.off : 0));
       // two passes, eight vectors at a time: the row's maximum, then its values
       float a = 0.f;
@@ -573,13 +577,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float shift[4] = {l4.x, l4.y, l4.z, l4.w}, inv_vs[4] = {i4.x, i4.y, i4.z, i4.w};
       const int pos0 = j * kTileKeys;
       tc::tmem_wait_ld();
-      if (pos0 + kTileKeys - 1 > last) {  // keys past this row's causal limit
+      if (pos0 + kTileKeys - 1 > cut) {  // keys past some row's causal limit
 #pragma unroll
         for (int k = 0; k < kTileKeys; ++k)
           if (pos0 + k > last) v[k] = __float_as_uint(-INFINITY);
       }
       float alpha = 1.f, add = 0.f;
-      bool move = j == 0;  // set the reference to the maximum
+      bool move = j == 0;     // set the reference to the maximum
+      bool rescale = false;   // some row of the warp moved its reference
 #pragma unroll 1
       for (int pass = 0; pass < 2; ++pass) {
         if (move) {
@@ -595,6 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           alpha = m_new > m_used ? fast_exp2(m_used - m_new) : 1.f;
           m_used = m_new;
         }
+        rescale = pass > 0;
         const float mref = (m_used == -INFINITY ? 0.f : m_used) - kWeightLog2;
         float most = 0.f;
         add = 0.f;
@@ -625,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!__any_sync(0xffffffffu, move)) break;
       }
       l_sum = l_sum * alpha + add;
-      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+      if (rescale && j > 0) {
         // O_X has to hold all products before this tile's.  S_{j+1} was computed
         // after them; only the last tiles have a barrier for it of their own.
         // (W_j is not there yet, so no later phase can have completed.)

@@ -486,16 +486,18 @@ def _ptr(t, name, dtype, index):
     return _dev(t, name, dtype)  # raises: it is not the type or layout asked for
 
 
-def _call_on(index, name, stream, *args):
-    """Call entry point ``name`` with device ``index`` current; its stream comes last."""
-    fn = getattr(_lib or _load(), name)
-    if torch.cuda.current_device() == index:
-        status = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
-    else:
-        with torch.cuda.device(index):
-            status = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
-    if status:
-        _check(name, status)
+def _elsewhere(index):
+    """Whether another device than ``index`` is current (a call then repeats
+    itself with ``index`` current)."""
+    return torch.cuda.current_device() != index
+
+
+_TYPE_CODES = {torch.float32: PKV_F32, torch.bfloat16: PKV_BF16}
+
+
+def _type_code(dtype):
+    code = _TYPE_CODES.get(dtype)
+    return _dtype_code(dtype) if code is None else code  # (raises)
 
 
 def _fp8_pool(k_pool, v_pool, k_scales, v_scales):
@@ -513,9 +515,8 @@ def _fp8_pool(k_pool, v_pool, k_scales, v_scales):
     if index < 0:
         raise ValueError("k_pool must be a CUDA tensor (the library has no CPU path)")
     desc = PoolDesc(nb, bs, nkv, hd, PKV_FP8_E4M3)
-    return index, desc, (_ptr(k_pool, "k_pool", _f8, index), _ptr(v_pool, "v_pool", _f8, index),
-                         _ptr(k_scales, "k_scales", _f32, index),
-                         _ptr(v_scales, "v_scales", _f32, index))
+    return (index, desc, _ptr(k_pool, "k_pool", _f8, index), _ptr(v_pool, "v_pool", _f8, index),
+            _ptr(k_scales, "k_scales", _f32, index), _ptr(v_scales, "v_scales", _f32, index))
 
 
 def _batch(block_tables, seq_lens):
@@ -545,17 +546,24 @@ def kv_write_fp8(k, v, block_tables, seq_lens, cu_new_lens, k_pool, v_pool, k_sc
     keeps at least its scale; where a new token needs a larger one the earlier
     rows are moved to it.
     """
-    i, desc, pools = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
+    i, desc, kp, vp, ks, vs = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
     B, W = _batch(block_tables, seq_lens)
     shape = k.shape
     if len(shape) != 3 or shape != (shape[0], desc.n_kv, desc.head_dim) or v.shape != shape:
         raise ValueError("k, v must be [T, n_kv, head_dim] matching the pool")
+    if _elsewhere(i):
+        with torch.cuda.device(i):
+            return kv_write_fp8(k, v, block_tables, seq_lens, cu_new_lens, k_pool, v_pool,
+                                k_scales, v_scales, err=err, stream=stream)
     dt = k.dtype
-    _call_on(i, "pkv_kv_write_fp8", stream, _ptr(k, "k", dt, i), _ptr(v, "v", dt, i),
-             _dtype_code(dt), _ptr(block_tables, "block_tables", _int, i), W,
-             _ptr(seq_lens, "seq_lens", _int, i), _offsets(cu_new_lens, "cu_new_lens", B, i), B,
-             shape[0], *pools, ctypes.byref(desc),
-             None if err is None else _ptr(err, "err", _int, i))
+    status = (_lib or _load()).pkv_kv_write_fp8(
+        _ptr(k, "k", dt, i), _ptr(v, "v", dt, i), _type_code(dt),
+        _ptr(block_tables, "block_tables", _int, i), W, _ptr(seq_lens, "seq_lens", _int, i),
+        _offsets(cu_new_lens, "cu_new_lens", B, i), B, shape[0], kp, vp, ks, vs,
+        ctypes.byref(desc), None if err is None else _ptr(err, "err", _int, i),
+        _raw_stream(i) if stream is None else _stream(stream))
+    if status:
+        raise PkvError("pkv_kv_write_fp8", status)
 
 
 def kv_gather_fp8(k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, cu_seq_lens,
@@ -564,10 +572,10 @@ def kv_gather_fp8(k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, cu
     """Contiguous [total_tokens, n_kv, head_dim] K and V of an 8-bit cache in
     logical order, each value times its scale, in ``dtype`` (float32 or
     bfloat16; that of ``k_out`` / ``v_out`` where given)."""
-    i, desc, pools = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
+    i, desc, kp, vp, ks, vs = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
     B, W = _batch(block_tables, seq_lens)
     dt = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else dtype
-    code = _dtype_code(dt)
+    code = _type_code(dt)
     shape = (int(total_tokens), desc.n_kv, desc.head_dim)
     if k_out is None:
         k_out = torch.empty(shape, dtype=dt, device=k_pool.device)
@@ -575,11 +583,19 @@ def kv_gather_fp8(k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, cu
         v_out = torch.empty(shape, dtype=dt, device=k_pool.device)
     if k_out.shape != shape or v_out.shape != shape:
         raise ValueError(f"k_out, v_out must be {shape}")
-    _call_on(i, "pkv_kv_gather_fp8", stream, *pools, ctypes.byref(desc),
-             _ptr(block_tables, "block_tables", _int, i), W, _ptr(seq_lens, "seq_lens", _int, i),
-             _offsets(cu_seq_lens, "cu_seq_lens", B, i), B, shape[0], code,
-             _ptr(k_out, "k_out", dt, i), _ptr(v_out, "v_out", dt, i),
-             None if err is None else _ptr(err, "err", _int, i))
+    if _elsewhere(i):
+        with torch.cuda.device(i):
+            return kv_gather_fp8(k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
+                                 cu_seq_lens, total_tokens, k_out=k_out, v_out=v_out, err=err,
+                                 stream=stream)
+    status = (_lib or _load()).pkv_kv_gather_fp8(
+        kp, vp, ks, vs, ctypes.byref(desc), _ptr(block_tables, "block_tables", _int, i), W,
+        _ptr(seq_lens, "seq_lens", _int, i), _offsets(cu_seq_lens, "cu_seq_lens", B, i), B,
+        shape[0], code, _ptr(k_out, "k_out", dt, i), _ptr(v_out, "v_out", dt, i),
+        None if err is None else _ptr(err, "err", _int, i),
+        _raw_stream(i) if stream is None else _stream(stream))
+    if status:
+        raise PkvError("pkv_kv_gather_fp8", status)
     return k_out, v_out
 
 
@@ -610,7 +626,7 @@ def paged_attention_decode_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tabl
     :func:`paged_attention_decode`, with ``decode_fp8_workspace_bytes(...)``
     bytes; calls that may run at the same time need a workspace each.
     """
-    i, desc, pools = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
+    i, desc, kp, vp, ks, vs = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
     B, W = _batch(block_tables, seq_lens)
     out, rows, H = _fp8_query(q, desc.head_dim, out)
     if rows != B:
@@ -620,12 +636,22 @@ def paged_attention_decode_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tabl
     if workspace is None:
         need = decode_fp8_workspace_bytes(B, H, desc.head_dim, max_seq_len, max_ctas)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if _elsewhere(i):
+        with torch.cuda.device(i):
+            return paged_attention_decode_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tables,
+                                              seq_lens, scale, max_seq_len, out=out,
+                                              workspace=workspace, max_ctas=max_ctas, err=err,
+                                              stream=stream)
     dt = q.dtype
-    _call_on(i, "pkv_paged_attention_decode_fp8", stream, _ptr(q, "q", dt, i), _dtype_code(dt), B,
-             H, *pools, ctypes.byref(desc), _ptr(block_tables, "block_tables", _int, i), W,
-             _ptr(seq_lens, "seq_lens", _int, i), int(max_seq_len), float(scale), int(max_ctas),
-             _ptr(out, "out", dt, i), _ptr(workspace, "workspace", workspace.dtype, i),
-             workspace.nbytes, None if err is None else _ptr(err, "err", _int, i))
+    status = (_lib or _load()).pkv_paged_attention_decode_fp8(
+        _ptr(q, "q", dt, i), _type_code(dt), B, H, kp, vp, ks, vs, ctypes.byref(desc),
+        _ptr(block_tables, "block_tables", _int, i), W, _ptr(seq_lens, "seq_lens", _int, i),
+        int(max_seq_len), float(scale), int(max_ctas), _ptr(out, "out", dt, i),
+        _ptr(workspace, "workspace", workspace.dtype, i), workspace.nbytes,
+        None if err is None else _ptr(err, "err", _int, i),
+        _raw_stream(i) if stream is None else _stream(stream))
+    if status:
+        raise PkvError("pkv_paged_attention_decode_fp8", status)
     return out
 
 
@@ -635,17 +661,26 @@ def paged_attention_prefill_fp8(q, cu_q_lens, k_pool, v_pool, k_scales, v_scales
                                 stream=None):
     """Causal chunked-prefill attention [total_q, n_heads, head_dim] (float32
     or bfloat16) over the paged history of an 8-bit cache."""
-    i, desc, pools = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
+    i, desc, kp, vp, ks, vs = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
     B, W = _batch(block_tables, seq_lens)
     out, rows, H = _fp8_query(q, desc.head_dim, out)
     if max_q_len is None:
         max_q_len = int((cu_q_lens[1:] - cu_q_lens[:-1]).max().item()) if B else 0
     if max_seq_len is None:
         max_seq_len = int(seq_lens.max().item()) if B else 0
+    if _elsewhere(i):
+        with torch.cuda.device(i):
+            return paged_attention_prefill_fp8(q, cu_q_lens, k_pool, v_pool, k_scales, v_scales,
+                                               block_tables, seq_lens, scale, max_q_len,
+                                               max_seq_len, out=out, err=err, stream=stream)
     dt = q.dtype
-    _call_on(i, "pkv_paged_attention_prefill_fp8", stream, _ptr(q, "q", dt, i), _dtype_code(dt),
-             _offsets(cu_q_lens, "cu_q_lens", B, i), B, rows, int(max_q_len), H, *pools,
-             ctypes.byref(desc), _ptr(block_tables, "block_tables", _int, i), W,
-             _ptr(seq_lens, "seq_lens", _int, i), int(max_seq_len), float(scale),
-             _ptr(out, "out", dt, i), None if err is None else _ptr(err, "err", _int, i))
+    status = (_lib or _load()).pkv_paged_attention_prefill_fp8(
+        _ptr(q, "q", dt, i), _type_code(dt), _offsets(cu_q_lens, "cu_q_lens", B, i), B, rows,
+        int(max_q_len), H, kp, vp, ks, vs, ctypes.byref(desc),
+        _ptr(block_tables, "block_tables", _int, i), W, _ptr(seq_lens, "seq_lens", _int, i),
+        int(max_seq_len), float(scale), _ptr(out, "out", dt, i),
+        None if err is None else _ptr(err, "err", _int, i),
+        _raw_stream(i) if stream is None else _stream(stream))
+    if status:
+        raise PkvError("pkv_paged_attention_prefill_fp8", status)
     return out

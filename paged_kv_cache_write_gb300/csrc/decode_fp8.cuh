@@ -20,7 +20,6 @@
 namespace pkv {
 namespace fp8 {
 
-using attn::Cursor;
 using attn::DecodeParams;
 using attn::DecodeWs;
 using attn::Ring;
@@ -46,6 +45,42 @@ inline int head_group(int n_kv) {
     if (n_kv % h == 0) best = h;
   return best;
 }
+
+// Lengths that a CTA which plans for itself keeps in shared memory (larger
+// batches read them again where they are needed).
+constexpr int kKeptLens = 1024;
+
+// Walks a CTA's contiguous range of units segment by segment: a segment is the
+// run of one (sequence, head group)'s blocks inside the range.
+struct Walk {
+  const DecodeParams& p;
+  const int* lens;  // kept lengths, or null
+  int b = 0, grp = 0, j = 0, L = 0, nblk = 1;
+
+  __device__ __forceinline__ void enter() {
+    L = lens != nullptr ? lens[b] : attn::used_len(p, b);
+    nblk = (L + kBS - 1) / kBS;
+  }
+  __device__ __forceinline__ void begin(int4 st) {
+    b = st.x, grp = st.y, j = st.z;
+    enter();
+  }
+  // past n units of the current group
+  __device__ __forceinline__ void advance(int n) {
+    j += n;
+    if (j < nblk) return;
+    j = 0;
+    if (++grp < p.n_groups) return;
+    grp = 0;
+    do {
+      if (++b >= p.B) {  // past the last unit: never used
+        nblk = 1;
+        return;
+      }
+      enter();
+    } while (nblk == 0);
+  }
+};
 
 // tc::tma_load_3d with an L2 cache policy for the copied lines.
 __device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* map, int x, int y,
@@ -221,6 +256,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
   const int G = gridDim.x;
   int U;
   int4 st = make_int4(0, 0, 0, 0);
+  int* lens_s = reinterpret_cast<int*>(smem + p.part_off);  // [kKeptLens]
+  const bool kept = p.plan_in_kernel && p.B <= kKeptLens;
   if (p.plan_in_kernel) {
     // scan the units per sequence in the (still unused) ring stages
     int* cu_s = reinterpret_cast<int*>(ring.stages);  // [B + 1]
@@ -228,7 +265,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     const int nt = blockDim.x;
     for (int b = threadIdx.x; b < p.B; b += nt) {
       if (blockIdx.x == 0) attn::check_length(p, b);
-      cu_s[b] = attn::units_of(p, b);
+      const int L = attn::used_len(p, b);
+      if (kept) lens_s[b] = L;
+      cu_s[b] = p.n_groups * ((L + kBS - 1) / kBS);
     }
     __syncthreads();
     const int chunk = (p.B + nt - 1) / nt;
@@ -248,7 +287,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     const int r0 = attn::range_begin(blockIdx.x, U, G);
     if (r0 < attn::range_begin(blockIdx.x + 1, U, G)) {
       const int b = attn::seq_of_unit(cu_s, p.B, r0);
-      const int nblk = attn::walked_blocks(p, attn::used_len(p, b));
+      const int nblk = (cu_s[b + 1] - cu_s[b]) / p.n_groups;
       const int grp = (r0 - cu_s[b]) / nblk;
       st = make_int4(b, grp, (r0 - cu_s[b]) - grp * nblk, 0);
     }
@@ -266,12 +305,13 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
   const int r0 = attn::range_begin(blockIdx.x, U, G);
   const int r1 = attn::range_begin(blockIdx.x + 1, U, G);
   const int rows_per_group = p.hg_size * p.rep;
-  Cursor cur;
-  if (r0 < r1) cur.load(p, st);
+  Walk cur{p, kept ? lens_s : nullptr};
+  if (r0 < r1) cur.begin(st);
 
   if (warp == consumers) {
     // -------------------------------------------------------- producer
     if (elect_one()) {
+      const int nblk0 = cur.nblk;
       // (each block is read once: its lines leave L2 first)
       Producer pr{ring, &tm_k, &tm_v, p.num_blocks, p.err, tc::l2_evict_first_policy()};
       bool ok = true;
@@ -279,13 +319,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
         const int n = min(r1 - u, cur.nblk - cur.j);
         ok = pr.fetch_row(p.bt + int64_t(cur.b) * p.W + cur.j, n, cur.grp * p.hg_size * HD / width);
         u += n;
-        cur.advance(p, n);
+        cur.advance(n);
       }
       if (!ok) pr.drain();
       // the split group this CTA merges (read by the merge kernel)
       p.splits[blockIdx.x] =
-          r0 < r1 ? attn::split_entry(blockIdx.x, G, U, st.x, st.y, st.z,
-                                      attn::walked_blocks(p, attn::used_len(p, st.x)))
+          r0 < r1 ? attn::split_entry(blockIdx.x, G, U, st.x, st.y, st.z, nblk0)
                   : make_int4(-1, 0, 0, 0);
     }
   } else if (warp < consumers) {
@@ -343,7 +382,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
             [&](int r) -> float* { return p.ws_ml + (base + r) * 2; });
       }
       u += n;
-      cur.advance(p, n);
+      cur.advance(n);
     }
   }
 }
@@ -460,19 +499,21 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 template <typename T, int HD, int NT>
 struct DecodeFp8 {
   static int stage_bytes(int hg) { return 2 * kBS * hg * HD; }
+  // barriers, alignment slack and ring; what follows starts there
   static size_t smem_for(int hg, int nstages) {
     return kBarrierBytes + 1024 + size_t(nstages) * stage_bytes(hg);
   }
   // Ring depth: about 176 KB of stages per SM, shared by the CTAs of 8
-  // consumer warps in all (narrow groups: several CTAs per SM).
+  // consumer warps in all (narrow groups: several CTAs per SM, each with its
+  // barriers and kept lengths).
   static int ring_stages(int hg) {
     const int ctas = std::max(1, 8 / hg);
-    const int ns = 176 * 1024 / ctas / stage_bytes(hg);
+    const int ns = (176 - 4 * (ctas - 1)) * 1024 / ctas / stage_bytes(hg);
     return std::max(2, std::min(kMaxStages, ns));
   }
   static cudaError_t grid(const AttnArgs& a, int hg, int* G, size_t* smem, int* nstages, int* wave) {
     *nstages = ring_stages(hg);
-    *smem = smem_for(hg, *nstages);
+    *smem = smem_for(hg, *nstages) + kKeptLens * 4;
     static KernelSetup setup;
     int per_sm = 0;
     const cudaError_t e = kernel_setup(setup, decode_kernel<T, HD, NT>, static_cast<int>(*smem),
@@ -567,6 +608,7 @@ struct DecodeFp8 {
       e = cudaLaunchKernelEx(&cfg, decode_cluster_kernel<T, HD, NT>, tm_k, tm_v, p, sc, width);
       return e != cudaSuccess ? e : cudaGetLastError();
     }
+    p.part_off = static_cast<int>(smem_for(hg, p.nstages));  // the kept lengths
     // every CTA scans the lengths in its ring stages; larger batches have a
     // plan kernel
     p.plan_in_kernel = a.num_seqs <= kKernelPlanSeqs &&

@@ -62,6 +62,13 @@ __device__ __forceinline__ int window_seq(const int32_t* __restrict__ cu, int nu
   return x;
 }
 
+// Programmatic launch: this kernel may have started while the one before it
+// ends, and the next may start while it runs (and waits in the same way).
+__device__ __forceinline__ void pdl_begin() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 struct WriteParams {
   const uint8_t *k, *v;  // new rows
   uint8_t *k_pool, *v_pool;
@@ -205,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
   __shared__ int cnt_s[kWindow];
   __shared__ int4 run_s[kWindow];  // first token, tokens, offset in the block, block
   __shared__ int runs_s;
+  pdl_begin();
   const int t0 = blockIdx.x * kWindow;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = window_seq<kWindow>(p.cu, p.num_seqs, t0, cnt_s);
@@ -350,6 +358,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) kv_gather_fp8_kernel(const GatherParams p) {
   __shared__ int cnt_s[kGatherTokens];
   __shared__ int blk_s[kGatherTokens], off_s[kGatherTokens];
+  pdl_begin();
   const int t0 = blockIdx.x * kGatherTokens;
   const int n = min(kGatherTokens, p.total - t0);
   const int b = window_seq<kGatherTokens>(p.cu, p.num_seqs, t0, cnt_s);
@@ -435,12 +444,12 @@ template <typename T>
 static cudaError_t write_as(const WriteParams& p, dim3 grid, cudaStream_t stream) {
   // two units at once where 16 rows of a head are at most half of what a warp
   // holds, and blocks have no more rows than that
-  if (p.bs <= 16 && p.hd == 16) kv_write_fp8_kernel<T, 2, 2><<<grid, kThreads, 0, stream>>>(p);
-  else if (p.bs <= 16 && p.hd == 32) kv_write_fp8_kernel<T, 4, 2><<<grid, kThreads, 0, stream>>>(p);
-  else if (p.bs <= 16 && p.hd == 64) kv_write_fp8_kernel<T, 8, 2><<<grid, kThreads, 0, stream>>>(p);
-  else if (p.hd == 128) kv_write_fp8_kernel<T, 16, 1><<<grid, kThreads, 0, stream>>>(p);
-  else kv_write_fp8_kernel<T, 0, 1><<<grid, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  auto kern = kv_write_fp8_kernel<T, 0, 1>;
+  if (p.bs <= 16 && p.hd == 16) kern = kv_write_fp8_kernel<T, 2, 2>;
+  else if (p.bs <= 16 && p.hd == 32) kern = kv_write_fp8_kernel<T, 4, 2>;
+  else if (p.bs <= 16 && p.hd == 64) kern = kv_write_fp8_kernel<T, 8, 2>;
+  else if (p.hd == 128) kern = kv_write_fp8_kernel<T, 16, 1>;
+  return launch_pdl(kern, grid, kThreads, 0, stream, p);
 }
 
 cudaError_t launch_kv_write_fp8(const void* k, const void* v, int32_t dtype, const int32_t* bt,
@@ -510,11 +519,9 @@ cudaError_t launch_kv_gather_fp8(const void* k_pool, const void* v_pool, const f
   p.hd = pool.head_dim;
   const unsigned grid = static_cast<unsigned>((int64_t(total_tokens) + kGatherTokens - 1) /
                                               kGatherTokens);
-  if (dtype == PKV_F32)
-    kv_gather_fp8_kernel<float><<<grid, kThreads, 0, stream>>>(p);
-  else
-    kv_gather_fp8_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(dtype == PKV_F32 ? kv_gather_fp8_kernel<float>
+                                     : kv_gather_fp8_kernel<__nv_bfloat16>,
+                    dim3(grid), kThreads, 0, stream, p);
 }
 
 }  // namespace pkv

@@ -80,6 +80,24 @@ struct AttnArgs {
   int32_t* err;
 };
 
+// Launch `kern` so that it may start while the kernel before it in the stream
+// ends (it waits for that one's results itself, with griddepcontrol.wait).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem,
+                       cudaStream_t stream, const Args&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 enum : int32_t { kPlanInCall = 0, kPlanOnly = 1, kPlanned = 2 };
 
 // Decode support / sizing.

@@ -28,6 +28,8 @@ __global__ void __launch_bounds__((kPrefillWarps + 1) * 32, 1)
                    const __grid_constant__ CUtensorMap tm_v, const PrefillParams p,
                    const Scales sc) {
   extern __shared__ __align__(128) uint8_t smem[];
+  attn::pdl_wait();
+  attn::pdl_launch_dependents();
   const int b = blockIdx.z;
   const int g = blockIdx.y;
   const int q0 = __ldg(p.cu_q + b);
@@ -150,8 +152,8 @@ cudaError_t prefill_run(const AttnArgs& a, const Scales& sc, cudaStream_t stream
     ps.seq_lens += s0;
     ps.bt += int64_t(s0) * p.W;
     const dim3 grid(static_cast<unsigned>(tiles), pool.n_kv, ps.B);
-    prefill_kernel<T, HD><<<grid, threads, smem, stream>>>(tm_k, tm_v, ps, sc);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_pdl(prefill_kernel<T, HD>, grid, threads, smem, stream, tm_k, tm_v, ps, sc);
+    if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }

@@ -145,6 +145,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
 
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the preceding kernel's results
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // Work order, as in the bf16 prefill: with at most blockDim.x sequences, x
   // numbers the (sequence, KV head, tile pair) triples, sequences by
   // descending work and each one's pairs from the last (most keys) down;
@@ -758,8 +760,7 @@ cudaError_t run_tc(const AttnArgs& a, const float* k_scales, const float* v_scal
     p.cu_q = a.cu_q_lens + s0;
     const dim3 grid = p.ordered ? dim3(static_cast<unsigned>(slots), 1, 1)
                                 : dim3((a.max_q_len + qpp - 1) / qpp, pool.n_kv, p.B);
-    kern<<<grid, kThreads, Lay::REQUEST, stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_pdl(kern, grid, kThreads, Lay::REQUEST, stream, p)) != cudaSuccess) return e;
   }
   return cudaSuccess;
 }

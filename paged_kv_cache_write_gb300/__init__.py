@@ -486,10 +486,18 @@ def _ptr(t, name, dtype, index):
     return _dev(t, name, dtype)  # raises: it is not the type or layout asked for
 
 
-def _elsewhere(index):
-    """Whether another device than ``index`` is current (a call then repeats
-    itself with ``index`` current)."""
-    return torch.cuda.current_device() != index
+def _context(stream, index):
+    """What a call on a cache of device ``index`` has to run under (it then
+    repeats itself there), or None: the stream it was given, so that what it
+    allocates and reads belongs to that stream, or the cache's device."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = (torch.cuda.ExternalStream(int(stream), device=index) if int(stream)
+                      else torch.cuda.default_stream(index))
+        if stream.device_index != index:
+            raise ValueError(f"stream is on device {stream.device_index}, the cache on {index}")
+        return torch.cuda.stream(stream)
+    return None if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
 _TYPE_CODES = {torch.float32: PKV_F32, torch.bfloat16: PKV_BF16}
@@ -547,21 +555,22 @@ def kv_write_fp8(k, v, block_tables, seq_lens, cu_new_lens, k_pool, v_pool, k_sc
     rows are moved to it.
     """
     i, desc, kp, vp, ks, vs = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
+    there = _context(stream, i)
+    if there is not None:
+        with there:
+            return kv_write_fp8(k, v, block_tables, seq_lens, cu_new_lens, k_pool, v_pool,
+                                k_scales, v_scales, err=err)
     B, W = _batch(block_tables, seq_lens)
     shape = k.shape
     if len(shape) != 3 or shape != (shape[0], desc.n_kv, desc.head_dim) or v.shape != shape:
         raise ValueError("k, v must be [T, n_kv, head_dim] matching the pool")
-    if _elsewhere(i):
-        with torch.cuda.device(i):
-            return kv_write_fp8(k, v, block_tables, seq_lens, cu_new_lens, k_pool, v_pool,
-                                k_scales, v_scales, err=err, stream=stream)
     dt = k.dtype
     status = (_lib or _load()).pkv_kv_write_fp8(
         _ptr(k, "k", dt, i), _ptr(v, "v", dt, i), _type_code(dt),
         _ptr(block_tables, "block_tables", _int, i), W, _ptr(seq_lens, "seq_lens", _int, i),
         _offsets(cu_new_lens, "cu_new_lens", B, i), B, shape[0], kp, vp, ks, vs,
         ctypes.byref(desc), None if err is None else _ptr(err, "err", _int, i),
-        _raw_stream(i) if stream is None else _stream(stream))
+        _raw_stream(i))
     if status:
         raise PkvError("pkv_kv_write_fp8", status)
 
@@ -573,6 +582,12 @@ def kv_gather_fp8(k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, cu
     logical order, each value times its scale, in ``dtype`` (float32 or
     bfloat16; that of ``k_out`` / ``v_out`` where given)."""
     i, desc, kp, vp, ks, vs = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
+    there = _context(stream, i)
+    if there is not None:
+        with there:
+            return kv_gather_fp8(k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
+                                 cu_seq_lens, total_tokens, dtype=dtype, k_out=k_out,
+                                 v_out=v_out, err=err)
     B, W = _batch(block_tables, seq_lens)
     dt = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else dtype
     code = _type_code(dt)
@@ -583,17 +598,12 @@ def kv_gather_fp8(k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, cu
         v_out = torch.empty(shape, dtype=dt, device=k_pool.device)
     if k_out.shape != shape or v_out.shape != shape:
         raise ValueError(f"k_out, v_out must be {shape}")
-    if _elsewhere(i):
-        with torch.cuda.device(i):
-            return kv_gather_fp8(k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
-                                 cu_seq_lens, total_tokens, k_out=k_out, v_out=v_out, err=err,
-                                 stream=stream)
     status = (_lib or _load()).pkv_kv_gather_fp8(
         kp, vp, ks, vs, ctypes.byref(desc), _ptr(block_tables, "block_tables", _int, i), W,
         _ptr(seq_lens, "seq_lens", _int, i), _offsets(cu_seq_lens, "cu_seq_lens", B, i), B,
         shape[0], code, _ptr(k_out, "k_out", dt, i), _ptr(v_out, "v_out", dt, i),
         None if err is None else _ptr(err, "err", _int, i),
-        _raw_stream(i) if stream is None else _stream(stream))
+        _raw_stream(i))
     if status:
         raise PkvError("pkv_kv_gather_fp8", status)
     return k_out, v_out
@@ -627,6 +637,12 @@ def paged_attention_decode_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tabl
     bytes; calls that may run at the same time need a workspace each.
     """
     i, desc, kp, vp, ks, vs = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
+    there = _context(stream, i)
+    if there is not None:
+        with there:
+            return paged_attention_decode_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tables,
+                                              seq_lens, scale, max_seq_len, out=out,
+                                              workspace=workspace, max_ctas=max_ctas, err=err)
     B, W = _batch(block_tables, seq_lens)
     out, rows, H = _fp8_query(q, desc.head_dim, out)
     if rows != B:
@@ -636,12 +652,6 @@ def paged_attention_decode_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tabl
     if workspace is None:
         need = decode_fp8_workspace_bytes(B, H, desc.head_dim, max_seq_len, max_ctas)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    if _elsewhere(i):
-        with torch.cuda.device(i):
-            return paged_attention_decode_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tables,
-                                              seq_lens, scale, max_seq_len, out=out,
-                                              workspace=workspace, max_ctas=max_ctas, err=err,
-                                              stream=stream)
     dt = q.dtype
     status = (_lib or _load()).pkv_paged_attention_decode_fp8(
         _ptr(q, "q", dt, i), _type_code(dt), B, H, kp, vp, ks, vs, ctypes.byref(desc),
@@ -649,7 +659,7 @@ def paged_attention_decode_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tabl
         int(max_seq_len), float(scale), int(max_ctas), _ptr(out, "out", dt, i),
         _ptr(workspace, "workspace", workspace.dtype, i), workspace.nbytes,
         None if err is None else _ptr(err, "err", _int, i),
-        _raw_stream(i) if stream is None else _stream(stream))
+        _raw_stream(i))
     if status:
         raise PkvError("pkv_paged_attention_decode_fp8", status)
     return out
@@ -662,17 +672,18 @@ def paged_attention_prefill_fp8(q, cu_q_lens, k_pool, v_pool, k_scales, v_scales
     """Causal chunked-prefill attention [total_q, n_heads, head_dim] (float32
     or bfloat16) over the paged history of an 8-bit cache."""
     i, desc, kp, vp, ks, vs = _fp8_pool(k_pool, v_pool, k_scales, v_scales)
+    there = _context(stream, i)
+    if there is not None:
+        with there:
+            return paged_attention_prefill_fp8(q, cu_q_lens, k_pool, v_pool, k_scales, v_scales,
+                                               block_tables, seq_lens, scale, max_q_len,
+                                               max_seq_len, out=out, err=err)
     B, W = _batch(block_tables, seq_lens)
     out, rows, H = _fp8_query(q, desc.head_dim, out)
     if max_q_len is None:
         max_q_len = int((cu_q_lens[1:] - cu_q_lens[:-1]).max().item()) if B else 0
     if max_seq_len is None:
         max_seq_len = int(seq_lens.max().item()) if B else 0
-    if _elsewhere(i):
-        with torch.cuda.device(i):
-            return paged_attention_prefill_fp8(q, cu_q_lens, k_pool, v_pool, k_scales, v_scales,
-                                               block_tables, seq_lens, scale, max_q_len,
-                                               max_seq_len, out=out, err=err, stream=stream)
     dt = q.dtype
     status = (_lib or _load()).pkv_paged_attention_prefill_fp8(
         _ptr(q, "q", dt, i), _type_code(dt), _offsets(cu_q_lens, "cu_q_lens", B, i), B, rows,
@@ -680,7 +691,7 @@ def paged_attention_prefill_fp8(q, cu_q_lens, k_pool, v_pool, k_scales, v_scales
         _ptr(block_tables, "block_tables", _int, i), W, _ptr(seq_lens, "seq_lens", _int, i),
         int(max_seq_len), float(scale), _ptr(out, "out", dt, i),
         None if err is None else _ptr(err, "err", _int, i),
-        _raw_stream(i) if stream is None else _stream(stream))
+        _raw_stream(i))
     if status:
         raise PkvError("pkv_paged_attention_prefill_fp8", status)
     return out

@@ -34,6 +34,8 @@ pkv_status check_fp8(const void* q, int32_t dtype, int32_t num_seqs, int32_t n_h
   st = pkv::check_attention_args(q, num_seqs, n_heads, k_pool, v_pool, *shape, block_tables,
                                  max_blocks_per_seq, seq_lens, max_seq_len, scale, out);
   if (st != PKV_OK) return st;
+  // (positions are 32-bit)
+  if (int64_t(max_blocks_per_seq) * shape->block_size > INT32_MAX) return PKV_ERR_RANGE;
   if (num_seqs > 0 && (!k_scales || !v_scales)) return PKV_ERR_NULL;
   if (!aligned4(k_scales) || !aligned4(v_scales)) return PKV_ERR_ALIGN;
   if (!pkv::fp8_attention_supported(*shape, n_heads)) return PKV_ERR_UNSUPPORTED;

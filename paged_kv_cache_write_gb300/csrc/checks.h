@@ -40,6 +40,10 @@ inline pkv_status check_pool_fp8(const pkv_pool_desc* pool, PoolShape* out) {
   if (pool->num_blocks <= 0 || pool->block_size <= 0 || pool->n_kv <= 0 || pool->head_dim <= 0)
     return PKV_ERR_SHAPE;
   if (pool->head_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
+  // (the kernels count a token's elements, and a block's of one head, in 32 bits)
+  if ((int64_t)pool->n_kv * pool->head_dim > (1 << 26) ||
+      (int64_t)pool->block_size * pool->head_dim > INT32_MAX)
+    return PKV_ERR_RANGE;
   *out = PoolShape{pool->num_blocks, pool->block_size, pool->n_kv, pool->head_dim, pool->dtype};
   if ((int64_t)pool->num_blocks * pool->block_size > INT32_MAX) return PKV_ERR_RANGE;
   return PKV_OK;

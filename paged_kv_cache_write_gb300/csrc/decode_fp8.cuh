@@ -206,8 +206,8 @@ struct ScaleBatch {
   __device__ __forceinline__ void load(const Scales& sc, const DecodeParams& p, int id, int head) {
     const bool ok = id >= 0 && id < p.num_blocks;  // others are read as zeros
     const int64_t at = int64_t(ok ? id : 0) * p.n_kv + head;
-    ks = ok ? __ldg(sc.k + at) : 1.f;
-    vs = ok ? __ldg(sc.v + at) : 1.f;
+    ks = ok ? sc.k[at] : 1.f;
+    vs = ok ? sc.v[at] : 1.f;
   }
   __device__ __forceinline__ void settle() { lv = __log2f(vs); }
 };
@@ -523,7 +523,7 @@ struct DecodeFp8 {
     *wave = *G = sm_count() * per_sm;
     if (a.max_ctas > 0 && a.max_ctas < *G) *G = a.max_ctas;
     const int64_t max_units = int64_t(a.num_seqs) * (a.pool.n_kv / hg) *
-                              ((std::min(a.max_seq_len, a.max_blocks_per_seq * kBS) + kBS - 1) / kBS);
+                              ((int64_t(a.max_seq_len) + kBS - 1) / kBS);
     if (max_units < *G) *G = static_cast<int>(std::max<int64_t>(1, max_units));
     return cudaSuccess;
   }
@@ -548,7 +548,7 @@ struct DecodeFp8 {
     p.n_groups = pool.n_kv / hg;
     p.W = a.max_blocks_per_seq;
     p.num_blocks = pool.num_blocks;
-    p.max_len = std::min(a.max_seq_len, a.max_blocks_per_seq * kBS);
+    p.max_len = a.max_seq_len;  // (no more than the tables hold)
     p.max_seq_len = a.max_seq_len;
     p.head_dim = HD;
     p.elem_bytes = 1;
@@ -584,7 +584,7 @@ struct DecodeFp8 {
 
     // Latency-bound batches, by the rule of the bf16 decode: the longest
     // sequence at most 64 blocks and the clusters within two waves.
-    const int nmax = (p.max_len + kBS - 1) / kBS;
+    const int nmax = p.max_len / kBS + (p.max_len % kBS != 0);
     const int C = std::max(1, std::min(kMaxCluster, (nmax + 3) / 4));
     const int64_t ctas = int64_t(p.B) * p.n_groups * C;
     if (a.max_ctas == 0 && nmax <= 8 * kMaxCluster && ctas <= 2 * int64_t(wave)) {

@@ -15,6 +15,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "device.cuh"
 #include "fp8.cuh"
@@ -41,12 +42,13 @@ __device__ __forceinline__ int window_seq(const int32_t* __restrict__ cu, int nu
   const int tid = threadIdx.x;
   if (tid < N) cnt_s[tid] = 0;  // [0]: ends at or before t0; [i]: ends at t0 + i
   __syncthreads();
+  const int t1 = t0 + min(N, INT_MAX - t0);
   int before = 0;
 #pragma unroll 4
   for (int i = tid; i < num_seqs; i += kThreads) {
     const int end = __ldg(cu + i + 1);
     if (end <= t0) ++before;
-    else if (end < t0 + N) atomicAdd(cnt_s + (end - t0), 1);
+    else if (end < t1) atomicAdd(cnt_s + (end - t0), 1);
   }
   before = __reduce_add_sync(0xffffffffu, before);
   if ((tid & 31) == 0 && before > 0) atomicAdd(cnt_s, before);
@@ -63,7 +65,11 @@ __device__ __forceinline__ int window_seq(const int32_t* __restrict__ cu, int nu
 }
 
 // Programmatic launch: this kernel may have started while the one before it
-// ends, and the next may start while it runs (and waits in the same way).
+// ends, and the next may start while it runs (and waits in the same way).  The
+// cache, and tensors that another kernel of the library may have written, are
+// therefore read with ordinary loads, here and in the attention kernels:
+// read-only ones (__ldg) are for data that nothing changes while the kernel
+// runs, and this one may run, waiting, while those are written.
 __device__ __forceinline__ void pdl_begin() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -90,7 +96,7 @@ struct Vec8<__nv_bfloat16> {
   using Max = __nv_bfloat162;
   uint4 w;
   __device__ __forceinline__ void load(const uint8_t* p) {
-    w = __ldg(reinterpret_cast<const uint4*>(p));
+    w = *reinterpret_cast<const uint4*>(p);
   }
   __device__ __forceinline__ uint32_t word(int i) const {
     return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
@@ -118,8 +124,8 @@ struct Vec8<float> {
   using Max = float;
   float4 a, b;
   __device__ __forceinline__ void load(const uint8_t* p) {
-    a = __ldg(reinterpret_cast<const float4*>(p));
-    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
   }
   __device__ __forceinline__ float2 pair(int i) const {
     return i == 0 ? make_float2(a.x, a.y) : i == 1 ? make_float2(a.z, a.w)
@@ -230,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
         const int start = __ldg(p.cu + b), end = __ldg(p.cu + b + 1);
         const int L = __ldg(p.seq_lens + b);
         const int64_t pos = int64_t(L) - end + t;
-        if (L < 0 || start < 0 || end - start > L || end > p.num_tokens || pos < 0) {
+        if (start < 0 || t < start || t >= end || end > p.num_tokens || L < 0 || end - start > L) {
           report(p.err, PKV_DEVERR_LENGTH);
         } else if (pos / p.bs >= p.W) {
           report(p.err, PKV_DEVERR_TABLE_WIDTH);
@@ -422,7 +428,7 @@ __global__ void __launch_bounds__(kThreads) kv_gather_fp8_kernel(const GatherPar
 #pragma unroll
         for (int k = 0; k < kGatherRows; ++k) {
           w[k][q] = __ldcs(reinterpret_cast<const Load*>(src[k]) + c);
-          s[k][q] = __ldg(scale[k] + h);
+          s[k][q] = scale[k][h];
         }
       }
 #pragma unroll

@@ -45,7 +45,7 @@ __global__ void __launch_bounds__((kPrefillWarps + 1) * 32, 1)
   if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0) {
     if (L < c || L < 0) report(p.err, PKV_DEVERR_LENGTH);
     else if (L > p.max_len)
-      report(p.err, L > p.W * kBS ? PKV_DEVERR_TABLE_WIDTH : PKV_DEVERR_LENGTH);
+      report(p.err, L > int64_t(p.W) * kBS ? PKV_DEVERR_TABLE_WIDTH : PKV_DEVERR_LENGTH);
   }
   if (L > p.max_len) L = p.max_len;
   if (L < c) return;  // inconsistent chunk: reported above, nothing computed
@@ -128,7 +128,7 @@ cudaError_t prefill_run(const AttnArgs& a, const Scales& sc, cudaStream_t stream
   p.rep = a.n_heads / pool.n_kv;
   p.W = a.max_blocks_per_seq;
   p.num_blocks = pool.num_blocks;
-  p.max_len = std::min(a.max_seq_len, a.max_blocks_per_seq * kBS);
+  p.max_len = a.max_seq_len;  // (no more than the tables hold)
   p.total_q = a.total_q;
   p.scale_log2 = a.scale * attn::kLog2e;
   p.queries_per_warp = kPrefillRows / p.rep;

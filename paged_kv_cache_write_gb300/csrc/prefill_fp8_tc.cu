@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0 && i0 == 0 && g == 0) {
     if (L < c || L < 0) report(p.err, PKV_DEVERR_LENGTH);
     else if (L > p.max_len)
-      report(p.err, L > p.W * kBlk ? PKV_DEVERR_TABLE_WIDTH : PKV_DEVERR_LENGTH);
+      report(p.err, L > int64_t(p.W) * kBlk ? PKV_DEVERR_TABLE_WIDTH : PKV_DEVERR_LENGTH);
   }
   if (L > p.max_len) L = p.max_len;
   if (L < c) return;
@@ -325,10 +325,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int blk = max(id, 0);
       const uint8_t* src = ((u & 4) ? p.v_pool : p.k_pool) + int64_t(blk) * (kBlk * pitch) + lane_off;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) x[i] = __ldg(reinterpret_cast<const uint4*>(src + i * step_off));
+      for (int i = 0; i < NV; ++i) x[i] = *reinterpret_cast<const uint4*>(src + i * step_off);
       if (!(u & 4)) {
-        ks = __ldg(p.k_scales + int64_t(blk) * p.n_kv + g);
-        vs = __ldg(p.v_scales + int64_t(blk) * p.n_kv + g);
+        ks = p.k_scales[int64_t(blk) * p.n_kv + g];
+        vs = p.v_scales[int64_t(blk) * p.n_kv + g];
       }
     };
     const int w = warp - kLoadWarp0;
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const Row o = row_of((s0 + i) * RG + lane / RL);
-          u[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (o.qi >= 0 ? o.off : 0)) + lane % RL);
+          u[i] = reinterpret_cast<const uint4*>(p.q + (o.qi >= 0 ? o.off : 0))[lane % RL];
           if (o.qi < 0) u[i] = make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
@@ -750,7 +750,7 @@ cudaError_t run_tc(const AttnArgs& a, const float* k_scales, const float* v_scal
   p.rep = rep;
   p.W = a.max_blocks_per_seq;
   p.num_blocks = pool.num_blocks;
-  p.max_len = std::min(a.max_seq_len, a.max_blocks_per_seq * kBlk);
+  p.max_len = a.max_seq_len;  // (no more than the tables hold)
   p.total_q = a.total_q;
   p.q_per_tile = kRows / rep;
   p.scale_log2 = a.scale * kLog2e;

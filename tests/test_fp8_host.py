@@ -234,3 +234,13 @@ def test_binding_refuses_mismatched_tensors(pkv):
         w(k, k, bt, sl.cpu(), cu, kp, kp, sc, sc)
     with pytest.raises(ValueError, match="head_dim"):
         pkv.paged_attention_decode_fp8(q.cuda(), kp, kp, sc, sc, bt, sl, 0.1, 1)
+
+
+def test_refusals_of_extents_past_32_bits(pkv):
+    """Extents that the kernels count in 32 bits, one past what they hold."""
+    for call in (_write, _gather):
+        assert call(pkv, desc=_desc(pkv, n_kv=(1 << 20) + 1)) == 5
+        assert call(pkv, desc=_desc(pkv, num_blocks=1, block_size=1 << 25)) == 5
+    for call in (_decode, _prefill):
+        assert call(pkv, W=1 << 27) == 5
+        assert call(pkv, desc=_desc(pkv, n_kv=(1 << 20) + 1), H=(1 << 20) + 1) == 5

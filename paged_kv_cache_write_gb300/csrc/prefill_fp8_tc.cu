@@ -90,7 +90,7 @@ struct TcParams {
   const int32_t* cu_q;
   __nv_bfloat16* out;
   int32_t* err;
-  int B, n_heads, n_kv, rep, W, num_blocks, max_len, total_q, q_per_tile;
+  int B, n_heads, n_kv, rep, rep_inv, W, num_blocks, max_len, total_q, q_per_tile;
   int ordered;
   float scale_log2;
 };
@@ -158,8 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (p.ordered) {
     const int t = threadIdx.x;
     int64_t* work_s = reinterpret_cast<int64_t*>(smem + Lay::V_OFF);
-    int* seq_s = reinterpret_cast<int*>(work_s + p.B);  // [B] sequence of each rank
-    int* pairs_s = seq_s + p.B;                         // [B] pairs of each rank
+    int* pairs_s = reinterpret_cast<int*>(work_s + p.B);
     const int qpp = 2 * p.q_per_tile;
     int64_t wt = 0;
     int pt = 0;
@@ -169,29 +168,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       wt = cs * (2 * Ls - cs + 1);
       pt = cs > 0 ? static_cast<int>((cs + qpp - 1) / qpp) : 0;
       work_s[t] = wt;
+      pairs_s[t] = pt;
     }
     if (t == 0) order_s = -1;
     __syncthreads();
-    int rank = 0;
-    if (t < p.B) {
+    if (t < p.B) {  // the sequence's first slot: the (head, pair) slots of the heavier ones
+      int64_t first = 0;
       for (int s = 0; s < p.B; ++s) {
         const int64_t ws = work_s[s];
-        rank += (ws > wt) || (ws == wt && s < t);
+        if (ws > wt || (ws == wt && s < t)) first += pairs_s[s];
       }
-      seq_s[rank] = t;
-      pairs_s[rank] = pt;
-    }
-    __syncthreads();
-    if (t < p.B) {  // rank t's first slot: the (head, pair) slots of the heavier ranks
-      int64_t first = 0;
-      for (int r = 0; r < t; ++r) first += pairs_s[r];
       const int64_t x = blockIdx.x;
-      const int64_t lo = first * p.n_kv, n = int64_t(pairs_s[t]) * p.n_kv;
+      const int64_t lo = first * p.n_kv, n = int64_t(pt) * p.n_kv;
       if (x >= lo && x < lo + n) {
         const int off = static_cast<int>(x - lo);
-        order_s = seq_s[t];
-        head_s = off / pairs_s[t];
-        pair_s = pairs_s[t] - 1 - (off - (off / pairs_s[t]) * pairs_s[t]);
+        order_s = t;
+        head_s = off / pt;
+        pair_s = pt - 1 - (off - (off / pt) * pt);
       }
     }
     __syncthreads();
@@ -490,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A row's 16-byte vectors of q (and of out) are RL = HD / 8 lanes' work: the
     // warp goes through its rows 32 / RL at a time, so that memory is touched
     // row by row (with every lane at a row of its own, 32 lines a load, one tile
-    // of 64 tokens took 12.7 us in place of 9.7).  Row `m` of the warp: its query,
+    // of 64 tokens took 3 us longer).  Row `m` of the warp: its query,
     // or -1, and its first element; read from shared memory where it is needed,
     // so that it takes no registers in between.
     constexpr int RL = HD / 8, RG = 32 / RL, STEPS = 32 / RG;
@@ -501,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto row_of = [&](int m) {
       const int* job = job_s;
       const int rr = (warp & 3) * 32 + m;
-      const int q = rr / p.rep;
+      const int q = (rr * p.rep_inv) >> 16;  // rr / p.rep
       const int qi = job[0] + x * p.q_per_tile + q;
       const bool active = q < p.q_per_tile && qi < job[1];
       return Row{active ? qi : -1,
@@ -518,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Row me = row_of(lane);
       last = me.qi >= 0 ? L - c + me.qi : INT_MAX;  // a row without a query is never masked
       cut = __reduce_min_sync(0xffffffffu, last);
-#pragma unroll 1
+#pragma unroll
       for (int s0 = 0; s0 < STEPS; s0 += 8) {
         uint4 u[8];
 #pragma unroll
@@ -748,6 +741,7 @@ cudaError_t run_tc(const AttnArgs& a, const float* k_scales, const float* v_scal
   p.n_heads = a.n_heads;
   p.n_kv = pool.n_kv;
   p.rep = rep;
+  p.rep_inv = (65536 + rep - 1) / rep;  // (exact for rows < 128 of rep <= 16)
   p.W = a.max_blocks_per_seq;
   p.num_blocks = pool.num_blocks;
   p.max_len = a.max_seq_len;  // (no more than the tables hold)

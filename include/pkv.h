@@ -18,8 +18,9 @@
  * pkv_paged_attention_decode_noalloc (decode without a caller workspace),
  * the 8-bit cache (pkv_kv_write_fp8, pkv_kv_gather_fp8,
  * pkv_paged_attention_decode_fp8, pkv_paged_attention_prefill_fp8: e4m3 pools
- * with a scale per block and KV head), the workspace size queries, pkv_status_string, pkv_abi_version and
- * pkv_selftest_bounded_wait (the kernels' bounded-wait failure path).
+ * with a scale per block and KV head), the workspace size queries,
+ * pkv_status_string, pkv_abi_version and pkv_selftest_bounded_wait (the
+ * kernels' bounded-wait failure path).
  *
  * Sources of the operations (page title, section):
  *   - "Build a Mini vLLM: Paged KV Cache and Continuous Batching From
@@ -509,11 +510,14 @@ pkv_status pkv_paged_attention_decode_noalloc(const void* q, int32_t num_seqs, i
  * prefill to bf16).
  *
  * head_dim must be a multiple of 16 (attention: 16, 32, 64 or 128, with
- * block_size 16).  `dtype` is the type of k, v, q and the outputs (PKV_F32
- * or PKV_BF16).  A block is copied on write with two pkv_copy_blocks calls:
- * one on the pools described as bf16 with head_dim / 2 (the bytes are copied
- * as they are), one on the scales described as fp32 blocks of one token,
- * one head and head_dim n_kv (n_kv a multiple of 4).
+ * block_size 16), n_kv * head_dim at most 2^26, and block_size * head_dim and
+ * max_blocks_per_seq * block_size below 2^31 (PKV_ERR_RANGE).  `dtype` is the
+ * type of k, v, q and the outputs (PKV_F32 or PKV_BF16).
+ *
+ * A block is copied on write with two pkv_copy_blocks calls: one on the pools
+ * described as bf16 with head_dim / 2 (the bytes are copied as they are), one
+ * on the scales described as fp32 blocks of one token, one head and head_dim
+ * n_kv (n_kv a multiple of 4).
  */
 
 /*
@@ -599,6 +603,11 @@ pkv_status pkv_paged_attention_decode_fp8(const void* q, int32_t dtype, int32_t 
  * paged history (the chunk's own K/V written with pkv_kv_write_fp8 first).
  * A key or value that a query may not see does not reach its output, NaN
  * included.  It needs no workspace.
+ *
+ * Scores, softmax sums and outputs are held in fp32.  For bf16 queries,
+ * weights are rounded to 11 significand bits before they multiply V, those
+ * below 2^-18 of the row's largest (times their value scales) to fewer; for
+ * fp32 queries and weights keep 22.
  *
  *   q, out      [total_q, n_heads, head_dim] of `dtype`, 16-byte aligned
  *   everything else as for pkv_paged_attention_prefill; supported shapes as

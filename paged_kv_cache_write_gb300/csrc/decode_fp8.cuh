@@ -12,6 +12,13 @@
 // a stage at 8 heads of 128); one consumer warp per KV head.  Block ids and
 // scales are gathered by the consumer warps, 32 blocks at a time and a batch
 // ahead of use, so their latency is off the path.
+//
+// Measured, bf16 queries, where a plain copy reaches 6.79 TB/s: 256 sequences
+// of 2,040 - 2,048 tokens, 8 KV heads: head_dim 128 163 us (6.6 TB/s), 64 98 us
+// (5.5 TB/s), 32 81 us (3.3 TB/s: the consumers' conversions and products, the
+// same for any width, bound narrow heads).  64 sequences of 512 - 2,048 tokens
+// of 8 x 64 (81 MB) 25 us, of which 13.5 stream; the rest is the plan (2 us),
+// the first scales and tile (2 us) and the merge launch (5 us).
 #pragma once
 
 #include "attention.cuh"

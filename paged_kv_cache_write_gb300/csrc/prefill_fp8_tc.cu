@@ -37,6 +37,18 @@
 //               loads straight from the pool, each warp's next two blocks on
 //               their way, e4m3 -> f16 in registers, 128-byte-swizzled tiles
 //               in four-stage rings.
+// Two row tiles a CTA, because they share the conversion of K and V: CTAs of one
+// row tile, two on an SM, took 381 us for 214 (32 heads on 8, 4 chunks of 512
+// after 2,048 - 8,192 tokens of head_dim 128).
+//
+// Measured: 4 chunks of 512 after 0 - 4,096 tokens, 64 heads of 128 on 8,
+// 160 us (930 TFLOP/s); 2 chunks of 2,048 ending at 8,192, 829 us (1,161);
+// head_dim 64, 32 heads on 8, 4 chunks of 1,024 ending at 4,096, 233 us (516).
+// Bound by the softmax warps, some 1,800 cycles a key tile of 64 (MMAs: 1,330 at
+// head_dim 128), and by 10,000 cycles of each CTA that are not its loop: work
+// order 2,500, set-up 500, queries 3,000 - 6,000, first scores 1,500, output
+// 2,000 - 4,000.
+//
 // 16 warps leave 128 registers a thread, and no loop may spill: with 200 KB of
 // shared memory little L1 is left, and a reload from local memory costs an L2
 // round trip.

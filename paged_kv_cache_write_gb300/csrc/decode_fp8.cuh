@@ -5,7 +5,7 @@
 // Bound by reading the cache: 2 x n_kv x head_dim bytes a token, 8 bytes of
 // scales per block and head.  The work split is that of the bf16 decode, since
 // what it is for is the same: a persistent grid over equal contiguous ranges
-// of (sequence, head group, block) units, a merge kernel for the groups that
+// of (sequence, head group, block) units, a joining kernel for the groups that
 // several CTAs share, and one thread-block cluster per (sequence, head group)
 // for batches too small to stream.  A producer lane fetches whole blocks of the
 // group's heads with TMA (16 tokens x hg heads x head_dim bytes, K and V: 32 KB
@@ -17,8 +17,9 @@
 // of 2,040 - 2,048 tokens, 8 KV heads: head_dim 128 163 us (6.6 TB/s), 64 98 us
 // (5.5 TB/s), 32 81 us (3.3 TB/s: the consumers' conversions and products, the
 // same for any width, bound narrow heads).  64 sequences of 512 - 2,048 tokens
-// of 8 x 64 (81 MB) 25 us, of which 13.5 stream; the rest is the plan (2 us),
-// the first scales and tile (2 us) and the merge launch (5 us).
+// of 8 x 64 (81 MB) 24 us, of which 13.5 stream; the rest is the plan (2 us),
+// the first scales and tile (2 us) and the joining launch (3 us, 1.2 of which an
+// empty one would take too).
 #pragma once
 
 #include "attention.cuh"
@@ -501,6 +502,72 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
   cluster_sync();  // the peers have read this CTA's partials
 }
 
+// Joins the split group that CTA x of the decode merges: its parts' outputs
+// weighted by 2^(M - max M) l, one float4 of the group's rows a thread.  As the
+// bf16 decode's merge, but a group's rows lie over several small CTAs (y), which
+// fit an SM beside a decode's CTA (this call's, and the next one's, which is
+// there early): 64 sequences of 512 - 2,048 tokens of 8 x 128, 32 heads, take
+// 33.4 us in place of 35.4, of 8 x 64 24.1 in place of 24.9.
+constexpr int kJoinThreads = 128;
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p) {
+  constexpr int NB = 4;  // parts in flight
+  attn::pdl_launch_dependents();
+  attn::pdl_wait();  // the decode's partials and split entries
+  const int4 sp = __ldcg(p.splits + blockIdx.x);
+  if (sp.x < 0) return;
+  const int rows = p.hg_size * p.rep;
+  const int E = rows * HD;  // elements of a part
+  const int e = (blockIdx.y * blockDim.x + threadIdx.x) * 4;
+  if (e >= E) return;
+  const bool c0_tail = (sp.y & attn::kSplitC0Tail) != 0;
+  const bool dense = (sp.y & attn::kSplitDense) != 0;
+  const int U = dense ? 0 : __ldcg(p.total_units);  // only sparse grids look at range starts
+  const int G = p.grid;
+  const int c0 = sp.z & 0xffff, c1 = static_cast<int>(static_cast<uint32_t>(sp.z) >> 16);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float M = -INFINITY, den = 0.f;
+  for (int cs = c0; cs <= c1; cs += NB) {
+    float4 o[NB];
+    float2 ml[NB];
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int c = cs + k;
+      o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (c <= c1 && (dense || attn::range_begin(c + 1, U, G) > attn::range_begin(c, U, G))) {
+        // c0 holds the group's first units at the end of its range, unless its
+        // range starts at the group
+        const int64_t slot = 2 * c + (c == c0 && c0_tail ? 1 : 0);
+        o[k] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + slot * E + e));
+        ml[k] = __ldcg(reinterpret_cast<const float2*>(p.ws_ml + (slot * rows + e / HD) * 2));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      if (ml[k].y > 0.f) {  // a part that saw no key has no weight
+        const float Mn = fmaxf(M, ml[k].x);
+        const float a = fast_exp2(M - Mn);
+        const float w = fast_exp2(ml[k].x - Mn) * ml[k].y;
+        acc = make_float4(fmaf(w, o[k].x, acc.x * a), fmaf(w, o[k].y, acc.y * a),
+                          fmaf(w, o[k].z, acc.z * a), fmaf(w, o[k].w, acc.w * a));
+        den = fmaf(den, a, w);
+        M = Mn;
+      }
+    }
+  }
+  const int64_t row0 = int64_t(sp.x) * p.n_heads + (sp.y & 0xffff) * rows;
+  T* out = static_cast<T*>(p.out) + row0 * HD + e;
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const float4 v = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(out) = v;
+  } else {
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  }
+}
+
 // --------------------------------------------------------------- host side
 
 template <typename T, int HD, int NT>
@@ -628,8 +695,12 @@ struct DecodeFp8 {
     cfg.dynamicSmemBytes = smem;
     e = cudaLaunchKernelEx(&cfg, decode_kernel<T, HD, NT>, tm_k, tm_v, p, sc, width);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(G);
-    e = attn::launch_merge<T, HD>(cfg, p);
+    const int vecs = hg * p.rep * HD / 4;  // of a group's rows
+    const int threads = std::min(kJoinThreads, (vecs + 31) / 32 * 32);
+    cfg.gridDim = dim3(G, (vecs + threads - 1) / threads);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, join_kernel<T, HD>, p);
     return e != cudaSuccess ? e : cudaGetLastError();
   }
 };

@@ -42,7 +42,7 @@
 // after 2,048 - 8,192 tokens of head_dim 128).
 //
 // Measured: 4 chunks of 512 after 0 - 4,096 tokens, 64 heads of 128 on 8,
-// 160 us (930 TFLOP/s); 2 chunks of 2,048 ending at 8,192, 829 us (1,161);
+// 158 us (940 TFLOP/s); 2 chunks of 2,048 ending at 8,192, 829 us (1,161);
 // head_dim 64, 32 heads on 8, 4 chunks of 1,024 ending at 4,096, 233 us (516).
 // Bound by the softmax warps, some 1,800 cycles a key tile of 64 (MMAs: 1,330 at
 // head_dim 128), and by 10,000 cycles of each CTA that are not its loop: work
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // descending work and each one's pairs from the last (most keys) down;
   // otherwise z, y, x in the natural order.  Work values are staged in the
   // (still unused) V stages.
-  __shared__ int order_s, pair_s, head_s, job_s[4];
+  __shared__ int order_s, pair_s, head_s, seq_s[3], job_s[4];  // seq_s: cu_q of both ends, length
   int g = blockIdx.y;
   int b = blockIdx.z, pair = blockIdx.x;
   if (p.ordered) {
@@ -173,10 +173,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* pairs_s = reinterpret_cast<int*>(work_s + p.B);
     const int qpp = 2 * p.q_per_tile;
     int64_t wt = 0;
-    int pt = 0;
+    int pt = 0, at = 0, end = 0, len = 0;
     if (t < p.B) {
-      const int64_t cs = int64_t(__ldg(p.cu_q + t + 1)) - __ldg(p.cu_q + t);
-      const int64_t Ls = min(__ldg(p.seq_lens + t), p.max_len);
+      at = __ldg(p.cu_q + t);
+      end = __ldg(p.cu_q + t + 1);
+      len = __ldg(p.seq_lens + t);
+      const int64_t cs = int64_t(end) - at;
+      const int64_t Ls = min(len, p.max_len);
       wt = cs * (2 * Ls - cs + 1);
       pt = cs > 0 ? static_cast<int>((cs + qpp - 1) / qpp) : 0;
       work_s[t] = wt;
@@ -186,6 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (t < p.B) {  // the sequence's first slot: the (head, pair) slots of the heavier ones
       int64_t first = 0;
+#pragma unroll 8
       for (int s = 0; s < p.B; ++s) {
         const int64_t ws = work_s[s];
         if (ws > wt || (ws == wt && s < t)) first += pairs_s[s];
@@ -195,6 +199,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (x >= lo && x < lo + n) {
         const int off = static_cast<int>(x - lo);
         order_s = t;
+        seq_s[0] = at;
+        seq_s[1] = end;
+        seq_s[2] = len;
         head_s = off / pt;
         pair_s = pt - 1 - (off - (off / pt) * pt);
       }
@@ -204,16 +211,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     b = order_s;
     g = head_s;
     pair = pair_s;
+  } else {
+    if (threadIdx.x == 0) {
+      seq_s[0] = __ldg(p.cu_q + b);
+      seq_s[1] = __ldg(p.cu_q + b + 1);
+      seq_s[2] = __ldg(p.seq_lens + b);
+    }
+    __syncthreads();
   }
-  const int q0 = __ldg(p.cu_q + b);
-  const int c = __ldg(p.cu_q + b + 1) - q0;
+  const int q0 = seq_s[0];
+  const int c = seq_s[1] - q0;
   const int i0 = pair * 2 * p.q_per_tile;  // first query of tile A
   if (i0 >= c) return;                     // idle CTA: leave before any barrier or TMEM use
   if (q0 < 0 || int64_t(q0) + c > p.total_q) {
     if (threadIdx.x == 0 && i0 == 0 && g == 0) report(p.err, PKV_DEVERR_LENGTH);
     return;
   }
-  int L = __ldg(p.seq_lens + b);
+  int L = seq_s[2];
   if (threadIdx.x == 0 && i0 == 0 && g == 0) {
     if (L < c || L < 0) report(p.err, PKV_DEVERR_LENGTH);
     else if (L > p.max_len)
@@ -717,12 +731,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
+      const int first = job_s[0] + x * p.q_per_tile;  // the tile's first query
+      const int nq = min(p.q_per_tile, job_s[1] - first);
+      const int q_step = (p.n_heads - p.rep) * HD;
+      __nv_bfloat16* tile_out =
+          p.out + (int64_t(job_s[2] + first) * p.n_heads + job_s[3] * p.rep) * HD;
 #pragma unroll 4
       for (int i = 0; i < STEPS; ++i) {
         const int m = i * RG + lane / RL;
-        const Row o = row_of(m);
-        if (o.qi >= 0)
-          reinterpret_cast<uint4*>(p.out + o.off)[lane % RL] =
+        const int rr = (warp & 3) * 32 + m;
+        const int q = (rr * p.rep_inv) >> 16;
+        if (q < nq)
+          reinterpret_cast<uint4*>(tile_out + int64_t(q) * q_step + rr * HD)[lane % RL] =
               *reinterpret_cast<const uint4*>(q_at(m, lane % RL));
       }
     }

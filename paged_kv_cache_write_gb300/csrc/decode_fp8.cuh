@@ -14,10 +14,10 @@
 // ahead of use, so their latency is off the path.
 //
 // Measured, bf16 queries, where a plain copy reaches 6.79 TB/s: 256 sequences
-// of 2,040 - 2,048 tokens, 8 KV heads: head_dim 128 163 us (6.6 TB/s), 64 98 us
-// (5.5 TB/s), 32 81 us (3.3 TB/s: the consumers' conversions and products, the
+// of 2,040 - 2,048 tokens, 8 KV heads: head_dim 128 163 us (6.6 TB/s), 64 88 us
+// (6.1 TB/s), 32 57 us (4.8 TB/s), 16 49 us (2.8 TB/s: the consumers' chains, the
 // same for any width, bound narrow heads).  64 sequences of 512 - 2,048 tokens
-// of 8 x 64 (81 MB) 24 us, of which 13.5 stream; the rest is the plan (2 us),
+// of 8 x 64 (81 MB) 22 us, of which 12 stream; the rest is the plan (2 us),
 // the first scales and tile (2 us) and the joining launch (3 us, 1.2 of which an
 // empty one would take too).
 #pragma once
@@ -249,8 +249,17 @@ __device__ __forceinline__ bool take_tiles(RowsT& rows, const Ring& ring, RingPo
   return true;
 }
 
+// CTAs of 8 consumer warps that an SM's registers hold.  A warp is a chain of
+// latencies (tile, scores, maximum, weights, product), some 900 cycles a block
+// whatever the head's width, and HBM brings a block of 8 x 64 in 720: narrow
+// heads run on two CTAs an SM, with half the ring each, at 96 registers (more
+// query rows or fp32's second terms would spill).  256 sequences of 2,048 tokens,
+// 8 KV heads: head_dim 64 97.4 -> 88.2 us, 32 80.8 -> 56.8, 16 71.5 -> 49.2.
 template <typename T, int HD, int NT>
-__global__ void __launch_bounds__(kMaxThreads, 1)
+constexpr int kCtasPerSm = NT == 1 && HD * int(sizeof(T)) / 2 <= 64 ? 2 : 1;
+
+template <typename T, int HD, int NT, int CTAS>
+__global__ void __launch_bounds__(kMaxThreads, CTAS)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const DecodeParams p, const Scales sc, const int width) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -572,36 +581,45 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p
 
 template <typename T, int HD, int NT>
 struct DecodeFp8 {
+  static constexpr int kSmemMax = 226 * 1024;  // what both kernels opt in to
   static int stage_bytes(int hg) { return 2 * kBS * hg * HD; }
   // barriers, alignment slack and ring; what follows starts there
   static size_t smem_for(int hg, int nstages) {
     return kBarrierBytes + 1024 + size_t(nstages) * stage_bytes(hg);
   }
+  // 2: CTAs for twice 8 consumer warps an SM.  Not for groups whose rows are not
+  // whole 128 bytes, whose copies are twice as many: 256 sequences of 2,048
+  // tokens, 9 heads on 3 of 64, take 52.4 us so and 49.3 with one CTA's registers.
+  static int doubled(int hg) { return tile_width(hg, HD) == 128 ? kCtasPerSm<T, HD, NT> : 1; }
+  static auto kernel(int hg) {
+    return doubled(hg) == 2 ? decode_kernel<T, HD, NT, kCtasPerSm<T, HD, NT>>
+                            : decode_kernel<T, HD, NT, 1>;
+  }
   // Ring depth: about 176 KB of stages per SM, shared by the CTAs of 8
   // consumer warps in all (narrow groups: several CTAs per SM, each with its
   // barriers and kept lengths).
   static int ring_stages(int hg) {
-    const int ctas = std::max(1, 8 / hg);
+    const int ctas = std::max(1, 8 / hg) * doubled(hg);
     const int ns = (176 - 4 * (ctas - 1)) * 1024 / ctas / stage_bytes(hg);
     return std::max(2, std::min(kMaxStages, ns));
   }
   static cudaError_t grid(const AttnArgs& a, int hg, int* G, size_t* smem, int* nstages, int* wave) {
     *nstages = ring_stages(hg);
     *smem = smem_for(hg, *nstages) + kKeptLens * 4;
-    static KernelSetup setup;
+    static KernelSetup setup[2];
     int per_sm = 0;
-    const cudaError_t e = kernel_setup(setup, decode_kernel<T, HD, NT>, static_cast<int>(*smem),
-                                       (hg + 1) * 32, &per_sm);
+    const cudaError_t e = kernel_setup(setup[doubled(hg) - 1], kernel(hg), static_cast<int>(*smem),
+                                       (hg + 1) * 32, &per_sm, kSmemMax);
     if (e != cudaSuccess) return e;
     per_sm = std::max(1, std::min(per_sm, 16));  // 16: what the workspace is sized for
-    *wave = *G = sm_count() * per_sm;
+    *G = sm_count() * per_sm;
+    *wave = *G / doubled(hg);
     if (a.max_ctas > 0 && a.max_ctas < *G) *G = a.max_ctas;
     const int64_t max_units = int64_t(a.num_seqs) * (a.pool.n_kv / hg) *
                               ((int64_t(a.max_seq_len) + kBS - 1) / kBS);
     if (max_units < *G) *G = static_cast<int>(std::max<int64_t>(1, max_units));
     return cudaSuccess;
   }
-  static constexpr int kClusterSmemMax = 226 * 1024;
 
   static cudaError_t run(const AttnArgs& a, const Scales& sc, cudaStream_t stream) {
     const PoolShape& pool = a.pool;
@@ -666,10 +684,10 @@ struct DecodeFp8 {
       p.nstages = std::max(2, std::min(p.nstages, (nmax + C - 1) / C));
       const size_t rows = size_t(hg) * p.rep;
       const size_t extra = rows * HD * 4 + (rows * 2 * 4 + 15) / 16 * 16;
-      while (p.nstages > 2 && smem_for(hg, p.nstages) + extra > size_t(kClusterSmemMax)) --p.nstages;
+      while (p.nstages > 2 && smem_for(hg, p.nstages) + extra > size_t(kSmemMax)) --p.nstages;
       p.part_off = static_cast<int>(smem_for(hg, p.nstages));
       static KernelSetup setup;
-      e = kernel_setup(setup, decode_cluster_kernel<T, HD, NT>, kClusterSmemMax, (hg + 1) * 32,
+      e = kernel_setup(setup, decode_cluster_kernel<T, HD, NT>, kSmemMax, (hg + 1) * 32,
                        nullptr);
       if (e != cudaSuccess) return e;
       attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -693,7 +711,7 @@ struct DecodeFp8 {
     }
     cfg.gridDim = dim3(G);
     cfg.dynamicSmemBytes = smem;
-    e = cudaLaunchKernelEx(&cfg, decode_kernel<T, HD, NT>, tm_k, tm_v, p, sc, width);
+    e = cudaLaunchKernelEx(&cfg, kernel(hg), tm_k, tm_v, p, sc, width);
     if (e != cudaSuccess) return e;
     const int vecs = hg * p.rep * HD / 4;  // of a group's rows
     const int threads = std::min(kJoinThreads, (vecs + 31) / 32 * 32);

@@ -2,6 +2,7 @@
 // and occupancy), so repeated calls do not repeat driver queries.
 #pragma once
 
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 
@@ -24,8 +25,12 @@ struct KernelSetup {
 // Opt `kern` into `smem` bytes of dynamic shared memory on the current
 // device and report its resident CTAs per SM for `threads` threads
 // (per_sm may be null).  Driver calls happen once per device and size.
+// optin: shared memory to opt in to where it is not `smem` (a kernel launched
+// with several sizes opts in to the largest: threads of the host that launch
+// it at the same time would else take each other's opt-in back).
 template <typename Kern>
-cudaError_t kernel_setup(KernelSetup& ks, Kern kern, int smem, int threads, int* per_sm) {
+cudaError_t kernel_setup(KernelSetup& ks, Kern kern, int smem, int threads, int* per_sm,
+                         int optin = 0) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -37,7 +42,8 @@ cudaError_t kernel_setup(KernelSetup& ks, Kern kern, int smem, int threads, int*
       return cudaSuccess;
     }
   }
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           std::max(smem, optin));
   if (e != cudaSuccess) return e;
   int occ = 0;
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, threads, smem);

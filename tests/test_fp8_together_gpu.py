@@ -278,3 +278,47 @@ def test_prefill_longer_than_it_was_told():
                                                0.1, 2, 40, err=bt.err)
         assert np.array_equal(f64(good[2:]), f64(out[2:]))
         bt.no_error()
+
+
+def test_calls_from_two_threads():
+    """Two host threads, each with shapes of its own that the same kernels are
+    launched with in different sizes."""
+    import threading
+    shapes = [(8, 8, 64), (9, 3, 64), (6, 2, 64), (5, 1, 64)]
+    batches = [Batch([1500, 700, 30], n_kv=kv, head_dim=hd, seed=i)
+               for i, (_, kv, hd) in enumerate(shapes)]
+    qs, alone = [], []
+    for bt, (heads, _, _) in zip(batches, shapes):
+        bt.fill()
+        qs.append(bt.queries(3, heads))
+        alone.append(bt.decode(qs[-1]))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(mine):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for i in range(150):
+                    for j in mine:
+                        out = batches[j].pkv.paged_attention_decode_fp8(
+                            d_q[j], *batches[j].cache, batches[j].bt, lens[j],
+                            1.0 / np.sqrt(batches[j].hd), 1500, err=batches[j].err)
+                    if i % 50 == 49:
+                        torch.cuda.current_stream().synchronize()
+                        if not torch.equal(out, alone[mine[-1]]):
+                            bad.append((mine, i))
+        except Exception as e:  # noqa: BLE001 (reported below)
+            bad.append(e)
+
+    d_q = [guarded_copy(q) for q in qs]
+    lens = [ints([1500, 700, 30]) for _ in shapes]
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(m,)) for m in ([0, 1], [2, 3])]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not bad, bad
+    for bt in batches:
+        bt.no_error()

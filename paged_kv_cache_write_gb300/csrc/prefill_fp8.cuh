@@ -9,7 +9,7 @@
 // the consumers' conversions and products: each warp turns the block's e4m3
 // values into f16 for itself.  Measured, 4 chunks of 256 at the end of 1,000
 // tokens, 32 heads on 8: fp32 94 us at head_dim 64 (78 TFLOP/s) and 163 us at
-// 128, bf16 58 us at head_dim 32.
+// 128, bf16 46 us at head_dim 32.
 #pragma once
 
 #include "attention.cuh"
@@ -24,8 +24,13 @@ constexpr int kPrefillWarps = 8;
 constexpr int kPrefillTiles = 2;  // row tiles of 8 per warp
 constexpr int kPrefillRows = 8 * kPrefillTiles;
 
-template <typename T, int HD>
-__global__ void __launch_bounds__((kPrefillWarps + 1) * 32, 1)
+// CTAS: that an SM's registers hold.  Two, at 96 registers, hide each other's
+// latencies, but each is slower: for bf16 (narrow heads), where there are more CTAs
+// than SMs (4 chunks of 256 at the end of 1,000 tokens, 32 heads of 32 on 8: 46.4
+// us in place of 58.5; 6 chunks of 37, 8 heads of 16 on 4: 9.5 and 8.9).  fp32
+// would spill (4 chunks as above, heads of 128: 251 us for 163).
+template <typename T, int HD, int CTAS>
+__global__ void __launch_bounds__((kPrefillWarps + 1) * 32, CTAS)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const PrefillParams p,
                    const Scales sc) {
@@ -139,13 +144,24 @@ cudaError_t prefill_run(const AttnArgs& a, const Scales& sc, cudaStream_t stream
   CUtensorMap tm_k{}, tm_v{};
   if (!encode_tiles(&tm_k, a.k_pool, pool, HD, 1) || !encode_tiles(&tm_v, a.v_pool, pool, HD, 1))
     return cudaErrorInvalidValue;
-  static KernelSetup setup;
-  const int threads = (kPrefillWarps + 1) * 32;
-  cudaError_t e = kernel_setup(setup, prefill_kernel<T, HD>, static_cast<int>(smem), threads, nullptr);
-  if (e != cudaSuccess) return e;
   const int tile_q = kPrefillWarps * p.queries_per_warp;
   const int64_t tiles = (int64_t(a.max_q_len) + tile_q - 1) / tile_q;
   if (tiles == 0 || a.num_seqs == 0) return cudaSuccess;
+  auto kern = prefill_kernel<T, HD, 1>;
+  int ctas = 1;
+  if constexpr (sizeof(T) == 2) {
+    // CTAs with work: each sequence may have one tile that is not full
+    const int64_t busy =
+        std::min(tiles * a.num_seqs, int64_t(a.total_q) / tile_q + a.num_seqs) * pool.n_kv;
+    if (busy > sm_count()) {
+      kern = prefill_kernel<T, HD, 2>;
+      ctas = 2;
+    }
+  }
+  static KernelSetup setup[2];
+  const int threads = (kPrefillWarps + 1) * 32;
+  cudaError_t e = kernel_setup(setup[ctas - 1], kern, static_cast<int>(smem), threads, nullptr);
+  if (e != cudaSuccess) return e;
   // the grid's y and z extents are 16-bit: long batches go in slices
   for (int s0 = 0; s0 < a.num_seqs; s0 += 65535) {
     PrefillParams ps = p;
@@ -154,7 +170,7 @@ cudaError_t prefill_run(const AttnArgs& a, const Scales& sc, cudaStream_t stream
     ps.seq_lens += s0;
     ps.bt += int64_t(s0) * p.W;
     const dim3 grid(static_cast<unsigned>(tiles), pool.n_kv, ps.B);
-    e = launch_pdl(prefill_kernel<T, HD>, grid, threads, smem, stream, tm_k, tm_v, ps, sc);
+    e = launch_pdl(kern, grid, threads, smem, stream, tm_k, tm_v, ps, sc);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -39,6 +39,7 @@ namespace fp8 {
 
 constexpr int kBS = 16;
 constexpr float kWeightLog2 = 15.f;  // log2 of the largest weight
+constexpr float kSumStep = 100.f;    // the sum is scaled by at most 2^-100 at once
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                               uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -290,7 +291,7 @@ struct Rows {
           for (int e = 0; e < 4; ++e)
             if (j0 + nb * kBS + tok_k + (e >> 1) * 8 > last[nt][e & 1]) w[nb][nt][e] = -INFINITY;
     }
-    float alpha[NT][2];
+    float d[NT][2], sum[NT][2];  // d: log2 of the factor on what came before
     bool moved = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -304,32 +305,43 @@ struct Rows {
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
         const float mn = fmaxf(m[nt][j], mx);
         const float ref = mn == -INFINITY ? 0.f : mn;  // nothing visible yet
-        alpha[nt][j] = fast_exp2(m[nt][j] - ref);
+        d[nt][j] = m[nt][j] - ref;
         moved |= mn != m[nt][j];
         m[nt][j] = mn;
-        float sum = 0.f;
+        sum[nt][j] = 0.f;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           const float p0 = fast_exp2(w[nb][nt][j] - (ref - kWeightLog2));
           const float p1 = fast_exp2(w[nb][nt][2 + j] - (ref - kWeightLog2));
-          sum += p0 + p1;
+          sum[nt][j] += p0 + p1;
           w[nb][nt][j] = p0 * vs[nb];
           w[nb][nt][2 + j] = p1 * vs[nb];
         }
-        l[nt][j] = l[nt][j] * alpha[nt][j] + sum;
       }
-    // the outputs are rescaled only when some row's maximum moved
+    // The outputs are rescaled only when some row's maximum moved.  The sum's
+    // factor is applied in two steps: 2^d underflows where a block's value scale
+    // is some 2^100 times the earlier ones', whose keys then still count in l
+    // (their weights p are as large as their scales are small).
     if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        const float a0 = fast_exp2(d[nt][0]), a1 = fast_exp2(d[nt][1]);
 #pragma unroll
         for (int i = 0; i < KK; ++i) {
-          o[nt][i][0] *= alpha[nt][0];
-          o[nt][i][1] *= alpha[nt][1];
-          o[nt][i][2] *= alpha[nt][0];
-          o[nt][i][3] *= alpha[nt][1];
+          o[nt][i][0] *= a0;
+          o[nt][i][1] *= a1;
+          o[nt][i][2] *= a0;
+          o[nt][i][3] *= a1;
         }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) l[nt][j] *= fast_exp2(fminf(d[nt][j] + kSumStep, 0.f));
+      }
     }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        l[nt][j] = l[nt][j] * fast_exp2(fmaxf(d[nt][j], -kSumStep)) + sum[nt][j];
     // V rows past the sequence's end hold whatever the pool holds there
     if (valid < NB * kBS) {
 #pragma unroll
@@ -484,8 +496,11 @@ struct Rows {
   }
 
   // Partial result of every row: normalised output (fp32), the reference of
-  // its sum in log2 units and the sum.  A NaN sum is passed on as NaN outputs
-  // with a sum of 1, so that a merge that drops parts without weight keeps it.
+  // its sum in log2 units and the sum.  A sum far from 1, as value scales far
+  // from 1 make it, hands its exponent to the reference: the difference of two
+  // parts' references is then that of what they weigh, and does not underflow in
+  // a merge for a part that counts.  A NaN sum is passed on as NaN outputs with a
+  // sum of 1, so that a merge that drops parts without weight keeps it.
   template <typename PartRow, typename MlRow>
   __device__ __forceinline__ void store_partial(PartRow part_row, MlRow ml_row) {
     reduce_sums();
@@ -509,8 +524,10 @@ struct Rows {
         store_f32(pp + g * DB, x);
         if (g == 0) {
           float* ml = ml_row(r);
-          ml[0] = bad ? 0.f : m[nt][j];
-          ml[1] = bad ? 1.f : l[nt][j];
+          int e = static_cast<int>(__float_as_uint(l[nt][j]) >> 23) - 127;
+          if (abs(e) <= 40 || l[nt][j] == 0.f) e = 0;
+          ml[0] = bad ? 0.f : m[nt][j] + static_cast<float>(e);
+          ml[1] = bad ? 1.f : l[nt][j] * pow2f(-e);
         }
       }
   }

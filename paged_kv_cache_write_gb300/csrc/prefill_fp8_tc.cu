@@ -602,6 +602,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float factor[4] = {fmaxf(rs * k4.x, 1.2e-38f), fmaxf(rs * k4.y, 1.2e-38f),
                                fmaxf(rs * k4.z, 1.2e-38f), fmaxf(rs * k4.w, 1.2e-38f)};
       const float shift[4] = {l4.x, l4.y, l4.z, l4.w}, inv_vs[4] = {i4.x, i4.y, i4.z, i4.w};
+      // A weight w is flushed 2^126 below 1, and counts in the sum as w / vs: beside
+      // a value scale 2^80 times its own (up to 2^60) a key's share could be lost.
+      // Tiles with such a scale take their sums from the scores, without scales.
+      const bool far = fminf(fminf(l4.x, l4.y), fminf(l4.z, l4.w)) < -20.f;
       const int pos0 = j * kTileKeys;
       tc::tmem_wait_ld();
       if (pos0 + kTileKeys - 1 > cut) {  // keys past some row's causal limit
@@ -609,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < kTileKeys; ++k)
           if (pos0 + k > last) v[k] = __float_as_uint(-INFINITY);
       }
-      float alpha = 1.f, add = 0.f;
+      float d = 0.f, add = 0.f;  // d: log2 of the factor on what came before
       bool move = j == 0;     // set the reference to the maximum
       bool rescale = false;   // some row of the warp moved its reference
 #pragma unroll 1
@@ -624,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx = fmaxf(mx, fmaf(mb, factor[bk], shift[bk]));
           }
           const float m_new = fmaxf(m_used, mx);
-          alpha = m_new > m_used ? fast_exp2(m_used - m_new) : 1.f;
+          if (m_new > m_used) d = m_used - m_new;
           m_used = m_new;
         }
         rescale = pass > 0;
@@ -654,10 +658,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc::tmem_st16(s_addr + ch * 16, pk);
         }
+        if (far) {
+          add = 0.f;
+#pragma unroll
+          for (int k = 0; k < kTileKeys; ++k)
+            add += fast_exp2(fmaf(__uint_as_float(v[k]), factor[k / 16], -mref));
+        }
         move = most > kWeightMax;
         if (!__any_sync(0xffffffffu, move)) break;
       }
-      l_sum = l_sum * alpha + add;
+      // (2^d in two steps: it underflows where a value scale is some 2^100 times the
+      // earlier ones, whose keys' share of the sum then still counts)
+      l_sum = l_sum * fast_exp2(fminf(d + 100.f, 0.f)) * fast_exp2(fmaxf(d, -100.f)) + add;
       if (rescale && j > 0) {
         // O_X has to hold all products before this tile's.  S_{j+1} was computed
         // after them; only the last tiles have a barrier for it of their own.
@@ -669,6 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc::fence_after_sync();
+        const float alpha = fast_exp2(d);
         const float2 a2 = make_float2(alpha, alpha);
 #pragma unroll 1
         for (int ch = 0; ch < HD / 32; ++ch) {

@@ -556,7 +556,9 @@ pkv_status pkv_kv_write_fp8(const void* k, const void* v, int32_t dtype,
 
 /*
  * pkv_kv_gather_fp8 - read an 8-bit cache back: pkv_kv_gather with every
- * value times its scale, in `dtype`.
+ * value times its scale, in `dtype`.  The outputs may be blocks of a bf16 or
+ * fp32 pool: no later kernel starts before they are written, a planned decode
+ * of that pool included.
  */
 pkv_status pkv_kv_gather_fp8(const void* k_pool, const void* v_pool, const float* k_scales,
                              const float* v_scales, const pkv_pool_desc* pool,

@@ -69,13 +69,13 @@ __device__ __forceinline__ int window_seq(const int32_t* __restrict__ cu, int nu
 }
 
 // Programmatic launch: this kernel may have started while the one before it
-// ends, and the next may start while it runs (and waits in the same way).  The
-// cache, and tensors that another kernel of the library may have written, are
-// therefore read with ordinary loads, here and in the attention kernels:
-// read-only ones (__ldg) are for data that nothing changes while the kernel
-// runs, and this one may run, waiting, while those are written.
-__device__ __forceinline__ void pdl_begin() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+// ends.  The cache, and tensors that another kernel of the library may have
+// written, are therefore read with ordinary loads, here and in the attention
+// kernels: read-only ones (__ldg) are for data that nothing changes while the
+// kernel runs, and this one may run, waiting, while those are written.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The next kernel may start while this one runs (and waits in the same way).
+__device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
@@ -222,7 +222,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
   __shared__ int cnt_s[kWindow];
   __shared__ int4 run_s[kWindow];  // first token, tokens, offset in the block, block
   __shared__ int runs_s;
-  pdl_begin();
+  pdl_wait();
+  pdl_launch_dependents();
   const int t0 = blockIdx.x * kWindow;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = window_seq<kWindow>(p.cu, p.num_seqs, t0, cnt_s);
@@ -368,7 +369,9 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) kv_gather_fp8_kernel(const GatherParams p) {
   __shared__ int cnt_s[kGatherTokens];
   __shared__ int blk_s[kGatherTokens], off_s[kGatherTokens];
-  pdl_begin();
+  // The next kernel is not let in early: a planned decode of the bf16 cache reads
+  // its first K/V before it waits, and these outputs may be that cache's blocks.
+  pdl_wait();
   const int t0 = blockIdx.x * kGatherTokens;
   const int n = min(kGatherTokens, p.total - t0);
   const int b = window_seq<kGatherTokens>(p.cu, p.num_seqs, t0, cnt_s);

@@ -54,6 +54,18 @@ inline int head_group(int n_kv) {
   return best;
 }
 
+// attn::used_len and attn::check_length by ordinary loads: these kernels start
+// while the lengths may still be written (see kv_fp8.cu's pdl_wait).
+__device__ __forceinline__ int length_of(const DecodeParams& p, int b) {
+  return max(0, min(p.seq_lens[b], p.max_len));
+}
+
+__device__ __forceinline__ void report_bad_length(const DecodeParams& p, int b) {
+  const int L = p.seq_lens[b];
+  if (L < 0 || L > p.max_seq_len) report(p.err, PKV_DEVERR_LENGTH);
+  else if (L > p.W * kBS) report(p.err, PKV_DEVERR_TABLE_WIDTH);
+}
+
 // Lengths that a CTA which plans for itself keeps in shared memory (larger
 // batches read them again where they are needed).
 constexpr int kKeptLens = 1024;
@@ -66,7 +78,7 @@ struct Walk {
   int b = 0, grp = 0, j = 0, L = 0, nblk = 1;
 
   __device__ __forceinline__ void enter() {
-    L = lens != nullptr ? lens[b] : attn::used_len(p, b);
+    L = lens != nullptr ? lens[b] : length_of(p, b);
     nblk = (L + kBS - 1) / kBS;
   }
   __device__ __forceinline__ void begin(int4 st) {
@@ -157,13 +169,13 @@ struct Producer {
     constexpr int kGroup = 8;
     int id[kGroup], next[kGroup];
 #pragma unroll
-    for (int i = 0; i < kGroup; ++i) next[i] = i < n ? __ldg(row + i) : 0;
+    for (int i = 0; i < kGroup; ++i) next[i] = i < n ? row[i] : 0;
     for (int k0 = 0; k0 < n; k0 += kGroup) {
 #pragma unroll
       for (int i = 0; i < kGroup; ++i) id[i] = next[i];
 #pragma unroll
       for (int i = 0; i < kGroup; ++i)
-        next[i] = k0 + kGroup + i < n ? __ldg(row + k0 + kGroup + i) : 0;
+        next[i] = k0 + kGroup + i < n ? row[k0 + kGroup + i] : 0;
       if (*ring.abort_flag) return false;
 #pragma unroll
       for (int i = 0; i < kGroup; ++i) {
@@ -281,8 +293,8 @@ __global__ void __launch_bounds__(kMaxThreads, CTAS)
     int* warp_tot = cu_s + p.B + 1;                   // [32]
     const int nt = blockDim.x;
     for (int b = threadIdx.x; b < p.B; b += nt) {
-      if (blockIdx.x == 0) attn::check_length(p, b);
-      const int L = attn::used_len(p, b);
+      if (blockIdx.x == 0) report_bad_length(p, b);
+      const int L = length_of(p, b);
       if (kept) lens_s[b] = L;
       cu_s[b] = p.n_groups * ((L + kBS - 1) / kBS);
     }
@@ -360,7 +372,7 @@ __global__ void __launch_bounds__(kMaxThreads, CTAS)
       const int last = cur.L - 1;
       // block ids a batch of 32 ahead of the scales, scales a batch ahead of use
       const int32_t* row = p.bt + int64_t(b) * p.W + cur.j;
-      auto id_at = [&](int i) { return i < n ? __ldg(row + i) : -1; };
+      auto id_at = [&](int i) { return i < n ? row[i] : -1; };
       ScaleBatch now, next;
       next.load(sc, p, id_at(lane), kv_head);
       int ids = id_at(32 + lane);
@@ -430,12 +442,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
   attn::pdl_wait();
   attn::pdl_launch_dependents();
   const int32_t* trow = p.bt + int64_t(b) * p.W;
-  const int L = attn::used_len(p, b);
+  const int L = length_of(p, b);
   const int nblk = (L + kBS - 1) / kBS;
   const int j0 = rank * nblk / C, j1 = (rank + 1) * nblk / C;
   if (blockIdx.x == 0 && threadIdx.x == 0)
     p.total_units[1] = -1;  // a call planning for itself replaces any kept plan
-  if (rank == 0 && grp == 0 && threadIdx.x == 0) attn::check_length(p, b);
+  if (rank == 0 && grp == 0 && threadIdx.x == 0) report_bad_length(p, b);
 
   if (warp == consumers) {
     if (elect_one()) {
@@ -448,7 +460,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     const int head0 = kv_head * p.rep;
     // scales of blocks j0 + lane (j1 - j0 <= 8)
     ScaleBatch now;
-    now.load(sc, p, j0 + lane < j1 ? __ldg(trow + j0 + lane) : -1, kv_head);
+    now.load(sc, p, j0 + lane < j1 ? trow[j0 + lane] : -1, kv_head);
     Rows<T, HD, NT, false> rows;
     rows.place(width, warp);
     rows.begin(

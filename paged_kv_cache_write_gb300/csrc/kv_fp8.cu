@@ -41,7 +41,7 @@ constexpr int kHeld = 8;     // 8-element vectors that a lane holds
 // One pass over the offsets with every load in flight, not a chain of
 // dependent ones.
 template <int N>
-__device__ __forceinline__ int window_seq(const int32_t* __restrict__ cu, int num_seqs, int t0,
+__device__ __forceinline__ int window_seq(const int32_t* cu, int num_seqs, int t0,
                                           int* cnt_s) {
   const int tid = threadIdx.x;
   if (tid < N) cnt_s[tid] = 0;  // [0]: ends at or before t0; [i]: ends at t0 + i
@@ -50,7 +50,7 @@ __device__ __forceinline__ int window_seq(const int32_t* __restrict__ cu, int nu
   int before = 0;
 #pragma unroll 4
   for (int i = tid; i < num_seqs; i += kThreads) {
-    const int end = __ldg(cu + i + 1);
+    const int end = cu[i + 1];
     if (end <= t0) ++before;
     else if (end < t1) atomicAdd(cnt_s + (end - t0), 1);
   }
@@ -69,10 +69,11 @@ __device__ __forceinline__ int window_seq(const int32_t* __restrict__ cu, int nu
 }
 
 // Programmatic launch: this kernel may have started while the one before it
-// ends.  The cache, and tensors that another kernel of the library may have
-// written, are therefore read with ordinary loads, here and in the attention
-// kernels: read-only ones (__ldg) are for data that nothing changes while the
-// kernel runs, and this one may run, waiting, while those are written.
+// ends.  Everything that it reads may still be written then, by a kernel of the
+// library or of the caller: lengths, offsets and tables as well as the cache.  Here
+// and in the attention kernels all of it is read with ordinary loads, after the
+// wait: read-only ones (__ldg) are for data that nothing changes while the kernel
+// runs, and may be moved before the wait.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // The next kernel may start while this one runs (and waits in the same way).
 __device__ __forceinline__ void pdl_launch_dependents() {
@@ -238,8 +239,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
       if (b >= p.num_seqs) {
         report(p.err, PKV_DEVERR_LENGTH);  // offsets that stop short of the token count
       } else {
-        const int start = __ldg(p.cu + b), end = __ldg(p.cu + b + 1);
-        const int L = __ldg(p.seq_lens + b);
+        const int start = p.cu[b], end = p.cu[b + 1];
+        const int L = p.seq_lens[b];
         const int64_t pos = int64_t(L) - end + t;
         if (start < 0 || t < start || t >= end || end > p.num_tokens || L < 0 || end - start > L) {
           report(p.err, PKV_DEVERR_LENGTH);
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
           const int off = static_cast<int>(pos % p.bs);
           begins = t == start || off == 0;
           if (begins) {
-            const int blk = __ldg(p.bt + int64_t(b) * p.W + pos / p.bs);
+            const int blk = p.bt[int64_t(b) * p.W + pos / p.bs];
             if (blk < 0 || blk >= p.num_blocks) {
               report(p.err, PKV_DEVERR_BLOCK_ID);
               begins = false;
@@ -382,13 +383,13 @@ __global__ void __launch_bounds__(kThreads) kv_gather_fp8_kernel(const GatherPar
       if (b >= p.num_seqs) {
         report(p.err, PKV_DEVERR_LENGTH);
       } else {
-        const int pos = t0 + i - __ldg(p.cu + b);
-        if (pos < 0 || pos >= __ldg(p.seq_lens + b)) {
+        const int pos = t0 + i - p.cu[b];
+        if (pos < 0 || pos >= p.seq_lens[b]) {
           report(p.err, PKV_DEVERR_LENGTH);
         } else if (pos / p.bs >= p.W) {
           report(p.err, PKV_DEVERR_TABLE_WIDTH);
         } else {
-          blk = __ldg(p.bt + int64_t(b) * p.W + pos / p.bs);
+          blk = p.bt[int64_t(b) * p.W + pos / p.bs];
           off = pos % p.bs;
           if (blk < 0 || blk >= p.num_blocks) {
             report(p.err, PKV_DEVERR_BLOCK_ID);

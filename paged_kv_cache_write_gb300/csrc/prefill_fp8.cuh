@@ -39,8 +39,8 @@ __global__ void __launch_bounds__((kPrefillWarps + 1) * 32, CTAS)
   attn::pdl_launch_dependents();
   const int b = blockIdx.z;
   const int g = blockIdx.y;
-  const int q0 = __ldg(p.cu_q + b);
-  const int c = __ldg(p.cu_q + b + 1) - q0;
+  const int q0 = p.cu_q[b];
+  const int c = p.cu_q[b + 1] - q0;
   const int tile_q = kPrefillWarps * p.queries_per_warp;
   const int i0 = blockIdx.x * tile_q;
   if (i0 >= c) return;  // whole CTA idle: exit before touching barriers
@@ -48,7 +48,7 @@ __global__ void __launch_bounds__((kPrefillWarps + 1) * 32, CTAS)
     if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0) report(p.err, PKV_DEVERR_LENGTH);
     return;
   }
-  int L = __ldg(p.seq_lens + b);
+  int L = p.seq_lens[b];
   if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0) {
     if (L < c || L < 0) report(p.err, PKV_DEVERR_LENGTH);
     else if (L > p.max_len)
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__((kPrefillWarps + 1) * 32, CTAS)
     DecodeParams dp{};  // what a scale batch needs of the pool
     dp.num_blocks = p.num_blocks;
     dp.n_kv = p.n_kv;
-    auto id_at = [&](int i) { return i < n_blocks ? __ldg(row + i) : -1; };
+    auto id_at = [&](int i) { return i < n_blocks ? row[i] : -1; };
     ScaleBatch now, next;
     next.load(sc, dp, id_at(lane), g);
     int ids = id_at(32 + lane);

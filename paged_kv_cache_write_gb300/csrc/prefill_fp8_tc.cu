@@ -175,9 +175,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t wt = 0;
     int pt = 0, at = 0, end = 0, len = 0;
     if (t < p.B) {
-      at = __ldg(p.cu_q + t);
-      end = __ldg(p.cu_q + t + 1);
-      len = __ldg(p.seq_lens + t);
+      at = p.cu_q[t];
+      end = p.cu_q[t + 1];
+      len = p.seq_lens[t];
       const int64_t cs = int64_t(end) - at;
       const int64_t Ls = min(len, p.max_len);
       wt = cs * (2 * Ls - cs + 1);
@@ -213,9 +213,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     pair = pair_s;
   } else {
     if (threadIdx.x == 0) {
-      seq_s[0] = __ldg(p.cu_q + b);
-      seq_s[1] = __ldg(p.cu_q + b + 1);
-      seq_s[2] = __ldg(p.seq_lens + b);
+      seq_s[0] = p.cu_q[b];
+      seq_s[1] = p.cu_q[b + 1];
+      seq_s[2] = p.seq_lens[b];
     }
     __syncthreads();
   }
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto id_of = [&](int u) {
       const int jb = (u >> 3) * kBlocks + (u & 3);
       int id = -1;
-      if (u < n_units && jb < n_blocks_seq) id = __ldg(row + jb);
+      if (u < n_units && jb < n_blocks_seq) id = row[jb];
       return id;
     };
     uint4 d[kAhead][NV];

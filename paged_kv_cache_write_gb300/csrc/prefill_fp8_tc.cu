@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int put_lo = half * Lay::KV_HALF + r0 * 128 + ((at ^ r0) << 4);
     const int put_hi = half * Lay::KV_HALF + r0 * 128 + (((at + 1) ^ r0) << 4);
     const int n_units = 2 * kBlocks * n_tiles;
-    // -1: nothing there, or a bad id
+    // -1: the sequence has no block there
     auto id_of = [&](int u) {
       const int jb = (u >> 3) * kBlocks + (u & 3);
       int id = -1;
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (unconditional loads, of block 0 where there is none, so that they stay
     // in flight: a selected load is waited for where it is issued)
     auto fetch = [&](uint4 (&x)[NV], float& ks, float& vs, int& id, int u) {
-      if (id >= p.num_blocks || id < -1) id = -2;  // reported when it is stored
+      if (id >= p.num_blocks || id < 0) id = -1;
       const int blk = max(id, 0);
       const uint8_t* src = ((u & 4) ? p.v_pool : p.k_pool) + int64_t(blk) * (kBlk * pitch) + lane_off;
 #pragma unroll
@@ -381,8 +381,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // The scales of tile j - 8 are no longer read: K stage j was free, so
           // S_{j-4} is complete, which was issued once W_{j-6} was there.
           const int o = (j % kScaleStages) * kBlocks + bi;
-          if (id_d[k] == -2) report(p.err, PKV_DEVERR_BLOCK_ID);
           const bool good = id_d[k] >= 0;
+          if (!good && pos0 < L) report(p.err, PKV_DEVERR_BLOCK_ID);  // (a block that it holds)
           ks_s[o] = good ? sk[k] : 1.f;
           lv_s[o] = good ? __log2f(sv[k]) : 0.f;
           iv_s[o] = good ? __fdividef(1.f, sv[k]) : 1.f;

@@ -19,8 +19,8 @@
  * the 8-bit cache (pkv_kv_write_fp8, pkv_kv_gather_fp8,
  * pkv_paged_attention_decode_fp8, pkv_paged_attention_prefill_fp8: e4m3 pools
  * with a scale per block and KV head), the workspace size queries,
- * pkv_status_string, pkv_abi_version and pkv_selftest_bounded_wait (the
- * kernels' bounded-wait failure path).
+ * pkv_status_string, pkv_abi_version, pkv_selftest_bounded_wait and
+ * pkv_selftest_bounded_wait_fp8 (the kernels' bounded-wait failure path).
  *
  * Sources of the operations (page title, section):
  *   - "Build a Mini vLLM: Paged KV Cache and Continuous Batching From
@@ -639,6 +639,15 @@ pkv_status pkv_paged_attention_prefill_fp8(
  *   err_word  device int32, required (PKV_ERR_NULL)
  */
 pkv_status pkv_selftest_bounded_wait(int32_t polls, int32_t* err_word, void* stream);
+
+/*
+ * pkv_selftest_bounded_wait_fp8 - the same for the waits of the 8-bit
+ * kernels, which a whole warp gives up together: a warp half of whose lanes
+ * wait for a phase that nothing completes.  The timeout bit is set if every
+ * lane then learns of it, and later waits end at once.  `polls` as above,
+ * each of at most 0.1 ms.
+ */
+pkv_status pkv_selftest_bounded_wait_fp8(int32_t polls, int32_t* err_word, void* stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */

@@ -27,6 +27,7 @@ __all__ = [
     "paged_attention_prefill", "status_string", "abi_version", "paged_attention_decode_noalloc",
     "selftest_bounded_wait", "PKV_FP8_E4M3", "kv_write_fp8", "kv_gather_fp8",
     "decode_fp8_workspace_bytes", "paged_attention_decode_fp8", "paged_attention_prefill_fp8",
+    "selftest_bounded_wait_fp8",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -102,6 +103,8 @@ def _load():
     L.pkv_paged_attention_prefill.restype = _i32
     L.pkv_paged_attention_prefill.argtypes = [_p, _p, _i32, _i32, _i32, _i32, _p, _p, _desc, _p,
                                               _i32, _p, _i32, _f, _p, _p, _sz, _p, _p]
+    L.pkv_selftest_bounded_wait_fp8.restype = _i32
+    L.pkv_selftest_bounded_wait_fp8.argtypes = [_i32, _p, _p]
     L.pkv_kv_write_fp8.restype = _i32
     L.pkv_kv_write_fp8.argtypes = [_p, _p, _i32, _p, _i32, _p, _p, _i32, _i32, _p, _p, _p, _p, _desc,
                                    _p, _p]
@@ -695,3 +698,10 @@ def paged_attention_prefill_fp8(q, cu_q_lens, k_pool, v_pool, k_scales, v_scales
     if status:
         raise PkvError("pkv_paged_attention_prefill_fp8", status)
     return out
+
+
+def selftest_bounded_wait_fp8(err, polls: int = 64, *, stream=None):
+    """:func:`selftest_bounded_wait` for the 8-bit kernels' waits, which a whole
+    warp gives up together."""
+    _check("pkv_selftest_bounded_wait_fp8", _load().pkv_selftest_bounded_wait_fp8(
+        int(polls), _dev(err, "err", torch.int32), _stream(stream)))

@@ -181,4 +181,12 @@ pkv_status pkv_paged_attention_prefill_fp8(
   return from_cuda(pkv::launch_prefill_fp8(a, dtype, k_scales, v_scales, as_stream(stream)));
 }
 
+pkv_status pkv_selftest_bounded_wait_fp8(int32_t polls, int32_t* err_word, void* stream) {
+  PKV_NVTX_RANGE("pkv_selftest_bounded_wait_fp8");
+  if (polls < 1) return PKV_ERR_RANGE;
+  if (!err_word) return PKV_ERR_NULL;
+  return from_cuda(pkv::launch_fp8_bounded_wait_selftest(static_cast<uint32_t>(polls), err_word,
+                                                         as_stream(stream)));
+}
+
 }  // extern "C"

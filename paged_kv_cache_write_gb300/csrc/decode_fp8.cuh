@@ -188,19 +188,19 @@ struct Producer {
     }
     return true;
   }
-
-  // After giving up: wait (bounded) for the copies still in flight, so that
-  // none lands after the CTA has left.
-  __device__ __forceinline__ void drain() const { attn::ring_drain(ring, issued); }
 };
 
-// Consumer warp: wait for its next tile; false if the producer gave up or the
-// wait timed out.
-__device__ __forceinline__ bool wait_tile(const Ring& r, const RingPos& pos, int32_t* err) {
-  if (wait_or_abort(r.full + pos.st, pos.round & 1, r.abort_flag)) return true;
-  // (the one that gives up first reports: the others see its flag)
-  if ((threadIdx.x & 31) == 0 && !*r.abort_flag) report(err, PKV_DEVERR_TIMEOUT);
-  return false;
+// Consumer warp: whether a thread of the CTA has given up (one of this warp for
+// certain, since it set the flag).
+__device__ __forceinline__ bool gave_up(const Ring& r) {
+  return __any_sync(0xffffffffu, *r.abort_flag != 0);
+}
+
+// Once every warp is past its loop (a barrier before): after some thread gave up
+// the producer lane waits (bounded) for its copies in flight, so that none lands
+// after the CTA has left.  issued: by this thread.
+__device__ __forceinline__ void drain_copies(const Ring& r, uint32_t issued) {
+  if (*r.abort_flag) attn::ring_drain(r, issued);
 }
 
 __device__ __forceinline__ void release_tile(const Ring& r, const RingPos& pos) {
@@ -233,9 +233,10 @@ struct ScaleBatch {
 };
 
 // Consumer warp: its next NB tiles of the ring, blocks k .. k + NB - 1 of the
-// batch in `sc`.  False: gave up (and told the others).
+// batch in `sc`.  After a wait that gave up the warp goes on over what is there
+// (its work is all its lanes'); gave_up tells before anything is stored.
 template <int NB, typename RowsT>
-__device__ __forceinline__ bool take_tiles(RowsT& rows, const Ring& ring, RingPos& pos,
+__device__ __forceinline__ void take_tiles(RowsT& rows, const Ring& ring, RingPos& pos,
                                            const ScaleBatch& sc, int k, int j0, int valid,
                                            bool use, int32_t* err) {
   float ks[NB], vs[NB], lv[NB];
@@ -249,16 +250,12 @@ __device__ __forceinline__ bool take_tiles(RowsT& rows, const Ring& ring, RingPo
     at[i] = pos;
     kt[i] = ring.k_tile(pos.st);
     vt[i] = ring.v_tile(pos.st);
-    if (!wait_tile(ring, pos, err)) {
-      *ring.abort_flag = 1;
-      return false;
-    }
+    wait_or_flag(ring.full + pos.st, pos.round & 1, ring.abort_flag, err);
     pos.next(ring);
   }
   if (use) rows.template blocks<NB>(kt, vt, j0, valid, ks, vs, lv);
 #pragma unroll
   for (int i = 0; i < NB; ++i) release_tile(ring, at[i]);
-  return true;
 }
 
 // CTAs of 8 consumer warps that an SM's registers hold.  A warp is a chain of
@@ -337,6 +334,7 @@ __global__ void __launch_bounds__(kMaxThreads, CTAS)
   Walk cur{p, kept ? lens_s : nullptr};
   if (r0 < r1) cur.begin(st);
 
+  uint32_t issued = 0;
   if (warp == consumers) {
     // -------------------------------------------------------- producer
     if (elect_one()) {
@@ -350,21 +348,20 @@ __global__ void __launch_bounds__(kMaxThreads, CTAS)
         u += n;
         cur.advance(n);
       }
-      if (!ok) pr.drain();
       // the split group this CTA merges (read by the merge kernel)
       p.splits[blockIdx.x] =
           r0 < r1 ? attn::split_entry(blockIdx.x, G, U, st.x, st.y, st.z, nblk0)
                   : make_int4(-1, 0, 0, 0);
+      issued = pr.issued;
     }
   } else if (warp < consumers) {
     // ------------------------------------------------------- consumers
     Rows<T, HD, NT, false> rows;
     rows.place(width, warp);
     RingPos pos;
-    bool ok = true;
     const T* q = static_cast<const T*>(p.q);
     T* out = static_cast<T*>(p.out);
-    for (int u = r0; u < r1 && ok;) {
+    for (int u = r0; u < r1;) {
       const int n = min(r1 - u, cur.nblk - cur.j);
       const int b = cur.b;
       const int kv_head = cur.grp * p.hg_size + warp;
@@ -382,8 +379,9 @@ __global__ void __launch_bounds__(kMaxThreads, CTAS)
           },
           [&](int) { return last; }, p.scale_log2);
       constexpr int PAIR = Rows<T, HD, NT, false>::PAIR;
-      for (int k = 0; k < n && ok;) {
+      for (int k = 0; k < n;) {
         if ((k & 31) == 0) {
+          if (gave_up(ring)) break;
           now = next;
           now.settle();
           next.load(sc, p, ids, kv_head);
@@ -391,14 +389,14 @@ __global__ void __launch_bounds__(kMaxThreads, CTAS)
         }
         const int j0 = (cur.j + k) * kBS;
         if (PAIR == 2 && k + 1 < n) {
-          ok = take_tiles<PAIR>(rows, ring, pos, now, k, j0, cur.L - j0, true, p.err);
+          take_tiles<PAIR>(rows, ring, pos, now, k, j0, cur.L - j0, true, p.err);
           k += PAIR;
         } else {
-          ok = take_tiles<1>(rows, ring, pos, now, k, j0, cur.L - j0, true, p.err);
+          take_tiles<1>(rows, ring, pos, now, k, j0, cur.L - j0, true, p.err);
           ++k;
         }
       }
-      if (!ok) break;
+      if (gave_up(ring)) break;
       if (cur.j == 0 && n == cur.nblk) {
         rows.store([&](int r) -> T* {
           return r < p.rep ? out + (int64_t(b) * p.n_heads + head0 + r) * HD : nullptr;
@@ -414,6 +412,8 @@ __global__ void __launch_bounds__(kMaxThreads, CTAS)
       cur.advance(n);
     }
   }
+  __syncthreads();
+  drain_copies(ring, issued);
 }
 
 // Batches too small to stream: one cluster of C CTAs per (sequence, head
@@ -449,10 +449,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     p.total_units[1] = -1;  // a call planning for itself replaces any kept plan
   if (rank == 0 && grp == 0 && threadIdx.x == 0) report_bad_length(p, b);
 
+  uint32_t issued = 0;
   if (warp == consumers) {
     if (elect_one()) {
       Producer pr{ring, &tm_k, &tm_v, p.num_blocks, p.err, tc::l2_evict_first_policy()};
-      if (!pr.fetch_row(trow + j0, j1 - j0, grp * p.hg_size * HD / width)) pr.drain();
+      pr.fetch_row(trow + j0, j1 - j0, grp * p.hg_size * HD / width);
+      issued = pr.issued;
     }
   } else if (warp < consumers) {
     const T* q = static_cast<const T*>(p.q);
@@ -474,10 +476,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     for (int j = j0; j < j1;) {
       const int jp = j * kBS;
       if (PAIR == 2 && j + 1 < j1) {
-        if (!take_tiles<PAIR>(rows, ring, pos, now, j - j0, jp, L - jp, true, p.err)) break;
+        take_tiles<PAIR>(rows, ring, pos, now, j - j0, jp, L - jp, true, p.err);
         j += PAIR;
       } else {
-        if (!take_tiles<1>(rows, ring, pos, now, j - j0, jp, L - jp, true, p.err)) break;
+        take_tiles<1>(rows, ring, pos, now, j - j0, jp, L - jp, true, p.err);
         ++j;
       }
     }
@@ -488,6 +490,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
   }
 
   cluster_sync();  // every CTA's partial is in its shared memory
+  drain_copies(ring, issued);
   // CTA `rank` combines elements [rank E / C, (rank + 1) E / C) of the group
   const int E = rows_per_group * HD;
   const int e0 = rank * E / C, e1 = (rank + 1) * E / C;

@@ -89,13 +89,36 @@ __device__ __forceinline__ bool mbar_park(uint64_t* bar, uint32_t parity) {
 
 // Bounded wait that also ends once some thread of the CTA has given up.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity,
-                                              volatile int* abort_flag) {
+                                              volatile int* abort_flag,
+                                              uint32_t polls = kFp8Polls) {
   if (mbar_park(bar, parity)) return true;
-  for (uint32_t i = 0; i < kFp8Polls; ++i) {
+  for (uint32_t i = 0; i < polls; ++i) {
     if (mbar_park(bar, parity)) return true;
     if (*abort_flag) return false;
   }
   return false;
+}
+
+// The same by a whole warp, whose lanes then agree: each lane looks for itself,
+// and one may see the flag where another sees the phase complete, but what
+// follows (shuffles, matrix products) is the whole warp's.
+__device__ __forceinline__ bool warp_wait_or_abort(uint64_t* bar, uint32_t parity,
+                                                   volatile int* abort_flag,
+                                                   uint32_t polls = kFp8Polls) {
+  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, polls)) != 0;
+}
+
+// The same without a vote for each wait (one costs a consumer of narrow heads 3 to
+// 8%): a lane that gives up sets the flag and goes on with its warp.  The warp looks
+// at the flag, by vote, before it stores what it computed.
+__device__ __forceinline__ void wait_or_flag(uint64_t* bar, uint32_t parity,
+                                             volatile int* abort_flag, int32_t* err,
+                                             uint32_t polls = kFp8Polls) {
+  if (!wait_or_abort(bar, parity, abort_flag, polls)) {
+    // (the one that gives up first reports: the others see its flag)
+    if (!*abort_flag) report(err, PKV_DEVERR_TIMEOUT);
+    *abort_flag = 1;
+  }
 }
 
 }  // namespace pkv

@@ -452,7 +452,40 @@ __global__ void __launch_bounds__(kThreads) kv_gather_fp8_kernel(const GatherPar
   }
 }
 
+// Self-test of the 8-bit kernels' waits: a warp half of whose lanes wait for a
+// phase that is complete and half for one that nothing completes, for at most
+// `polls` polls.  The lanes that give up report the timeout (err) and tell the
+// CTA; err is left clear if some lane is told otherwise than its warp.
+__global__ void fp8_wait_selftest_kernel(uint32_t polls, int32_t* err) {
+  __shared__ uint64_t bars[2];
+  __shared__ int flag, reported;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) {
+    mbar_init(bars, 1);
+    mbar_init(bars + 1, 1);
+    flag = reported = 0;
+    fence_barrier_init();
+    mbar_arrive(bars);
+  }
+  __syncwarp();
+  const bool there = warp_wait_or_abort(bars, 0, &flag, polls);
+  const bool mixed = warp_wait_or_abort(bars + (lane & 1), 0, &flag, polls);
+  const bool quiet = flag == 0;
+  __syncwarp();
+  wait_or_flag(bars + (lane & 1), 0, &flag, &reported, polls);
+  __syncwarp();
+  // (the flag is set: this ends at once, not after the kernels' own limit)
+  const bool told = warp_wait_or_abort(bars + (lane & 1), 0, &flag);
+  if (__all_sync(0xffffffffu, there && !mixed && quiet && flag == 1 && !told) && lane == 0)
+    report(err, reported);
+}
+
 }  // namespace
+
+cudaError_t launch_fp8_bounded_wait_selftest(uint32_t polls, int32_t* err, cudaStream_t stream) {
+  fp8_wait_selftest_kernel<<<1, 32, 0, stream>>>(polls, err);
+  return cudaGetLastError();
+}
 
 template <typename T>
 static cudaError_t write_as(const WriteParams& p, dim3 grid, cudaStream_t stream) {

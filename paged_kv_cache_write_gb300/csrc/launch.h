@@ -44,6 +44,7 @@ cudaError_t launch_kv_write_fp8(const void* k, const void* v, int32_t dtype,
                                 int32_t num_seqs, int32_t num_tokens, void* k_pool, void* v_pool,
                                 float* k_scales, float* v_scales, const PoolShape& pool,
                                 int32_t* err, cudaStream_t stream);
+cudaError_t launch_fp8_bounded_wait_selftest(uint32_t polls, int32_t* err, cudaStream_t stream);
 cudaError_t launch_kv_gather_fp8(const void* k_pool, const void* v_pool, const float* k_scales,
                                  const float* v_scales, const PoolShape& pool,
                                  const int32_t* block_tables, int32_t max_blocks_per_seq,

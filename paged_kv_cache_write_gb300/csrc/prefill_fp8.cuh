@@ -64,10 +64,12 @@ __global__ void __launch_bounds__((kPrefillWarps + 1) * 32, CTAS)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t* row = p.bt + int64_t(b) * p.W;
 
+  uint32_t issued = 0;
   if (warp == kPrefillWarps) {
     if (elect_one()) {  // (the chunk's other tiles read the blocks again: no eviction hint)
       Producer pr{ring, &tm_k, &tm_v, p.num_blocks, p.err, 0};
-      if (!pr.fetch_row(row, n_blocks, g)) pr.drain();
+      pr.fetch_row(row, n_blocks, g);
+      issued = pr.issued;
     }
   } else {
     Rows<T, HD, kPrefillTiles, true> rows;
@@ -96,6 +98,7 @@ __global__ void __launch_bounds__((kPrefillWarps + 1) * 32, CTAS)
     constexpr int PAIR = Rows<T, HD, kPrefillTiles, true>::PAIR;
     for (int k = 0; k < n_blocks;) {
       if ((k & 31) == 0) {
+        if (gave_up(ring)) break;
         now = next;
         now.settle();
         next.load(sc, dp, ids, g);
@@ -104,19 +107,23 @@ __global__ void __launch_bounds__((kPrefillWarps + 1) * 32, CTAS)
       const int j0 = k * kBS;
       const bool use = j0 <= my_last;
       if (PAIR == 2 && k + 1 < n_blocks) {
-        if (!take_tiles<PAIR>(rows, ring, pos, now, k, j0, L - j0, use, p.err)) return;
+        take_tiles<PAIR>(rows, ring, pos, now, k, j0, L - j0, use, p.err);
         k += PAIR;
       } else {
-        if (!take_tiles<1>(rows, ring, pos, now, k, j0, L - j0, use, p.err)) return;
+        take_tiles<1>(rows, ring, pos, now, k, j0, L - j0, use, p.err);
         ++k;
       }
     }
-    T* out = static_cast<T*>(p.out);
-    rows.store([&](int r) -> T* {
-      if (r >= nrows || query_of(r) >= c) return nullptr;
-      return out + (int64_t(q0 + query_of(r)) * p.n_heads + head_of(r)) * HD;
-    });
+    if (!gave_up(ring)) {
+      T* out = static_cast<T*>(p.out);
+      rows.store([&](int r) -> T* {
+        if (r >= nrows || query_of(r) >= c) return nullptr;
+        return out + (int64_t(q0 + query_of(r)) * p.n_heads + head_of(r)) * HD;
+      });
+    }
   }
+  __syncthreads();
+  drain_copies(ring, issued);
 }
 
 template <typename T, int HD>

@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return wait_or_abort(bar, parity, abort_flag);
   };
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait_one(bar, parity)) != 0;
+    return warp_wait_or_abort(bar, parity, abort_flag);
   };
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) mbar_init(q_full + i, 4);

@@ -666,6 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         move = most > kWeightMax;
         if (!__any_sync(0xffffffffu, move)) break;
+        tc::tmem_wait_st();  // the second pass stores to the same columns
       }
       // (2^d in two steps: it underflows where a value scale is some 2^100 times the
       // earlier ones, whose keys' share of the sum then still counts)

@@ -612,6 +612,12 @@ pkv_status pkv_paged_attention_decode_fp8(const void* q, int32_t dtype, int32_t 
  * fp32 queries and weights keep 22.
  *
  *   q, out      [total_q, n_heads, head_dim] of `dtype`, 16-byte aligned
+ *   cu_q_lens   nondecreasing, cu_q_lens[num_seqs] = total_q, no chunk longer
+ *               than max_q_len: offsets that go back, stop short of the rows,
+ *               go past them or make a longer chunk are reported
+ *               (PKV_DEVERR_LENGTH).  Rows of no chunk, and of one that does
+ *               not lie within the rows, are left as they were; of a chunk
+ *               longer than max_q_len the rows past that may be
  *   everything else as for pkv_paged_attention_prefill; supported shapes as
  *   for pkv_paged_attention_decode_fp8
  */

@@ -60,6 +60,26 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t b) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// What a prefill reports of one sequence's chunk, query rows q0 .. end - 1 of
+// total_q, at the end of L tokens (last: the batch's last sequence).  The kernels
+// compute no chunk that reaches outside the rows or has more queries than tokens,
+// and not more than max_q_len rows of a longer one for certain.
+struct ChunkLimits {
+  int total_q, max_q_len, max_len;
+  int64_t table_tokens;  // that a table row has blocks for
+};
+
+__device__ __forceinline__ void report_bad_chunk(int32_t* err, const ChunkLimits& m, int q0,
+                                                 int end, int L, bool last) {
+  const int64_t c = int64_t(end) - q0;
+  if (q0 < 0 || c < 0 || c > m.max_q_len || end > m.total_q || (last && end != m.total_q))
+    report(err, PKV_DEVERR_LENGTH);
+  if (c <= 0) return;  // (nothing of the sequence is read)
+  if (L < c) report(err, PKV_DEVERR_LENGTH);
+  else if (L > m.max_len)
+    report(err, L > m.table_tokens ? PKV_DEVERR_TABLE_WIDTH : PKV_DEVERR_LENGTH);
+}
+
 // True in one lane of a converged warp.  Unlike a test of the lane id this
 // lets the compiler keep what the lane issues asynchronous operations with
 // (descriptors, shared-memory addresses) in uniform registers.

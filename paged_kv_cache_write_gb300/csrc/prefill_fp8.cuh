@@ -33,29 +33,22 @@ template <typename T, int HD, int CTAS>
 __global__ void __launch_bounds__((kPrefillWarps + 1) * 32, CTAS)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const PrefillParams p,
-                   const Scales sc) {
+                   const Scales sc, const ChunkLimits limits, const int last_seq) {
   extern __shared__ __align__(128) uint8_t smem[];
   attn::pdl_wait();
   attn::pdl_launch_dependents();
   const int b = blockIdx.z;
   const int g = blockIdx.y;
-  const int q0 = p.cu_q[b];
-  const int c = p.cu_q[b + 1] - q0;
+  const int q0 = p.cu_q[b], end = p.cu_q[b + 1];
+  if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0)
+    report_bad_chunk(p.err, limits, q0, end, p.seq_lens[b], b == last_seq);
+  if (q0 < 0 || end <= q0 || end > p.total_q) return;  // no chunk, or not within the rows
+  const int c = end - q0;
   const int tile_q = kPrefillWarps * p.queries_per_warp;
   const int i0 = blockIdx.x * tile_q;
   if (i0 >= c) return;  // whole CTA idle: exit before touching barriers
-  if (q0 < 0 || int64_t(q0) + c > p.total_q) {  // offsets disagree with the query count
-    if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0) report(p.err, PKV_DEVERR_LENGTH);
-    return;
-  }
-  int L = p.seq_lens[b];
-  if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0) {
-    if (L < c || L < 0) report(p.err, PKV_DEVERR_LENGTH);
-    else if (L > p.max_len)
-      report(p.err, L > int64_t(p.W) * kBS ? PKV_DEVERR_TABLE_WIDTH : PKV_DEVERR_LENGTH);
-  }
-  if (L > p.max_len) L = p.max_len;
-  if (L < c) return;  // inconsistent chunk: reported above, nothing computed
+  const int L = min(p.seq_lens[b], p.max_len);
+  if (L < c) return;  // inconsistent chunk: nothing computed
   const int i_end = min(c, i0 + tile_q);
   const int n_blocks = (L - c + i_end - 1) / kBS + 1;  // up to the last key any row sees
 
@@ -169,6 +162,8 @@ cudaError_t prefill_run(const AttnArgs& a, const Scales& sc, cudaStream_t stream
   const int threads = (kPrefillWarps + 1) * 32;
   cudaError_t e = kernel_setup(setup[ctas - 1], kern, static_cast<int>(smem), threads, nullptr);
   if (e != cudaSuccess) return e;
+  const ChunkLimits limits{a.total_q, a.max_q_len, a.max_seq_len,
+                           int64_t(a.max_blocks_per_seq) * kBS};
   // the grid's y and z extents are 16-bit: long batches go in slices
   for (int s0 = 0; s0 < a.num_seqs; s0 += 65535) {
     PrefillParams ps = p;
@@ -177,7 +172,8 @@ cudaError_t prefill_run(const AttnArgs& a, const Scales& sc, cudaStream_t stream
     ps.seq_lens += s0;
     ps.bt += int64_t(s0) * p.W;
     const dim3 grid(static_cast<unsigned>(tiles), pool.n_kv, ps.B);
-    e = launch_pdl(kern, grid, threads, smem, stream, tm_k, tm_v, ps, sc);
+    const int last_seq = s0 + ps.B == a.num_seqs ? ps.B - 1 : -1;
+    e = launch_pdl(kern, grid, threads, smem, stream, tm_k, tm_v, ps, sc, limits, last_seq);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

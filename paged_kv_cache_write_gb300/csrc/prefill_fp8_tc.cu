@@ -103,7 +103,8 @@ struct TcParams {
   __nv_bfloat16* out;
   int32_t* err;
   int B, n_heads, n_kv, rep, rep_inv, W, num_blocks, max_len, total_q, q_per_tile;
-  int ordered;
+  int ordered, last_seq;
+  ChunkLimits limits;
   float scale_log2;
 };
 
@@ -178,6 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       at = p.cu_q[t];
       end = p.cu_q[t + 1];
       len = p.seq_lens[t];
+      if (blockIdx.x == 0) report_bad_chunk(p.err, p.limits, at, end, len, t == p.last_seq);
       const int64_t cs = int64_t(end) - at;
       const int64_t Ls = min(len, p.max_len);
       wt = cs * (2 * Ls - cs + 1);
@@ -216,24 +218,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       seq_s[0] = p.cu_q[b];
       seq_s[1] = p.cu_q[b + 1];
       seq_s[2] = p.seq_lens[b];
+      if (pair == 0 && g == 0)
+        report_bad_chunk(p.err, p.limits, seq_s[0], seq_s[1], seq_s[2], b == p.last_seq);
     }
     __syncthreads();
   }
   const int q0 = seq_s[0];
+  // idle CTAs leave before any barrier or TMEM use
+  if (q0 < 0 || seq_s[1] <= q0 || seq_s[1] > p.total_q) return;  // no chunk, or not within the rows
   const int c = seq_s[1] - q0;
   const int i0 = pair * 2 * p.q_per_tile;  // first query of tile A
-  if (i0 >= c) return;                     // idle CTA: leave before any barrier or TMEM use
-  if (q0 < 0 || int64_t(q0) + c > p.total_q) {
-    if (threadIdx.x == 0 && i0 == 0 && g == 0) report(p.err, PKV_DEVERR_LENGTH);
-    return;
-  }
-  int L = seq_s[2];
-  if (threadIdx.x == 0 && i0 == 0 && g == 0) {
-    if (L < c || L < 0) report(p.err, PKV_DEVERR_LENGTH);
-    else if (L > p.max_len)
-      report(p.err, L > int64_t(p.W) * kBlk ? PKV_DEVERR_TABLE_WIDTH : PKV_DEVERR_LENGTH);
-  }
-  if (L > p.max_len) L = p.max_len;
+  if (i0 >= c) return;
+  const int L = min(seq_s[2], p.max_len);
   if (L < c) return;
   const int i_end = min(c, i0 + 2 * p.q_per_tile);
   const int n_tiles = (L - c + i_end - 1) / kTileKeys + 1;
@@ -794,6 +790,8 @@ cudaError_t run_tc(const AttnArgs& a, const float* k_scales, const float* v_scal
   p.total_q = a.total_q;
   p.q_per_tile = kRows / rep;
   p.scale_log2 = a.scale * kLog2e;
+  p.limits = ChunkLimits{a.total_q, a.max_q_len, a.max_seq_len,
+                         int64_t(a.max_blocks_per_seq) * kBlk};
   auto kern = prefill_fp8_tc_kernel<HD>;
   static KernelSetup setup;
   cudaError_t e = kernel_setup(setup, kern, Lay::REQUEST, kThreads, nullptr);
@@ -810,6 +808,7 @@ cudaError_t run_tc(const AttnArgs& a, const float* k_scales, const float* v_scal
     p.bt = a.block_tables + int64_t(s0) * p.W;
     p.seq_lens = a.seq_lens + s0;
     p.cu_q = a.cu_q_lens + s0;
+    p.last_seq = s0 + p.B == a.num_seqs ? p.B - 1 : -1;
     const dim3 grid = p.ordered ? dim3(static_cast<unsigned>(slots), 1, 1)
                                 : dim3((a.max_q_len + qpp - 1) / qpp, pool.n_kv, p.B);
     if ((e = launch_pdl(kern, grid, kThreads, Lay::REQUEST, stream, p)) != cudaSuccess) return e;

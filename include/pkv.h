@@ -545,7 +545,8 @@ pkv_status pkv_paged_attention_decode_noalloc(const void* q, int32_t num_seqs, i
  *   cu_new_lens   int32 [num_seqs + 1], cu_new_lens[0] = 0, nondecreasing,
  *                 cu_new_lens[num_seqs] = num_tokens (n_b = 0: writes nothing)
  *   k_pool, v_pool  16-byte aligned; k_scales, v_scales fp32 [num_blocks, n_kv]
- *   A token whose length, offset or block id is bad is skipped and reported.
+ *   A token whose length, offset or block id is bad is skipped and reported,
+ *   and so are offsets that go past num_tokens.
  */
 pkv_status pkv_kv_write_fp8(const void* k, const void* v, int32_t dtype,
                             const int32_t* block_tables, int32_t max_blocks_per_seq,

@@ -263,6 +263,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
     const unsigned m = __ballot_sync(0xffffffffu, begins);
     if (begins) run_s[__popc(m & ((1u << lane) - 1u))] = run;
     if (lane == 0) runs_s = __popc(m);
+  } else if (threadIdx.x == 32 && blockIdx.x == 0 && blockIdx.y == 0) {
+    if (p.cu[p.num_seqs] > p.num_tokens) report(p.err, PKV_DEVERR_LENGTH);
   }
   __syncthreads();
 

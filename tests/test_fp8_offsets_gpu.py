@@ -1,4 +1,4 @@
-"""Query offsets of the 8-bit prefill that disagree with its arguments."""
+"""Offsets of the 8-bit prefill and write that disagree with their arguments."""
 import numpy as np
 import pytest
 import torch
@@ -64,3 +64,22 @@ def test_offsets_that_disagree_are_reported(head_dim, dtype, n, cu, good):
             assert torch.equal(out[lo:hi], want[lo:hi]), i
     assert bool((out[~owned] == 7.0).all())
     assert ref.shape[0] == 6 * n
+
+
+@pytest.mark.parametrize("n", [4, 700])
+def test_write_reports_sequences_past_the_tokens(n):
+    """The last sequences' tokens are not among those given: the others' are
+    written and the loss is reported."""
+    import paged_kv_cache_write_gb300 as pkv
+    bt, ref = (Batch([20] * n, n_kv=2, head_dim=32, seed=1) for _ in range(2))
+    k = guarded_copy(bt.draw(3))
+    lens = ints([20] * n)
+    for cu in ([0, 1, 2, 3] + [4] * (n - 3), [0, 1, 2, 3] + [2 ** 31 - 1] * (n - 3)):
+        bt.err.zero_()
+        pkv.kv_write_fp8(k, k, bt.bt, lens, ints(cu), *bt.cache, err=bt.err)
+        torch.cuda.synchronize()
+        assert int(bt.err.item()) == pkv.DEVERR["length"]
+    pkv.kv_write_fp8(k, k, ref.bt, lens, ints([0, 1, 2, 3] + [3] * (n - 3)), *ref.cache, err=ref.err)
+    ref.no_error()
+    for x, y in zip(bt.cache, ref.cache):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))

@@ -510,8 +510,9 @@ pkv_status pkv_paged_attention_decode_noalloc(const void* q, int32_t num_seqs, i
  * prefill to bf16).
  *
  * head_dim must be a multiple of 16 (attention: 16, 32, 64 or 128, with
- * block_size 16), n_kv * head_dim at most 2^26, and block_size * head_dim and
- * max_blocks_per_seq * block_size below 2^31 (PKV_ERR_RANGE).  `dtype` is the
+ * block_size 16), n_kv * head_dim at most 2^26 (attention: n_kv at most
+ * 65,535 besides), and block_size * head_dim and max_blocks_per_seq *
+ * block_size below 2^31 (PKV_ERR_RANGE).  `dtype` is the
  * type of k, v, q and the outputs (PKV_F32 or PKV_BF16).
  *
  * A block is copied on write with two pkv_copy_blocks calls: one on the pools

@@ -30,6 +30,8 @@ pkv_status check_fp8(const void* q, int32_t dtype, int32_t num_seqs, int32_t n_h
                      PoolShape* shape) {
   pkv_status st = check_pool_fp8(pool, shape);
   if (st != PKV_OK) return st;
+  // (a KV head is a grid's y in the prefill, and 16 bits of a decode's split entry)
+  if (shape->n_kv > 65535) return PKV_ERR_RANGE;
   if (!float_type(dtype)) return PKV_ERR_DTYPE;
   st = pkv::check_attention_args(q, num_seqs, n_heads, k_pool, v_pool, *shape, block_tables,
                                  max_blocks_per_seq, seq_lens, max_seq_len, scale, out);

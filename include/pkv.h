@@ -208,7 +208,7 @@ pkv_status pkv_kv_gather(const void* k_pool, const void* v_pool, const pkv_pool_
  *
  *   block_pairs  int32 [num_pairs][2] (source, destination), device memory
  *   k_pool, v_pool  16-byte aligned; n_kv * head_dim * sizeof(dtype) a
- *                   multiple of 16 bytes
+ *                   multiple of 4 bytes
  */
 pkv_status pkv_copy_blocks(void* k_pool, void* v_pool, const pkv_pool_desc* pool,
                            const int32_t* block_pairs, int32_t num_pairs, int32_t* err_word,
@@ -518,7 +518,7 @@ pkv_status pkv_paged_attention_decode_noalloc(const void* q, int32_t num_seqs, i
  * A block is copied on write with two pkv_copy_blocks calls: one on the pools
  * described as bf16 with head_dim / 2 (the bytes are copied as they are), one
  * on the scales described as fp32 blocks of one token, one head and head_dim
- * n_kv (n_kv a multiple of 4).
+ * n_kv.
  */
 
 /*

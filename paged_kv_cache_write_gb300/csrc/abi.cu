@@ -76,7 +76,7 @@ pkv_status pkv_copy_blocks(void* k_pool, void* v_pool, const pkv_pool_desc* pool
                           void* stream) {
   PKV_NVTX_RANGE("pkv_copy_blocks");
   PoolShape shape;
-  pkv_status st = check_pool(pool, &shape);
+  pkv_status st = check_pool(pool, &shape, 4);
   if (st != PKV_OK) return st;
   if (num_pairs < 0) return PKV_ERR_SHAPE;
   if (num_pairs == 0) return PKV_OK;

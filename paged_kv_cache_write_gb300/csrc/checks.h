@@ -19,15 +19,15 @@ inline pkv_status from_cuda(cudaError_t e) {
   return PKV_ERR_CUDA;
 }
 
-// A pool descriptor: known dtype, positive sizes, 16-byte token rows and a
-// flat slot index that fits in int32.
-inline pkv_status check_pool(const pkv_pool_desc* pool, PoolShape* out) {
+// A pool descriptor: known dtype, positive sizes, token rows of whole words of
+// `row_align` bytes and a flat slot index that fits in int32.
+inline pkv_status check_pool(const pkv_pool_desc* pool, PoolShape* out, int row_align = 16) {
   if (pool == nullptr) return PKV_ERR_NULL;
   if (pool->dtype != PKV_F32 && pool->dtype != PKV_BF16) return PKV_ERR_DTYPE;
   if (pool->num_blocks <= 0 || pool->block_size <= 0 || pool->n_kv <= 0 || pool->head_dim <= 0)
     return PKV_ERR_SHAPE;
   *out = PoolShape{pool->num_blocks, pool->block_size, pool->n_kv, pool->head_dim, pool->dtype};
-  if (out->row_bytes() % 16 != 0) return PKV_ERR_ALIGN;
+  if (out->row_bytes() % row_align != 0) return PKV_ERR_ALIGN;
   if ((int64_t)pool->num_blocks * pool->block_size > INT32_MAX) return PKV_ERR_RANGE;
   return PKV_OK;
 }

@@ -86,12 +86,15 @@ __global__ void kv_write_kernel(const uint4* __restrict__ k, const uint4* __rest
 // pairs[i][1] in both pools.  The K and V blocks are one run of 16-byte
 // words (K first, then V); each thread moves kCopyUnroll words per pass
 // with all loads issued before any store, streaming past the caches (the
-// copied data is not read again by this kernel).
+// copied data is not read again by this kernel).  Blocks that are not whole
+// 16-byte words (the scales of an 8-bit cache of 1, 2, 3, .. KV heads) go by
+// 4-byte words.
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 8;
 
+template <typename Word>
 __global__ void __launch_bounds__(kCopyThreads)
-    copy_blocks_kernel(uint4* __restrict__ k_pool, uint4* __restrict__ v_pool,
+    copy_blocks_kernel(Word* __restrict__ k_pool, Word* __restrict__ v_pool,
                        const int32_t* __restrict__ pairs, int64_t words_per_block,
                        int num_blocks, int32_t* err) {
   const int src = __ldg(pairs + 2 * int64_t(blockIdx.x));
@@ -101,12 +104,12 @@ __global__ void __launch_bounds__(kCopyThreads)
     return;
   }
   const int64_t n = 2 * words_per_block;
-  const uint4* ks = k_pool + src * words_per_block;
-  const uint4* vs = v_pool + src * words_per_block;
-  uint4* kd = k_pool + dst * words_per_block;
-  uint4* vd = v_pool + dst * words_per_block;
+  const Word* ks = k_pool + src * words_per_block;
+  const Word* vs = v_pool + src * words_per_block;
+  Word* kd = k_pool + dst * words_per_block;
+  Word* vd = v_pool + dst * words_per_block;
   for (int64_t base = threadIdx.x; base < n; base += int64_t(kCopyThreads) * kCopyUnroll) {
-    uint4 x[kCopyUnroll];
+    Word x[kCopyUnroll];
 #pragma unroll
     for (int u = 0; u < kCopyUnroll; ++u) {
       const int64_t i = base + int64_t(u) * kCopyThreads;
@@ -213,10 +216,15 @@ cudaError_t launch_copy_blocks(void* k_pool, void* v_pool, const PoolShape& pool
                                const int32_t* pairs, int32_t num_pairs, int32_t* err,
                                cudaStream_t stream) {
   if (num_pairs == 0) return cudaSuccess;
-  const int64_t words = int64_t(pool.block_size) * pool.row_bytes() / 16;
-  copy_blocks_kernel<<<num_pairs, kCopyThreads, 0, stream>>>(
-      static_cast<uint4*>(k_pool), static_cast<uint4*>(v_pool), pairs, words, pool.num_blocks,
-      err);
+  const int64_t bytes = int64_t(pool.block_size) * pool.row_bytes();
+  if (bytes % 16 == 0)
+    copy_blocks_kernel<<<num_pairs, kCopyThreads, 0, stream>>>(
+        static_cast<uint4*>(k_pool), static_cast<uint4*>(v_pool), pairs, bytes / 16,
+        pool.num_blocks, err);
+  else
+    copy_blocks_kernel<<<num_pairs, kCopyThreads, 0, stream>>>(
+        static_cast<uint32_t*>(k_pool), static_cast<uint32_t*>(v_pool), pairs, bytes / 4,
+        pool.num_blocks, err);
   return cudaGetLastError();
 }
 

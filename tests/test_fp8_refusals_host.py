@@ -31,3 +31,11 @@ def test_attention_refuses_more_kv_heads_than_its_grids_hold(pkv):
         assert pkv.lib.pkv_paged_attention_prefill_fp8(
             FAKE, 1, FAKE, 2, 10, 8, 17 * n_kv, FAKE, FAKE, FAKE, FAKE, by, FAKE, 4, FAKE, 64, 0.1,
             FAKE, None, None) == status
+
+
+def test_copy_blocks_takes_rows_of_whole_4_byte_words(pkv):
+    def copy(**kw):
+        d = pkv.PoolDesc(**{**dict(num_blocks=8, block_size=1, n_kv=1, head_dim=3, dtype=0), **kw})
+        return pkv.lib.pkv_copy_blocks(FAKE, FAKE, ctypes.byref(d), FAKE, 0, None, None)
+    assert copy() == 0 and copy(head_dim=1) == 0 and copy(dtype=1, head_dim=2) == 0
+    assert copy(dtype=1) == 4  # bf16 rows of 6 bytes

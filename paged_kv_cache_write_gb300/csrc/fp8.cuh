@@ -21,7 +21,6 @@
 
 namespace pkv {
 
-constexpr float kE4m3Max = 448.f;  // 1.75 * 2^8
 constexpr int kFp8MinExp = -60;
 constexpr int kFp8MaxExp = 60;
 

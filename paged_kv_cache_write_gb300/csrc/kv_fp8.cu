@@ -32,21 +32,18 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kWindow = 32;  // consecutive tokens whose runs one CTA column handles
+constexpr int kWindow = 32;  // consecutive tokens that one CTA (column) handles: a warp's lanes
 constexpr int kHeld = 8;     // 8-element vectors that a lane holds
 
-// Sequences of the tokens t0 .. t0 + N - 1 (N = 32 or 64) of a ragged batch,
-// by the whole CTA: thread i < N gets the number of sequences that end at or
-// before token t0 + i, i.e. its sequence (num_seqs if it lies past the last).
-// One pass over the offsets with every load in flight, not a chain of
-// dependent ones.
-template <int N>
-__device__ __forceinline__ int window_seq(const int32_t* cu, int num_seqs, int t0,
-                                          int* cnt_s) {
+// Sequences of the window's tokens of a ragged batch, by the whole CTA: lane i of
+// warp 0 gets the number of sequences that end at or before token t0 + i, i.e. its
+// sequence (num_seqs if it lies past the last).  One pass over the offsets with
+// every load in flight, not a chain of dependent ones.
+__device__ __forceinline__ int window_seq(const int32_t* cu, int num_seqs, int t0, int* cnt_s) {
   const int tid = threadIdx.x;
-  if (tid < N) cnt_s[tid] = 0;  // [0]: ends at or before t0; [i]: ends at t0 + i
+  if (tid < kWindow) cnt_s[tid] = 0;  // [0]: ends at or before t0; [i]: ends at t0 + i
   __syncthreads();
-  const int t1 = t0 + min(N, INT_MAX - t0);
+  const int t1 = t0 + min(kWindow, INT_MAX - t0);
   int before = 0;
 #pragma unroll 4
   for (int i = tid; i < num_seqs; i += kThreads) {
@@ -57,14 +54,13 @@ __device__ __forceinline__ int window_seq(const int32_t* cu, int num_seqs, int t
   before = __reduce_add_sync(0xffffffffu, before);
   if ((tid & 31) == 0 && before > 0) atomicAdd(cnt_s, before);
   __syncthreads();
-  if (tid >= N) return 0;
+  if (tid >= kWindow) return 0;
   int x = cnt_s[tid];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if ((tid & 31) >= o) x += y;
+    if (tid >= o) x += y;
   }
-  if (tid >= 32) x += __reduce_add_sync(0xffffffffu, cnt_s[tid & 31]);
   return x;
 }
 
@@ -227,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
   pdl_launch_dependents();
   const int t0 = blockIdx.x * kWindow;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = window_seq<kWindow>(p.cu, p.num_seqs, t0, cnt_s);
+  const int b = window_seq(p.cu, p.num_seqs, t0, cnt_s);
   if (warp == 0) {
     // a run: the new tokens of one sequence in one block.  Lane i looks at
     // token t0 + i: it begins a run if it is its sequence's first new token
@@ -320,7 +316,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
 
 // ------------------------------------------------------------------ gather
 
-constexpr int kGatherTokens = 32;
 constexpr int kGatherRows = 4;   // rows a warp reads at once
 constexpr int kGatherSteps = 2;  // and steps of 32 items in each
 
@@ -365,20 +360,20 @@ struct Item<__nv_bfloat16> {
   }
 };
 
-// A CTA reads back kGatherTokens tokens: 2 x kGatherTokens rows of n_kv x hd
+// A CTA reads back kWindow tokens: 2 x kWindow rows of n_kv x hd
 // elements (K and V), kGatherRows rows of a warp at a time with
 // kGatherRows x kGatherSteps loads in flight per lane.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) kv_gather_fp8_kernel(const GatherParams p) {
-  __shared__ int cnt_s[kGatherTokens];
-  __shared__ int blk_s[kGatherTokens], off_s[kGatherTokens];
+  __shared__ int cnt_s[kWindow];
+  __shared__ int blk_s[kWindow], off_s[kWindow];
   // The next kernel is not let in early: a planned decode of the bf16 cache reads
   // its first K/V before it waits, and these outputs may be that cache's blocks.
   pdl_wait();
-  const int t0 = blockIdx.x * kGatherTokens;
-  const int n = min(kGatherTokens, p.total - t0);
-  const int b = window_seq<kGatherTokens>(p.cu, p.num_seqs, t0, cnt_s);
-  if (threadIdx.x < kGatherTokens) {
+  const int t0 = blockIdx.x * kWindow;
+  const int n = min(kWindow, p.total - t0);
+  const int b = window_seq(p.cu, p.num_seqs, t0, cnt_s);
+  if (threadIdx.x < kWindow) {
     const int i = threadIdx.x;
     int blk = -1, off = 0;  // -1: nothing to read, zeros
     if (i < n) {
@@ -566,8 +561,8 @@ cudaError_t launch_kv_gather_fp8(const void* k_pool, const void* v_pool, const f
   p.num_blocks = pool.num_blocks;
   p.n_kv = pool.n_kv;
   p.hd = pool.head_dim;
-  const unsigned grid = static_cast<unsigned>((int64_t(total_tokens) + kGatherTokens - 1) /
-                                              kGatherTokens);
+  const unsigned grid = static_cast<unsigned>((int64_t(total_tokens) + kWindow - 1) /
+                                              kWindow);
   return launch_pdl(dtype == PKV_F32 ? kv_gather_fp8_kernel<float>
                                      : kv_gather_fp8_kernel<__nv_bfloat16>,
                     dim3(grid), kThreads, 0, stream, p);

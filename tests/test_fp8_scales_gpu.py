@@ -51,3 +51,31 @@ def test_prefill(head_dim, dtype, small):
         out = bt.prefill(q, [n], [c])
         bt.no_error()
         bt.check(out, q, [0] * c, range(n - c, n), held=4)
+
+
+@pytest.mark.parametrize("head_dim,dtype", [(16, "bf16"), (64, "bf16"), (128, "bf16"), (64, "f32")])
+def test_scales_that_are_no_powers_of_two(head_dim, dtype):
+    """A cache that another quantiser wrote, with any positive scales: attended
+    and read back at value times scale."""
+    import paged_kv_cache_write_gb300 as pkv
+    lens = [700, 33, 130]
+    bt = Batch(lens, n_kv=2, head_dim=head_dim, dtype=dtype, seed=2)
+    bt.fill()
+    rng = np.random.default_rng(0)
+    for host, dev in ((bt.ks, bt.d_ks), (bt.vs, bt.d_vs)):
+        host[:] = (host * rng.uniform(0.5, 2.0, size=host.shape)).astype(np.float32)
+        dev.copy_(torch.from_numpy(host))
+    q = bt.queries(3, 8)
+    for ctas in (0, 1, 7):
+        bt.check(bt.decode(q, max_ctas=ctas), q, range(3), [n - 1 for n in lens])
+    new = [20, 33, 1]
+    q = bt.queries(sum(new), 8)
+    out = bt.prefill(q, lens, new)
+    bt.check(out, q, [b for b, c in enumerate(new) for _ in range(c)],
+             [n - c + i for n, c in zip(lens, new) for i in range(c)], held=4)
+    sl, cu = (torch.as_tensor(np.asarray(x, dtype=np.int32), device="cuda")
+              for x in (lens, np.concatenate([[0], np.cumsum(lens)])))
+    k, _ = pkv.kv_gather_fp8(*bt.cache, bt.bt, sl, cu, sum(lens), dtype=torch.float32, err=bt.err)
+    ref = np.concatenate([bt.rows(b, n)[0] for b, n in enumerate(lens)])
+    assert np.array_equal(k.double().cpu().numpy(), ref.astype(np.float32).astype(np.float64))
+    bt.no_error()

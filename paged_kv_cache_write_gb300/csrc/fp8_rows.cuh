@@ -291,7 +291,8 @@ struct Rows {
           for (int e = 0; e < 4; ++e)
             if (j0 + nb * kBS + tok_k + (e >> 1) * 8 > last[nt][e & 1]) w[nb][nt][e] = -INFINITY;
     }
-    float d[NT][2], sum[NT][2];  // d: log2 of the factor on what came before
+    // d: log2 of the factor on what came before; f: that of the sum
+    float d[NT][2], f[NT][2], sum[NT][2];
     bool moved = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -308,6 +309,7 @@ struct Rows {
         d[nt][j] = m[nt][j] - ref;
         moved |= mn != m[nt][j];
         m[nt][j] = mn;
+        f[nt][j] = 1.f;
         sum[nt][j] = 0.f;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -334,14 +336,16 @@ struct Rows {
           o[nt][i][3] *= a1;
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) l[nt][j] *= fast_exp2(fminf(d[nt][j] + kSumStep, 0.f));
+        for (int j = 0; j < 2; ++j) {
+          l[nt][j] *= fast_exp2(fminf(d[nt][j] + kSumStep, 0.f));
+          f[nt][j] = fast_exp2(fmaxf(d[nt][j], -kSumStep));
+        }
       }
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        l[nt][j] = l[nt][j] * fast_exp2(fmaxf(d[nt][j], -kSumStep)) + sum[nt][j];
+      for (int j = 0; j < 2; ++j) l[nt][j] = l[nt][j] * f[nt][j] + sum[nt][j];
     // V rows past the sequence's end hold whatever the pool holds there
     if (valid < NB * kBS) {
 #pragma unroll

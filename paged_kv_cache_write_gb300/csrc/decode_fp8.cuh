@@ -188,19 +188,22 @@ struct Producer {
     }
     return true;
   }
+
+  // At the end: until the consumers have left the last tile, and all have landed;
+  // where some thread gave up, a bounded wait for the copies still in flight, so
+  // that none lands after the CTA has left.
+  __device__ __forceinline__ void finish() const {
+    if (issued == 0) return;
+    const uint32_t last = issued - 1, st = last % ring.nstages;
+    const bool left = wait_or_abort(ring.empty + st, (last / ring.nstages) & 1, ring.abort_flag);
+    if (!left || *ring.abort_flag) attn::ring_drain(ring, issued);
+  }
 };
 
 // Consumer warp: whether a thread of the CTA has given up (one of this warp for
 // certain, since it set the flag).
 __device__ __forceinline__ bool gave_up(const Ring& r) {
   return __any_sync(0xffffffffu, *r.abort_flag != 0);
-}
-
-// Once every warp is past its loop (a barrier before): after some thread gave up
-// the producer lane waits (bounded) for its copies in flight, so that none lands
-// after the CTA has left.  issued: by this thread.
-__device__ __forceinline__ void drain_copies(const Ring& r, uint32_t issued) {
-  if (*r.abort_flag) attn::ring_drain(r, issued);
 }
 
 __device__ __forceinline__ void release_tile(const Ring& r, const RingPos& pos) {
@@ -334,7 +337,6 @@ __global__ void __launch_bounds__(kMaxThreads, CTAS)
   Walk cur{p, kept ? lens_s : nullptr};
   if (r0 < r1) cur.begin(st);
 
-  uint32_t issued = 0;
   if (warp == consumers) {
     // -------------------------------------------------------- producer
     if (elect_one()) {
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(kMaxThreads, CTAS)
       p.splits[blockIdx.x] =
           r0 < r1 ? attn::split_entry(blockIdx.x, G, U, st.x, st.y, st.z, nblk0)
                   : make_int4(-1, 0, 0, 0);
-      issued = pr.issued;
+      pr.finish();
     }
   } else if (warp < consumers) {
     // ------------------------------------------------------- consumers
@@ -412,8 +414,6 @@ __global__ void __launch_bounds__(kMaxThreads, CTAS)
       cur.advance(n);
     }
   }
-  __syncthreads();
-  drain_copies(ring, issued);
 }
 
 // Batches too small to stream: one cluster of C CTAs per (sequence, head
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
   }
 
   cluster_sync();  // every CTA's partial is in its shared memory
-  drain_copies(ring, issued);
+  if (*ring.abort_flag) attn::ring_drain(ring, issued);  // (as Producer::finish)
   // CTA `rank` combines elements [rank E / C, (rank + 1) E / C) of the group
   const int E = rows_per_group * HD;
   const int e0 = rank * E / C, e1 = (rank + 1) * E / C;

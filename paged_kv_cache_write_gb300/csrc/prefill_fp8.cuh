@@ -57,12 +57,11 @@ __global__ void __launch_bounds__((kPrefillWarps + 1) * 32, CTAS)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t* row = p.bt + int64_t(b) * p.W;
 
-  uint32_t issued = 0;
   if (warp == kPrefillWarps) {
     if (elect_one()) {  // (the chunk's other tiles read the blocks again: no eviction hint)
       Producer pr{ring, &tm_k, &tm_v, p.num_blocks, p.err, 0};
       pr.fetch_row(row, n_blocks, g);
-      issued = pr.issued;
+      pr.finish();
     }
   } else {
     Rows<T, HD, kPrefillTiles, true> rows;
@@ -115,8 +114,6 @@ __global__ void __launch_bounds__((kPrefillWarps + 1) * 32, CTAS)
       });
     }
   }
-  __syncthreads();
-  drain_copies(ring, issued);
 }
 
 template <typename T, int HD>

@@ -537,8 +537,9 @@ pkv_status pkv_paged_attention_decode_noalloc(const void* q, int32_t num_seqs, i
  *     new elements   x -> e4m3(x / s)  (nearest even; past 448: +-448; NaN: NaN)
  *     earlier rows   if s > s_old, their values move to the new scale:
  *                    e4m3(value * s_old / s)
- * Rows past the sequence's end are left as they were.  Results do not
- * depend on any order of execution.
+ * (s_old: a power of two, as every write leaves it.)  Rows past the
+ * sequence's end are left as they were.  Results do not depend on any order
+ * of execution.
  *
  *   k, v          [num_tokens, n_kv, head_dim] of `dtype`, 16-byte aligned
  *   block_tables  int32 [num_seqs, max_blocks_per_seq]; a block written to
@@ -586,6 +587,8 @@ pkv_status pkv_kv_gather_fp8(const void* k_pool, const void* v_pool, const float
  *   q, out      [num_seqs, n_heads, head_dim] of `dtype`, 16-byte aligned
  *   workspace   at least pkv_decode_fp8_workspace_bytes(...) bytes, 16-byte
  *               aligned; calls that may run at the same time need one each
+ *               (max_seq_len, max_ctas and block_size are taken for forward
+ *               compatibility)
  *   Supported: head_dim 16, 32, 64, 128; block_size 16; n_heads % n_kv == 0,
  *              n_heads / n_kv <= 16.
  */

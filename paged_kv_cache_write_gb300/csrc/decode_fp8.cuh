@@ -14,10 +14,10 @@
 // ahead of use, so their latency is off the path.
 //
 // Measured, bf16 queries, where a plain copy reaches 6.79 TB/s: 256 sequences
-// of 2,040 - 2,048 tokens, 8 KV heads: head_dim 128 163 us (6.6 TB/s), 64 88 us
-// (6.1 TB/s), 32 57 us (4.8 TB/s), 16 49 us (2.8 TB/s: the consumers' chains, the
+// of 2,040 - 2,048 tokens, 8 KV heads: head_dim 128 163 us (6.6 TB/s), 64 87 us
+// (6.2 TB/s), 32 58 us (4.7 TB/s), 16 51 us (2.7 TB/s: the consumers' chains, the
 // same for any width, bound narrow heads).  64 sequences of 512 - 2,048 tokens
-// of 8 x 64 (81 MB) 22 us, of which 12 stream; the rest is the plan (2 us),
+// of 8 x 64 (81 MB) 23 us, of which 12 stream; the rest is the plan (2 us),
 // the first scales and tile (2 us) and the joining launch (3 us, 1.2 of which an
 // empty one would take too).
 #pragma once
@@ -264,9 +264,11 @@ __device__ __forceinline__ void take_tiles(RowsT& rows, const Ring& ring, RingPo
 // CTAs of 8 consumer warps that an SM's registers hold.  A warp is a chain of
 // latencies (tile, scores, maximum, weights, product), some 900 cycles a block
 // whatever the head's width, and HBM brings a block of 8 x 64 in 720: narrow
-// heads run on two CTAs an SM, with half the ring each, at 96 registers (more
-// query rows or fp32's second terms would spill).  256 sequences of 2,048 tokens,
-// 8 KV heads: head_dim 64 97.4 -> 88.2 us, 32 80.8 -> 56.8, 16 71.5 -> 49.2.
+// heads run on two CTAs an SM, with half the ring each, at 96 registers (bf16 at
+// head_dim 64 spills 28 bytes there; more query rows or fp32's second terms at 64
+// would spill much more).  One CTA -> two when it was chosen, 256 sequences of
+// 2,048 tokens, 8 KV heads: head_dim 64 97.4 -> 88.2 us, 32 80.8 -> 56.8, 16 71.5 ->
+// 49.2.
 template <typename T, int HD, int NT>
 constexpr int kCtasPerSm = NT == 1 && HD * int(sizeof(T)) / 2 <= 64 ? 2 : 1;
 

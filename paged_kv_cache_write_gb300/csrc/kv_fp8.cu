@@ -13,9 +13,11 @@
 // bound by HBM for prompts and by their chain of dependent loads (offsets,
 // length, table entry, row) for a decode step.  Measured, where a plain copy
 // reaches 6.79 TB/s: writing 64 prompts of 1,000 - 2,000 tokens of 8 x 128 bf16
-// 89 us (6.6 TB/s; 31,722 tokens of 8 x 64: 23 us, 4.2 TB/s, whose start and
-// last CTAs show), reading back 64 sequences of 512 - 2,048 tokens of 8 x 64
-// 39 us (6.2 TB/s), a decode step's write or a toy read-back 3.2 - 3.5 us.
+// 89 us (6.6 TB/s), of 8 x 64 56 us (5.3), 31,722 tokens of 8 x 64 23 us (4.2:
+// start and last CTAs show; at 64 registers the bf16 kernels of heads of 16 - 64,
+// two units at a time, spill 48 bytes a thread), reading back 64 sequences of 512 -
+// 2,048 tokens of 8 x 64 39 us (6.2 TB/s; in fp32 66 us, 6.1), a decode step's
+// write or a toy read-back 3.3 - 3.7 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>

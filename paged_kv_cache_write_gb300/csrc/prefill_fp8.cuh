@@ -8,8 +8,8 @@
 // a ring that all of them read, up to the tile's last visible key.  Bound by
 // the consumers' conversions and products: each warp turns the block's e4m3
 // values into f16 for itself.  Measured, 4 chunks of 256 at the end of 1,000
-// tokens, 32 heads on 8: fp32 94 us at head_dim 64 (78 TFLOP/s) and 163 us at
-// 128, bf16 46 us at head_dim 32.
+// tokens, 32 heads on 8: fp32 96 us at head_dim 64 (76 TFLOP/s) and 146 us at
+// 128 (which spills 272 bytes a thread), bf16 46 us at head_dim 32.
 #pragma once
 
 #include "attention.cuh"
@@ -26,9 +26,10 @@ constexpr int kPrefillRows = 8 * kPrefillTiles;
 
 // CTAS: that an SM's registers hold.  Two, at 96 registers, hide each other's
 // latencies, but each is slower: for bf16 (narrow heads), where there are more CTAs
-// than SMs (4 chunks of 256 at the end of 1,000 tokens, 32 heads of 32 on 8: 46.4
-// us in place of 58.5; 6 chunks of 37, 8 heads of 16 on 4: 9.5 and 8.9).  fp32
-// would spill (4 chunks as above, heads of 128: 251 us for 163).
+// than SMs (when it was chosen: 4 chunks of 256 at the end of 1,000 tokens, 32
+// heads of 32 on 8: 46.4 us in place of 58.5; 6 chunks of 37, 8 heads of 16 on 4:
+// 9.5 and 8.9).  fp32 would spill several times what it does (4 chunks as above,
+// heads of 128: 251 us for 163).
 template <typename T, int HD, int CTAS>
 __global__ void __launch_bounds__((kPrefillWarps + 1) * 32, CTAS)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_k,

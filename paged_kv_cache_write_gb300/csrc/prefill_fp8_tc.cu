@@ -41,9 +41,9 @@
 // row tile, two on an SM, took 381 us for 214 (32 heads on 8, 4 chunks of 512
 // after 2,048 - 8,192 tokens of head_dim 128).
 //
-// Measured: 4 chunks of 512 after 0 - 4,096 tokens, 64 heads of 128 on 8,
-// 158 us (940 TFLOP/s); 2 chunks of 2,048 ending at 8,192, 829 us (1,161);
-// head_dim 64, 32 heads on 8, 4 chunks of 1,024 ending at 4,096, 233 us (516).
+// Measured: 4 chunks of 512 after 990 - 3,018 tokens, 64 heads of 128 on 8,
+// 159 us (936 TFLOP/s); 2 chunks of 2,048 ending at 8,192, 823 us (1,168);
+// head_dim 64, 32 heads on 8, 4 chunks of 1,024 ending at 4,096, 226 us (533).
 // Bound by the softmax warps, some 1,800 cycles a key tile of 64 (MMAs: 1,330 at
 // head_dim 128), and by 10,000 cycles of each CTA that are not its loop: work
 // order 2,500, set-up 500, queries 3,000 - 6,000, first scores 1,500, output

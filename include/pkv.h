@@ -18,7 +18,10 @@
  * pkv_paged_attention_decode_noalloc (decode without a caller workspace),
  * the 8-bit cache (pkv_kv_write_fp8, pkv_kv_gather_fp8,
  * pkv_paged_attention_decode_fp8, pkv_paged_attention_prefill_fp8: e4m3 pools
- * with a scale per block and KV head), the workspace size queries,
+ * with a scale per block and KV head), the norm and rotation of queries and
+ * keys before the cache (pkv_qk_norm_rope, pkv_qk_norm_rope_write), the 4-bit
+ * cache (pkv_kv_write_fp4, pkv_qk_norm_rope_write_fp4, pkv_kv_gather_fp4: e2m1
+ * pools with a scale per 16 elements), the workspace size queries,
  * pkv_status_string, pkv_abi_version, pkv_selftest_bounded_wait and
  * pkv_selftest_bounded_wait_fp8 (the kernels' bounded-wait failure path).
  *
@@ -37,8 +40,9 @@
  *
  * Conventions shared by every call
  * --------------------------------
- *  Memory.  Every pointer argument except `pool` (a host struct) is DEVICE
- *  memory owned by the caller, contiguous and row-major.  Tensors read or
+ *  Memory.  Every pointer argument except `pool` and `rope` (host structs) is
+ *  DEVICE memory owned by the caller, contiguous and row-major (but for the
+ *  token strides that some entries take).  Tensors read or
  *  written as 16-byte vectors (q, k, v, pools, out) must be 16-byte
  *  aligned.  The library never allocates device memory and never
  *  synchronises the device.  The only state it keeps between calls is
@@ -102,8 +106,10 @@ typedef enum pkv_status {
 typedef enum pkv_dtype {
   PKV_F32 = 0,   /* IEEE binary32 */
   PKV_BF16 = 1,  /* bfloat16; attention accumulates in fp32, rounds RNE   */
-  PKV_FP8_E4M3 = 2  /* pools of the pkv_*_fp8 entries alone: e4m3 with a
+  PKV_FP8_E4M3 = 2, /* pools of the pkv_*_fp8 entries alone: e4m3 with a
                        scale per block and KV head (see pkv_kv_write_fp8) */
+  PKV_FP4_E2M1 = 3  /* pools of the pkv_*_fp4 entries alone: e2m1 with e4m3
+                       scales (see pkv_kv_write_fp4)                      */
 } pkv_dtype;
 
 /* Bits OR-ed into *err_word by kernels that meet bad device-resident data. */
@@ -632,6 +638,154 @@ pkv_status pkv_paged_attention_prefill_fp8(
     const float* k_scales, const float* v_scales, const pkv_pool_desc* pool,
     const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
     int32_t max_seq_len, float scale, void* out, int32_t* err_word, void* stream);
+
+/*
+ * Queries, keys and values on their way into the cache.
+ *
+ * "Build a Mini vLLM" section 4 stores each token's keys after the model has
+ * rotated them by position; models of later families also bring each head's
+ * query and key to unit mean square first.  Both are done here in one pass over
+ * the projection's output, and the keys and values can go straight to their
+ * slots.
+ */
+
+/* What the norm and the rotation take (host struct, device pointers). */
+typedef struct pkv_norm_rope_desc {
+  const void* q_weight;      /* [head_dim] of the rows' dtype, or NULL: no norm   */
+  const void* k_weight;      /* the same for keys                                 */
+  float eps;                 /* >= 0 and finite (used where there is a weight)    */
+  int32_t rot_dim;           /* leading dims of a head that turn: a multiple of
+                                16, 16 .. head_dim                                */
+  int32_t interleaved;       /* 0: dim i turns with i + rot_dim / 2;
+                                1: dim 2i turns with 2i + 1                       */
+  int32_t num_positions;     /* rows of cos_sin                                   */
+  const float* cos_sin;      /* fp32 [num_positions, rot_dim]: a position's
+                                rot_dim / 2 cosines, then its sines               */
+  const int32_t* positions;  /* int32 [num_tokens]                                */
+} pkv_norm_rope_desc;
+
+/*
+ * pkv_qk_norm_rope - norm and rotation of a step's queries and keys.
+ *
+ * For every token and head, with x the head's row and w its kind's weight:
+ *     z = x * (1 / sqrt(mean(x^2) + eps)) * w          (z = x without a weight)
+ *     y[i]  = z[i]  cos - z[i'] sin,  y[i'] = z[i'] cos + z[i] sin
+ * for the pairs (i, i') of the first rot_dim dims, with the cosine and sine of
+ * the pair at the token's position; the other dims are z.  In fp32, rounded once
+ * to the rows' type.
+ *
+ *   q, k        [num_tokens, heads, head_dim] of `dtype` (PKV_F32 or PKV_BF16), a
+ *               token's heads contiguous; *_stride: elements from a token to the
+ *               next (the rows may be parts of one projection's output).  Row
+ *               addresses and strides are multiples of 16 bytes.
+ *   q_out, k_out  the results, with strides of their own.  They may be q and k
+ *               themselves (same address and stride), and must not overlap them
+ *               otherwise.
+ *   A token whose position is outside [0, num_positions) is reported
+ *   (PKV_DEVERR_LENGTH) and gets zeros.
+ *   Supported: head_dim a multiple of 16 up to 256.
+ */
+pkv_status pkv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            int32_t dtype, int32_t num_tokens, int32_t n_heads, int32_t n_kv,
+                            int32_t head_dim, const pkv_norm_rope_desc* rope, void* q_out,
+                            int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                            int32_t* err_word, void* stream);
+
+/*
+ * pkv_qk_norm_rope_write - the same, with the keys' results and the values v
+ * written to their slots of a pool of the rows' type (pool->dtype), as
+ * pkv_kv_write: a negative slot skips a token's key and value, one past the pool
+ * is reported.  Equal bit for bit to pkv_qk_norm_rope and pkv_kv_write.  A token
+ * with a bad position stores nothing.
+ */
+pkv_status pkv_qk_norm_rope_write(const void* q, int64_t q_stride, const void* k,
+                                  int64_t k_stride, const void* v, int64_t v_stride,
+                                  int32_t num_tokens, int32_t n_heads,
+                                  const pkv_norm_rope_desc* rope, void* q_out,
+                                  int64_t q_out_stride, const int64_t* slot_mapping, void* k_pool,
+                                  void* v_pool, const pkv_pool_desc* pool, int32_t* err_word,
+                                  void* stream);
+
+/*
+ * The 4-bit cache.
+ *
+ * Half the bytes of the 8-bit cache, nearly: 9 / 16 byte an element.  An element
+ * stands for e2m1 x s x g:
+ *   - its e2m1 code, four bits (sign; 0 .5 1 1.5 2 3 4 6), two to a byte, the even
+ *     element in the low half: pools uint8 [num_blocks, n_kv, block_size,
+ *     head_dim / 2];
+ *   - s, the e4m3 scale of the 16 elements of its row that it is one of: k_groups,
+ *     v_groups [num_blocks, n_kv, block_size, head_dim / 16];
+ *   - g, the scale of its KV head for the whole cache: k_scale, v_scale fp32 [n_kv],
+ *     powers of two in 2^-60 .. 2^60 (an argument of every entry, chosen by the
+ *     caller so that a row's largest elements, over 6 g, lie well within e4m3's
+ *     2^-6 .. 448).  The reading entries take any positive finite g in those
+ *     bounds.
+ * A head's rows of a block lie together, so that whole blocks of any number of
+ * heads start on 16 bytes.  Pools and groups are 16-byte aligned.
+ *
+ * pool->dtype is PKV_FP4_E2M1, pool->head_dim counts elements: a multiple of 16 up
+ * to 256 (attention: 16, 32, 64 or 128, with block_size 16); n_kv at most 65,535;
+ * num_blocks * block_size below 2^31.  `dtype` is the type of k, v, q and the
+ * outputs (PKV_F32 or PKV_BF16).
+ *
+ * A block is copied on write with two pkv_copy_blocks calls: one on the pools
+ * described as bf16 with head_dim / 4 (the bytes are copied as they are), one on
+ * the groups described as fp32 blocks of one token, one head and n_kv * head_dim *
+ * block_size / 64.
+ */
+
+/*
+ * pkv_kv_write_fp4 - quantise this step's new K and V into a 4-bit cache.
+ *
+ * The 4-bit pkv_kv_write.  For each token with slot_mapping[t] >= 0, each KV head,
+ * K and V each for itself and each 16 consecutive elements x, with a the largest
+ * |x / g|:
+ *     s = the e4m3 value nearest to a / 6 (ties to the even byte; at most 448)
+ *     code of x = the e2m1 value nearest to x / (g s) (ties to the even code; at
+ *                 most 6; s = 0: zeros), with the sign of x
+ * as on exact quotients.  A group with a NaN gets the scale NaN and reads back as
+ * NaN; past 2,688 g values saturate.  A token's codes depend on that token alone:
+ * results depend on no order, and rows that no token goes to are left as they were.
+ * Slots must be distinct within one call (but negative ones).
+ *
+ *   k, v          [num_tokens, n_kv, head_dim] of `dtype`; *_stride as for
+ *                 pkv_qk_norm_rope
+ *   slot_mapping  int64 [num_tokens], as for pkv_kv_write
+ */
+pkv_status pkv_kv_write_fp4(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                            int32_t dtype, const int64_t* slot_mapping, int32_t num_tokens,
+                            void* k_pool, void* v_pool, void* k_groups, void* v_groups,
+                            const float* k_scale, const float* v_scale, const pkv_pool_desc* pool,
+                            int32_t* err_word, void* stream);
+
+/*
+ * pkv_qk_norm_rope_write_fp4 - pkv_qk_norm_rope_write into a 4-bit cache.  Equal bit
+ * for bit to pkv_qk_norm_rope and pkv_kv_write_fp4: the keys are rounded to the
+ * rows' type first.
+ */
+pkv_status pkv_qk_norm_rope_write_fp4(const void* q, int64_t q_stride, const void* k,
+                                      int64_t k_stride, const void* v, int64_t v_stride,
+                                      int32_t dtype, int32_t num_tokens, int32_t n_heads,
+                                      const pkv_norm_rope_desc* rope, void* q_out,
+                                      int64_t q_out_stride, const int64_t* slot_mapping,
+                                      void* k_pool, void* v_pool, void* k_groups, void* v_groups,
+                                      const float* k_scale, const float* v_scale,
+                                      const pkv_pool_desc* pool, int32_t* err_word, void* stream);
+
+/*
+ * pkv_kv_gather_fp4 - read a 4-bit cache back: pkv_kv_gather with every code times
+ * its scales, in `dtype` (rounded nowhere where g is a power of two).  The outputs
+ * may be blocks of a bf16 or fp32 pool: no later kernel starts before they are
+ * written.
+ */
+pkv_status pkv_kv_gather_fp4(const void* k_pool, const void* v_pool, const void* k_groups,
+                             const void* v_groups, const float* k_scale, const float* v_scale,
+                             const pkv_pool_desc* pool, const int32_t* block_tables,
+                             int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                             const int32_t* cu_seq_lens, int32_t num_seqs, int32_t total_tokens,
+                             int32_t dtype, void* k_out, void* v_out, int32_t* err_word,
+                             void* stream);
 
 /*
  * pkv_selftest_bounded_wait - check the kernels' failure path on this GPU.

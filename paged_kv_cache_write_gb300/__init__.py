@@ -27,7 +27,8 @@ __all__ = [
     "paged_attention_prefill", "status_string", "abi_version", "paged_attention_decode_noalloc",
     "selftest_bounded_wait", "PKV_FP8_E4M3", "kv_write_fp8", "kv_gather_fp8",
     "decode_fp8_workspace_bytes", "paged_attention_decode_fp8", "paged_attention_prefill_fp8",
-    "selftest_bounded_wait_fp8",
+    "selftest_bounded_wait_fp8", "PKV_FP4_E2M1", "NormRopeDesc", "qk_norm_rope",
+    "qk_norm_rope_write", "qk_norm_rope_write_fp4", "kv_write_fp4", "kv_gather_fp4",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -36,6 +37,7 @@ library_path = os.path.join(HERE, "libpkv.so")
 PKV_F32 = 0
 PKV_BF16 = 1
 PKV_FP8_E4M3 = 2
+PKV_FP4_E2M1 = 3
 DEVERR = {"block_id": 1, "slot": 2, "table_width": 4, "length": 8, "timeout": 16, "prefix": 32,
           "plan": 64}
 
@@ -46,12 +48,21 @@ class PoolDesc(ctypes.Structure):
                 ("dtype", ctypes.c_int32)]
 
 
+class NormRopeDesc(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("num_positions", ctypes.c_int32), ("cos_sin", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p)]
+
+
 _lib = None
 _p = ctypes.c_void_p
 _i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
 _f = ctypes.c_float
 _desc = ctypes.POINTER(PoolDesc)
+_turn = ctypes.POINTER(NormRopeDesc)
 
 
 def _load():
@@ -119,6 +130,21 @@ def _load():
     L.pkv_paged_attention_prefill_fp8.restype = _i32
     L.pkv_paged_attention_prefill_fp8.argtypes = [_p, _i32, _p, _i32, _i32, _i32, _i32, _p, _p, _p,
                                                   _p, _desc, _p, _i32, _p, _i32, _f, _p, _p, _p]
+    L.pkv_qk_norm_rope.restype = _i32
+    L.pkv_qk_norm_rope.argtypes = [_p, _i64, _p, _i64, _i32, _i32, _i32, _i32, _i32, _turn, _p, _i64,
+                                   _p, _i64, _p, _p]
+    L.pkv_qk_norm_rope_write.restype = _i32
+    L.pkv_qk_norm_rope_write.argtypes = [_p, _i64, _p, _i64, _p, _i64, _i32, _i32, _turn, _p, _i64, _p,
+                                         _p, _p, _desc, _p, _p]
+    L.pkv_qk_norm_rope_write_fp4.restype = _i32
+    L.pkv_qk_norm_rope_write_fp4.argtypes = [_p, _i64, _p, _i64, _p, _i64, _i32, _i32, _i32, _turn, _p,
+                                             _i64, _p, _p, _p, _p, _p, _p, _p, _desc, _p, _p]
+    L.pkv_kv_write_fp4.restype = _i32
+    L.pkv_kv_write_fp4.argtypes = [_p, _i64, _p, _i64, _i32, _p, _i32, _p, _p, _p, _p, _p, _p, _desc,
+                                   _p, _p]
+    L.pkv_kv_gather_fp4.restype = _i32
+    L.pkv_kv_gather_fp4.argtypes = [_p, _p, _p, _p, _p, _p, _desc, _p, _i32, _p, _p, _i32, _i32, _i32,
+                                    _p, _p, _p, _p]
     _lib = L
     return L
 
@@ -705,3 +731,253 @@ def selftest_bounded_wait_fp8(err, polls: int = 64, *, stream=None):
     warp gives up together."""
     _check("pkv_selftest_bounded_wait_fp8", _load().pkv_selftest_bounded_wait_fp8(
         int(polls), _dev(err, "err", torch.int32), _stream(stream)))
+
+
+# ------------------------------------- queries and keys before the cache
+#
+# Rows [tokens, heads, head_dim] may be parts of one projection's output: a
+# token's heads lie together, tokens any multiple of 16 bytes apart.
+
+_u8 = torch.uint8
+
+
+def _row_ptr(t, name, dtype, index, shape=None):
+    """(address, token stride in elements) of rows [tokens, heads, head_dim]."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 3 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be {shape or '[tokens, heads, head_dim]'}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the call on cuda:{index}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    T, H, hd = t.shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (H > 1 and s1 != hd):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.data_ptr(), s0 if T > 1 else H * hd
+
+
+def _index_of(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    return index
+
+
+def _norm_rope(cos_sin, positions, q_weight, k_weight, eps, interleaved, tokens, head_dim, dtype, index):
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [num_positions, rot_dim]")
+    if tuple(positions.shape) != (tokens,):
+        raise ValueError(f"positions must be {(tokens,)}: one per token")
+    at = []
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and tuple(w.shape) != (head_dim,):
+            raise ValueError(f"{name} must be {(head_dim,)}")
+        at.append(None if w is None else _ptr(w, name, dtype, index))
+    return NormRopeDesc(at[0], at[1], float(eps), cos_sin.shape[1], int(bool(interleaved)),
+                        cos_sin.shape[0], _ptr(cos_sin, "cos_sin", _f32, index),
+                        _ptr(positions, "positions", _int, index))
+
+
+def _slots(slot_mapping, tokens, index):
+    if tuple(slot_mapping.shape) != (tokens,):
+        raise ValueError(f"slot_mapping must be {(tokens,)}: one entry per token")
+    return _ptr(slot_mapping, "slot_mapping", torch.int64, index)
+
+
+def _rows_like(t):
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def qk_norm_rope(q, k, cos_sin, positions, *, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out=None, k_out=None, err=None, stream=None):
+    """Norm and rotation of a step's queries [T, n_heads, head_dim] and keys
+    [T, n_kv, head_dim] (float32 or bfloat16); returns both.
+
+    With a weight [head_dim], each head's row is first divided by its root mean
+    square (``eps`` inside the root) and multiplied by the weight.  The first
+    ``rot_dim`` dims are then turned by the angles of the token's row of
+    ``cos_sin``, float32 [num_positions, rot_dim] (cosines, then sines): dim i with
+    i + rot_dim / 2, or 2i with 2i + 1 where ``interleaved``.  ``positions`` is int32
+    [T].  All in fp32, rounded once.  Rows may be views of one projection's output;
+    ``q_out`` / ``k_out`` may be ``q`` / ``k`` themselves.
+    """
+    i = _index_of(q, "q")
+    there = _context(stream, i)
+    if there is not None:
+        with there:
+            return qk_norm_rope(q, k, cos_sin, positions, q_weight=q_weight, k_weight=k_weight, eps=eps,
+                                interleaved=interleaved, q_out=q_out, k_out=k_out, err=err)
+    dt = q.dtype
+    qp, qs = _row_ptr(q, "q", dt, i)
+    T, H, hd = q.shape
+    kp, ks = _row_ptr(k, "k", dt, i)
+    if k.shape[0] != T or k.shape[2] != hd:
+        raise ValueError("k must be [T, n_kv, head_dim] with q's tokens and head_dim")
+    turn = _norm_rope(cos_sin, positions, q_weight, k_weight, eps, interleaved, T, hd, dt, i)
+    q_out = _rows_like(q) if q_out is None else q_out
+    k_out = _rows_like(k) if k_out is None else k_out
+    qo, qos = _row_ptr(q_out, "q_out", dt, i, tuple(q.shape))
+    ko, kos = _row_ptr(k_out, "k_out", dt, i, tuple(k.shape))
+    status = (_lib or _load()).pkv_qk_norm_rope(
+        qp, qs, kp, ks, _type_code(dt), T, H, k.shape[1], hd, ctypes.byref(turn), qo, qos, ko, kos,
+        None if err is None else _ptr(err, "err", _int, i), _raw_stream(i))
+    if status:
+        raise PkvError("pkv_qk_norm_rope", status)
+    return q_out, k_out
+
+
+def qk_norm_rope_write(q, k, v, cos_sin, positions, slot_mapping, k_pool, v_pool, *, q_weight=None,
+                       k_weight=None, eps: float = 1e-6, interleaved: bool = False, q_out=None,
+                       err=None, stream=None):
+    """:func:`qk_norm_rope`, its keys and the values ``v`` [T, n_kv, head_dim] written
+    to their slots as by :func:`kv_write`, in one launch; returns the queries."""
+    i = _index_of(k_pool, "k_pool")
+    there = _context(stream, i)
+    if there is not None:
+        with there:
+            return qk_norm_rope_write(q, k, v, cos_sin, positions, slot_mapping, k_pool, v_pool,
+                                      q_weight=q_weight, k_weight=k_weight, eps=eps,
+                                      interleaved=interleaved, q_out=q_out, err=err)
+    desc = pool_desc(k_pool)
+    dt = k_pool.dtype
+    if v_pool.shape != k_pool.shape:
+        raise ValueError("k_pool and v_pool must have the same shape")
+    qp, qs = _row_ptr(q, "q", dt, i)
+    T, H, hd = q.shape
+    if hd != desc.head_dim:
+        raise ValueError("q must be [T, n_heads, head_dim] with the pool's head_dim")
+    shape = (T, desc.n_kv, hd)
+    kp, ks = _row_ptr(k, "k", dt, i, shape)
+    vp, vs = _row_ptr(v, "v", dt, i, shape)
+    turn = _norm_rope(cos_sin, positions, q_weight, k_weight, eps, interleaved, T, hd, dt, i)
+    q_out = _rows_like(q) if q_out is None else q_out
+    qo, qos = _row_ptr(q_out, "q_out", dt, i, tuple(q.shape))
+    status = (_lib or _load()).pkv_qk_norm_rope_write(
+        qp, qs, kp, ks, vp, vs, T, H, ctypes.byref(turn), qo, qos, _slots(slot_mapping, T, i),
+        _ptr(k_pool, "k_pool", dt, i), _ptr(v_pool, "v_pool", dt, i), ctypes.byref(desc),
+        None if err is None else _ptr(err, "err", _int, i), _raw_stream(i))
+    if status:
+        raise PkvError("pkv_qk_norm_rope_write", status)
+    return q_out
+
+
+# ------------------------------------------------------------ 4-bit cache
+
+def _fp4_pool(k_pool, v_pool, k_groups, v_groups, k_scale, v_scale):
+    """Device, descriptor and addresses of a 4-bit cache, its six tensors checked."""
+    shape = k_pool.shape
+    if len(shape) != 4:
+        raise ValueError("pool must be [num_blocks, n_kv, block_size, head_dim / 2]")
+    if v_pool.shape != shape:
+        raise ValueError("k_pool and v_pool must have the same shape")
+    nb, nkv, bs, half = shape
+    per = (nb, nkv, bs, half // 8)
+    if half % 8 or tuple(k_groups.shape) != per or tuple(v_groups.shape) != per:
+        raise ValueError(f"k_groups and v_groups must be {per}: one per 16 elements")
+    if tuple(k_scale.shape) != (nkv,) or tuple(v_scale.shape) != (nkv,):
+        raise ValueError(f"k_scale and v_scale must be {(nkv,)}: one per KV head")
+    index = _index_of(k_pool, "k_pool")
+    return (index, PoolDesc(nb, bs, nkv, 2 * half, PKV_FP4_E2M1),
+            (_ptr(k_pool, "k_pool", _u8, index), _ptr(v_pool, "v_pool", _u8, index),
+             _ptr(k_groups, "k_groups", _f8, index), _ptr(v_groups, "v_groups", _f8, index),
+             _ptr(k_scale, "k_scale", _f32, index), _ptr(v_scale, "v_scale", _f32, index)))
+
+
+def kv_write_fp4(k, v, slot_mapping, k_pool, v_pool, k_groups, v_groups, k_scale, v_scale, *, err=None,
+                 stream=None):
+    """Quantise k/v [T, n_kv, head_dim] (float32 or bfloat16) into a 4-bit cache at
+    slot_mapping [T]: pools of e2m1 codes, two to a byte, uint8 [num_blocks, n_kv,
+    block_size, head_dim / 2]; a ``torch.float8_e4m3fn`` scale per 16 elements of a
+    row, [num_blocks, n_kv, block_size, head_dim / 16]; and a float32 scale per KV
+    head, a power of two, [n_kv], which the caller chooses once for the cache.
+
+    A token's codes depend on that token alone.  Values past 2,688 x its head's
+    scale saturate; a group's scale loses precision below 0.1 x it.
+    """
+    i, desc, cache = _fp4_pool(k_pool, v_pool, k_groups, v_groups, k_scale, v_scale)
+    there = _context(stream, i)
+    if there is not None:
+        with there:
+            return kv_write_fp4(k, v, slot_mapping, k_pool, v_pool, k_groups, v_groups, k_scale,
+                                v_scale, err=err)
+    dt = k.dtype
+    T = k.shape[0]
+    shape = (T, desc.n_kv, desc.head_dim)
+    kp, ks = _row_ptr(k, "k", dt, i, shape)
+    vp, vs = _row_ptr(v, "v", dt, i, shape)
+    status = (_lib or _load()).pkv_kv_write_fp4(
+        kp, ks, vp, vs, _type_code(dt), _slots(slot_mapping, T, i), T, *cache, ctypes.byref(desc),
+        None if err is None else _ptr(err, "err", _int, i), _raw_stream(i))
+    if status:
+        raise PkvError("pkv_kv_write_fp4", status)
+
+
+def qk_norm_rope_write_fp4(q, k, v, cos_sin, positions, slot_mapping, k_pool, v_pool, k_groups,
+                           v_groups, k_scale, v_scale, *, q_weight=None, k_weight=None,
+                           eps: float = 1e-6, interleaved: bool = False, q_out=None, err=None,
+                           stream=None):
+    """:func:`qk_norm_rope`, its keys and the values ``v`` quantised into a 4-bit cache
+    as by :func:`kv_write_fp4`, in one launch; returns the queries."""
+    i, desc, cache = _fp4_pool(k_pool, v_pool, k_groups, v_groups, k_scale, v_scale)
+    there = _context(stream, i)
+    if there is not None:
+        with there:
+            return qk_norm_rope_write_fp4(q, k, v, cos_sin, positions, slot_mapping, k_pool, v_pool,
+                                          k_groups, v_groups, k_scale, v_scale, q_weight=q_weight,
+                                          k_weight=k_weight, eps=eps, interleaved=interleaved,
+                                          q_out=q_out, err=err)
+    dt = q.dtype
+    qp, qs = _row_ptr(q, "q", dt, i)
+    T, H, hd = q.shape
+    if hd != desc.head_dim:
+        raise ValueError("q must be [T, n_heads, head_dim] with the pool's head_dim")
+    shape = (T, desc.n_kv, hd)
+    kp, ks = _row_ptr(k, "k", dt, i, shape)
+    vp, vs = _row_ptr(v, "v", dt, i, shape)
+    turn = _norm_rope(cos_sin, positions, q_weight, k_weight, eps, interleaved, T, hd, dt, i)
+    q_out = _rows_like(q) if q_out is None else q_out
+    qo, qos = _row_ptr(q_out, "q_out", dt, i, tuple(q.shape))
+    status = (_lib or _load()).pkv_qk_norm_rope_write_fp4(
+        qp, qs, kp, ks, vp, vs, _type_code(dt), T, H, ctypes.byref(turn), qo, qos,
+        _slots(slot_mapping, T, i), *cache, ctypes.byref(desc),
+        None if err is None else _ptr(err, "err", _int, i), _raw_stream(i))
+    if status:
+        raise PkvError("pkv_qk_norm_rope_write_fp4", status)
+    return q_out
+
+
+def kv_gather_fp4(k_pool, v_pool, k_groups, v_groups, k_scale, v_scale, block_tables, seq_lens,
+                  cu_seq_lens, total_tokens: int, *, dtype=torch.bfloat16, k_out=None, v_out=None,
+                  err=None, stream=None):
+    """Contiguous [total_tokens, n_kv, head_dim] K and V of a 4-bit cache in logical
+    order, each code times its scales, in ``dtype`` (float32 or bfloat16; that of
+    ``k_out`` / ``v_out`` where given)."""
+    i, desc, cache = _fp4_pool(k_pool, v_pool, k_groups, v_groups, k_scale, v_scale)
+    there = _context(stream, i)
+    if there is not None:
+        with there:
+            return kv_gather_fp4(k_pool, v_pool, k_groups, v_groups, k_scale, v_scale, block_tables,
+                                 seq_lens, cu_seq_lens, total_tokens, dtype=dtype, k_out=k_out,
+                                 v_out=v_out, err=err)
+    B, W = _batch(block_tables, seq_lens)
+    dt = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else dtype
+    code = _type_code(dt)
+    shape = (int(total_tokens), desc.n_kv, desc.head_dim)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dt, device=k_pool.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dt, device=k_pool.device)
+    if k_out.shape != shape or v_out.shape != shape:
+        raise ValueError(f"k_out, v_out must be {shape}")
+    status = (_lib or _load()).pkv_kv_gather_fp4(
+        *cache, ctypes.byref(desc), _ptr(block_tables, "block_tables", _int, i), W,
+        _ptr(seq_lens, "seq_lens", _int, i), _offsets(cu_seq_lens, "cu_seq_lens", B, i), B, shape[0],
+        code, _ptr(k_out, "k_out", dt, i), _ptr(v_out, "v_out", dt, i),
+        None if err is None else _ptr(err, "err", _int, i), _raw_stream(i))
+    if status:
+        raise PkvError("pkv_kv_gather_fp4", status)
+    return k_out, v_out

@@ -49,6 +49,31 @@ inline pkv_status check_pool_fp8(const pkv_pool_desc* pool, PoolShape* out) {
   return PKV_OK;
 }
 
+// The descriptor of a 4-bit pool: positive sizes, rows of whole groups, a KV head
+// that fits a grid's y, slots that fit in int32.
+inline pkv_status check_pool_fp4(const pkv_pool_desc* pool, PoolShape* out) {
+  if (pool == nullptr) return PKV_ERR_NULL;
+  if (pool->dtype != PKV_FP4_E2M1) return PKV_ERR_DTYPE;
+  if (pool->num_blocks <= 0 || pool->block_size <= 0 || pool->n_kv <= 0 || pool->head_dim <= 0)
+    return PKV_ERR_SHAPE;
+  if (pool->head_dim % 16 != 0 || pool->head_dim > 256) return PKV_ERR_UNSUPPORTED;
+  if (pool->n_kv > 65535 || (int64_t)pool->num_blocks * pool->block_size > INT32_MAX)
+    return PKV_ERR_RANGE;
+  *out = PoolShape{pool->num_blocks, pool->block_size, pool->n_kv, pool->head_dim, pool->dtype};
+  return PKV_OK;
+}
+
+// Rows [num_tokens, heads, head_dim] with a token stride in elements.
+inline pkv_status check_rows(const void* p, int64_t stride, int32_t num_tokens, int32_t heads,
+                             int32_t head_dim, int32_t dtype) {
+  if (p == nullptr) return PKV_ERR_NULL;
+  const int es = dtype == PKV_F32 ? 4 : 2;
+  if (num_tokens > 1 && stride < (int64_t)heads * head_dim) return PKV_ERR_SHAPE;
+  if (stride > INT64_MAX / 4 / num_tokens) return PKV_ERR_RANGE;
+  if (!aligned16(p) || (num_tokens > 1 && stride * es % 16 != 0)) return PKV_ERR_ALIGN;
+  return PKV_OK;
+}
+
 // Arguments common to decode and prefill attention, the pool already
 // checked.  num_seqs == 0 passes before the pointer checks (nothing will be
 // read).

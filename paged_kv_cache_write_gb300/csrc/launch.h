@@ -52,6 +52,42 @@ cudaError_t launch_kv_gather_fp8(const void* k_pool, const void* v_pool, const f
                                  int32_t num_seqs, int32_t total_tokens, int32_t dtype,
                                  void* k_out, void* v_out, int32_t* err, cudaStream_t stream);
 
+// Norm, rotation and write of a step's rows (qk_norm_rope.cu).  Strides in elements,
+// from a token to the next.  No cos_sin: rows are stored as they are; no slots: keys
+// go to k_out and there are no values; k_groups: the pools are 4-bit ones.
+struct NormRopeArgs {
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  void *q_out, *k_out;
+  int64_t q_out_stride, k_out_stride;
+  const int64_t* slots;
+  void *k_pool, *v_pool;
+  uint8_t *k_groups, *v_groups;
+  const float *k_scale, *v_scale;
+  const void *q_weight, *k_weight;
+  const float* cos_sin;
+  const int32_t* positions;
+  int32_t* err;
+  int64_t num_slots;
+  float eps;
+  int32_t num_tokens, n_heads, n_kv, head_dim, rot, num_positions, block_size, dtype;
+  bool interleaved;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
+// Most tokens of a call whose tokens have `rows` rows.
+int64_t norm_rope_max_tokens(int32_t rows, int32_t head_dim);
+
+// A 4-bit cache.
+struct Fp4Cache {
+  const void *k_pool, *v_pool, *k_groups, *v_groups;
+  const float *k_scale, *v_scale;
+};
+cudaError_t launch_kv_gather_fp4(const Fp4Cache& c, const PoolShape& pool,
+                                 const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                 const int32_t* seq_lens, const int32_t* cu_seq_lens,
+                                 int32_t num_seqs, int32_t total_tokens, int32_t dtype,
+                                 void* k_out, void* v_out, int32_t* err, cudaStream_t stream);
+
 // Attention problem shared by decode and prefill.
 struct AttnArgs {
   const void* q;

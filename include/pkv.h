@@ -20,8 +20,9 @@
  * pkv_paged_attention_decode_fp8, pkv_paged_attention_prefill_fp8: e4m3 pools
  * with a scale per block and KV head), the norm and rotation of queries and
  * keys before the cache (pkv_qk_norm_rope, pkv_qk_norm_rope_write), the 4-bit
- * cache (pkv_kv_write_fp4, pkv_qk_norm_rope_write_fp4, pkv_kv_gather_fp4: e2m1
- * pools with a scale per 16 elements), the workspace size queries,
+ * cache (pkv_kv_write_fp4, pkv_qk_norm_rope_write_fp4, pkv_kv_gather_fp4,
+ * pkv_paged_attention_decode_fp4, pkv_paged_attention_prefill_fp4: e2m1 pools
+ * with a scale per 16 elements), the workspace size queries,
  * pkv_status_string, pkv_abi_version, pkv_selftest_bounded_wait and
  * pkv_selftest_bounded_wait_fp8 (the kernels' bounded-wait failure path).
  *
@@ -786,6 +787,55 @@ pkv_status pkv_kv_gather_fp4(const void* k_pool, const void* v_pool, const void*
                              const int32_t* cu_seq_lens, int32_t num_seqs, int32_t total_tokens,
                              int32_t dtype, void* k_out, void* v_out, int32_t* err_word,
                              void* stream);
+
+/*
+ * pkv_paged_attention_decode_fp4 - pkv_paged_attention_decode over a 4-bit cache: one
+ * query token per sequence attends to its whole history, read in place.  seq_lens[b]
+ * counts this step's token (write it first).  A sequence of length 0 gets zeros; slots
+ * past the length are never used, whatever bytes they hold.
+ *
+ * The work split, and with it what results depend on, is that of
+ * pkv_paged_attention_decode: logical positions, lengths and max_ctas, never physical
+ * block ids; identical calls give identical bits.  Keys and values enter exactly (code
+ * times group scale, the head's scale in the score and the output); scores, softmax
+ * sums and outputs are held in fp32.  For bf16, weights are rounded to 11 significand
+ * bits before they multiply V; for fp32 queries and weights keep 22.  A query element
+ * more than 2^28 below its row's largest loses bits.
+ *
+ *   q, out      [num_seqs, n_heads, head_dim] of `dtype`, 16-byte aligned
+ *   workspace   at least pkv_decode_fp4_workspace_bytes(...) bytes, 16-byte aligned;
+ *               calls that may run at the same time need one each (max_seq_len,
+ *               max_ctas and block_size are taken for forward compatibility)
+ *   Supported: head_dim 16, 32, 64, 128; block_size 16; n_heads % n_kv == 0,
+ *              n_heads / n_kv <= 16; max_blocks_per_seq * block_size below 2^31.
+ */
+size_t pkv_decode_fp4_workspace_bytes(int32_t num_seqs, int32_t n_heads, int32_t head_dim,
+                                      int32_t max_seq_len, int32_t max_ctas, int32_t block_size);
+
+pkv_status pkv_paged_attention_decode_fp4(
+    const void* q, int32_t dtype, int32_t num_seqs, int32_t n_heads, const void* k_pool,
+    const void* v_pool, const void* k_groups, const void* v_groups, const float* k_scale,
+    const float* v_scale, const pkv_pool_desc* pool, const int32_t* block_tables,
+    int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t max_seq_len, float scale,
+    int32_t max_ctas, void* out, void* workspace, size_t workspace_bytes, int32_t* err_word,
+    void* stream);
+
+/*
+ * pkv_paged_attention_prefill_fp4 - pkv_paged_attention_prefill over a 4-bit cache:
+ * causal attention of each sequence's query chunk over its paged history (the chunk's
+ * own K/V written first).  A key or value that a query may not see does not reach its
+ * output, NaN included.  It needs no workspace.  Precision as for the decode, but that
+ * with bf16 queries weights below 2^-18 of a row's largest are rounded to fewer than 11
+ * bits.  cu_q_lens, and which rows are left as they were, as for
+ * pkv_paged_attention_prefill_fp8; supported shapes as for the decode.
+ */
+pkv_status pkv_paged_attention_prefill_fp4(
+    const void* q, int32_t dtype, const int32_t* cu_q_lens, int32_t num_seqs, int32_t total_q,
+    int32_t max_q_len, int32_t n_heads, const void* k_pool, const void* v_pool,
+    const void* k_groups, const void* v_groups, const float* k_scale, const float* v_scale,
+    const pkv_pool_desc* pool, const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* seq_lens, int32_t max_seq_len, float scale, void* out, int32_t* err_word,
+    void* stream);
 
 /*
  * pkv_selftest_bounded_wait - check the kernels' failure path on this GPU.

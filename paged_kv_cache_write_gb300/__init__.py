@@ -29,6 +29,7 @@ __all__ = [
     "decode_fp8_workspace_bytes", "paged_attention_decode_fp8", "paged_attention_prefill_fp8",
     "selftest_bounded_wait_fp8", "PKV_FP4_E2M1", "NormRopeDesc", "qk_norm_rope",
     "qk_norm_rope_write", "qk_norm_rope_write_fp4", "kv_write_fp4", "kv_gather_fp4",
+    "decode_fp4_workspace_bytes", "paged_attention_decode_fp4", "paged_attention_prefill_fp4",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -145,6 +146,14 @@ def _load():
     L.pkv_kv_gather_fp4.restype = _i32
     L.pkv_kv_gather_fp4.argtypes = [_p, _p, _p, _p, _p, _p, _desc, _p, _i32, _p, _p, _i32, _i32, _i32,
                                     _p, _p, _p, _p]
+    L.pkv_decode_fp4_workspace_bytes.restype = _sz
+    L.pkv_decode_fp4_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32, _i32, _i32]
+    L.pkv_paged_attention_decode_fp4.restype = _i32
+    L.pkv_paged_attention_decode_fp4.argtypes = [_p, _i32, _i32, _i32, _p, _p, _p, _p, _p, _p, _desc,
+                                                 _p, _i32, _p, _i32, _f, _i32, _p, _p, _sz, _p, _p]
+    L.pkv_paged_attention_prefill_fp4.restype = _i32
+    L.pkv_paged_attention_prefill_fp4.argtypes = [_p, _i32, _p, _i32, _i32, _i32, _i32, _p, _p, _p, _p,
+                                                  _p, _p, _desc, _p, _i32, _p, _i32, _f, _p, _p, _p]
     _lib = L
     return L
 
@@ -981,3 +990,75 @@ def kv_gather_fp4(k_pool, v_pool, k_groups, v_groups, k_scale, v_scale, block_ta
     if status:
         raise PkvError("pkv_kv_gather_fp4", status)
     return k_out, v_out
+
+
+def decode_fp4_workspace_bytes(num_seqs, n_heads, head_dim, max_seq_len, max_ctas=0, block_size=16):
+    return int(_load().pkv_decode_fp4_workspace_bytes(num_seqs, n_heads, head_dim, max_seq_len,
+                                                      max_ctas, block_size))
+
+
+def paged_attention_decode_fp4(q, k_pool, v_pool, k_groups, v_groups, k_scale, v_scale, block_tables,
+                               seq_lens, scale: float, max_seq_len: int | None = None, *, out=None,
+                               workspace=None, max_ctas: int = 0, err=None, stream=None):
+    """Decode attention [B, n_heads, head_dim] (float32 or bfloat16) over the paged
+    history of a 4-bit cache (see :func:`kv_write_fp4`).
+
+    ``max_seq_len`` and ``workspace`` are as for :func:`paged_attention_decode`, with
+    ``decode_fp4_workspace_bytes(...)`` bytes; calls that may run at the same time need a
+    workspace each.
+    """
+    i, desc, cache = _fp4_pool(k_pool, v_pool, k_groups, v_groups, k_scale, v_scale)
+    there = _context(stream, i)
+    if there is not None:
+        with there:
+            return paged_attention_decode_fp4(q, k_pool, v_pool, k_groups, v_groups, k_scale, v_scale,
+                                              block_tables, seq_lens, scale, max_seq_len, out=out,
+                                              workspace=workspace, max_ctas=max_ctas, err=err)
+    B, W = _batch(block_tables, seq_lens)
+    out, rows, H = _fp8_query(q, desc.head_dim, out)
+    if rows != B:
+        raise ValueError("q must have one row per sequence")
+    if max_seq_len is None:
+        max_seq_len = int(seq_lens.max().item()) if B else 0
+    if workspace is None:
+        need = decode_fp4_workspace_bytes(B, H, desc.head_dim, max_seq_len, max_ctas)
+        workspace = torch.empty(need, dtype=_u8, device=q.device)
+    dt = q.dtype
+    status = (_lib or _load()).pkv_paged_attention_decode_fp4(
+        _ptr(q, "q", dt, i), _type_code(dt), B, H, *cache, ctypes.byref(desc),
+        _ptr(block_tables, "block_tables", _int, i), W, _ptr(seq_lens, "seq_lens", _int, i),
+        int(max_seq_len), float(scale), int(max_ctas), _ptr(out, "out", dt, i),
+        _ptr(workspace, "workspace", workspace.dtype, i), workspace.nbytes,
+        None if err is None else _ptr(err, "err", _int, i), _raw_stream(i))
+    if status:
+        raise PkvError("pkv_paged_attention_decode_fp4", status)
+    return out
+
+
+def paged_attention_prefill_fp4(q, cu_q_lens, k_pool, v_pool, k_groups, v_groups, k_scale, v_scale,
+                                block_tables, seq_lens, scale: float, max_q_len: int | None = None,
+                                max_seq_len: int | None = None, *, out=None, err=None, stream=None):
+    """Causal chunked-prefill attention [total_q, n_heads, head_dim] (float32 or
+    bfloat16) over the paged history of a 4-bit cache."""
+    i, desc, cache = _fp4_pool(k_pool, v_pool, k_groups, v_groups, k_scale, v_scale)
+    there = _context(stream, i)
+    if there is not None:
+        with there:
+            return paged_attention_prefill_fp4(q, cu_q_lens, k_pool, v_pool, k_groups, v_groups, k_scale,
+                                               v_scale, block_tables, seq_lens, scale, max_q_len,
+                                               max_seq_len, out=out, err=err)
+    B, W = _batch(block_tables, seq_lens)
+    out, rows, H = _fp8_query(q, desc.head_dim, out)
+    if max_q_len is None:
+        max_q_len = int((cu_q_lens[1:] - cu_q_lens[:-1]).max().item()) if B else 0
+    if max_seq_len is None:
+        max_seq_len = int(seq_lens.max().item()) if B else 0
+    dt = q.dtype
+    status = (_lib or _load()).pkv_paged_attention_prefill_fp4(
+        _ptr(q, "q", dt, i), _type_code(dt), _offsets(cu_q_lens, "cu_q_lens", B, i), B, rows,
+        int(max_q_len), H, *cache, ctypes.byref(desc), _ptr(block_tables, "block_tables", _int, i), W,
+        _ptr(seq_lens, "seq_lens", _int, i), int(max_seq_len), float(scale), _ptr(out, "out", dt, i),
+        None if err is None else _ptr(err, "err", _int, i), _raw_stream(i))
+    if status:
+        raise PkvError("pkv_paged_attention_prefill_fp4", status)
+    return out

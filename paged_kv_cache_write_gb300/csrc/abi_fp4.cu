@@ -11,6 +11,7 @@
 
 namespace {
 
+using pkv::Fp4Cache;
 using pkv::NormRopeArgs;
 using pkv::PoolShape;
 using pkv::aligned16;
@@ -104,6 +105,40 @@ void set_groups(void* k_groups, void* v_groups, const float* k_scale, const floa
   a->v_groups = static_cast<uint8_t*>(v_groups);
   a->k_scale = k_scale;
   a->v_scale = v_scale;
+}
+
+// The attention entries' common arguments, into `a` and `c`.
+pkv_status check_attention_fp4(const void* q, int32_t dtype, int32_t num_seqs, int32_t n_heads,
+                               const Fp4Cache& c, const pkv_pool_desc* pool,
+                               const int32_t* block_tables, int32_t max_blocks_per_seq,
+                               const int32_t* seq_lens, int32_t max_seq_len, float scale, void* out,
+                               int32_t* err_word, pkv::AttnArgs* a) {
+  PoolShape shape;
+  pkv_status st = check_pool_fp4(pool, &shape);
+  if (st != PKV_OK) return st;
+  if (!float_type(dtype)) return PKV_ERR_DTYPE;
+  st = pkv::check_attention_args(q, num_seqs, n_heads, c.k_pool, c.v_pool, shape, block_tables,
+                                 max_blocks_per_seq, seq_lens, max_seq_len, scale, out);
+  if (st != PKV_OK) return st;
+  // (positions are 32-bit)
+  if (int64_t(max_blocks_per_seq) * shape.block_size > INT32_MAX) return PKV_ERR_RANGE;
+  if (num_seqs > 0) {
+    st = check_groups(c.k_groups, c.v_groups, c.k_scale, c.v_scale);
+    if (st != PKV_OK) return st;
+  }
+  if (!pkv::fp8_attention_supported(shape, n_heads)) return PKV_ERR_UNSUPPORTED;
+  a->q = q;
+  a->out = out;
+  a->block_tables = block_tables;
+  a->seq_lens = seq_lens;
+  a->num_seqs = num_seqs;
+  a->n_heads = n_heads;
+  a->max_blocks_per_seq = max_blocks_per_seq;
+  a->max_seq_len = max_seq_len;
+  a->pool = shape;
+  a->scale = scale;
+  a->err = err_word;
+  return PKV_OK;
 }
 
 }  // namespace
@@ -239,10 +274,71 @@ pkv_status pkv_kv_gather_fp4(const void* k_pool, const void* v_pool, const void*
   if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_out) || !aligned16(v_out))
     return PKV_ERR_ALIGN;
   if ((st = check_groups(k_groups, v_groups, k_scale, v_scale)) != PKV_OK) return st;
-  const pkv::Fp4Cache c{k_pool, v_pool, k_groups, v_groups, k_scale, v_scale};
+  const Fp4Cache c{k_pool, v_pool, k_groups, v_groups, k_scale, v_scale};
   return from_cuda(pkv::launch_kv_gather_fp4(c, shape, block_tables, max_blocks_per_seq, seq_lens,
                                              cu_seq_lens, num_seqs, total_tokens, dtype, k_out,
                                              v_out, err_word, as_stream(stream)));
+}
+
+size_t pkv_decode_fp4_workspace_bytes(int32_t num_seqs, int32_t n_heads, int32_t head_dim,
+                                      int32_t max_seq_len, int32_t max_ctas, int32_t block_size) {
+  (void)max_seq_len;
+  (void)max_ctas;
+  (void)block_size;
+  return pkv::decode_fp8_workspace_bytes(num_seqs < 0 ? 0 : num_seqs, n_heads < 1 ? 1 : n_heads,
+                                         head_dim < 1 ? 1 : head_dim);
+}
+
+pkv_status pkv_paged_attention_decode_fp4(
+    const void* q, int32_t dtype, int32_t num_seqs, int32_t n_heads, const void* k_pool,
+    const void* v_pool, const void* k_groups, const void* v_groups, const float* k_scale,
+    const float* v_scale, const pkv_pool_desc* pool, const int32_t* block_tables,
+    int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t max_seq_len, float scale,
+    int32_t max_ctas, void* out, void* workspace, size_t workspace_bytes, int32_t* err_word,
+    void* stream) {
+  PKV_NVTX_RANGE("pkv_paged_attention_decode_fp4");
+  const Fp4Cache c{k_pool, v_pool, k_groups, v_groups, k_scale, v_scale};
+  pkv::AttnArgs a{};
+  const pkv_status st =
+      check_attention_fp4(q, dtype, num_seqs, n_heads, c, pool, block_tables, max_blocks_per_seq,
+                          seq_lens, max_seq_len, scale, out, err_word, &a);
+  if (st != PKV_OK) return st;
+  if (max_ctas < 0) return PKV_ERR_RANGE;
+  if (num_seqs == 0) return PKV_OK;
+  if (!workspace || workspace_bytes < pkv::decode_fp8_workspace_bytes(num_seqs, n_heads,
+                                                                      a.pool.head_dim))
+    return PKV_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return PKV_ERR_ALIGN;
+  a.max_q_len = 1;
+  a.total_q = num_seqs;
+  a.max_ctas = max_ctas;
+  a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
+  return from_cuda(pkv::launch_decode_fp4(a, dtype, c, as_stream(stream)));
+}
+
+pkv_status pkv_paged_attention_prefill_fp4(
+    const void* q, int32_t dtype, const int32_t* cu_q_lens, int32_t num_seqs, int32_t total_q,
+    int32_t max_q_len, int32_t n_heads, const void* k_pool, const void* v_pool,
+    const void* k_groups, const void* v_groups, const float* k_scale, const float* v_scale,
+    const pkv_pool_desc* pool, const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* seq_lens, int32_t max_seq_len, float scale, void* out, int32_t* err_word,
+    void* stream) {
+  PKV_NVTX_RANGE("pkv_paged_attention_prefill_fp4");
+  const Fp4Cache c{k_pool, v_pool, k_groups, v_groups, k_scale, v_scale};
+  pkv::AttnArgs a{};
+  const pkv_status st =
+      check_attention_fp4(q, dtype, num_seqs, n_heads, c, pool, block_tables, max_blocks_per_seq,
+                          seq_lens, max_seq_len, scale, out, err_word, &a);
+  if (st != PKV_OK) return st;
+  if (total_q < 0 || max_q_len < 0) return PKV_ERR_SHAPE;
+  if (num_seqs == 0 || total_q == 0) return PKV_OK;
+  if (!cu_q_lens) return PKV_ERR_NULL;
+  if (max_q_len == 0 || max_q_len > total_q || max_q_len > max_seq_len) return PKV_ERR_SHAPE;
+  a.cu_q_lens = cu_q_lens;
+  a.max_q_len = max_q_len;
+  a.total_q = total_q;
+  return from_cuda(pkv::launch_prefill_fp4(a, dtype, c, as_stream(stream)));
 }
 
 }  // extern "C"

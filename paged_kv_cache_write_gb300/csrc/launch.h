@@ -165,4 +165,13 @@ cudaError_t launch_prefill_fp8_tc(const AttnArgs& a, const float* k_scales, cons
 cudaError_t launch_prefill_fp8(const AttnArgs& a, int32_t dtype, const float* k_scales,
                                const float* v_scales, cudaStream_t stream);
 
+// Attention over the 4-bit cache: the shapes and the decode workspace of the 8-bit one
+// (a.k_pool / a.v_pool are not used: the cache is c).
+cudaError_t launch_decode_fp4(const AttnArgs& a, int32_t dtype, const Fp4Cache& c,
+                              cudaStream_t stream);
+// its tcgen05 path: bf16, head_dim 64 / 128
+cudaError_t launch_prefill_fp4_tc(const AttnArgs& a, const Fp4Cache& c, cudaStream_t stream);
+cudaError_t launch_prefill_fp4(const AttnArgs& a, int32_t dtype, const Fp4Cache& c,
+                               cudaStream_t stream);
+
 }  // namespace pkv

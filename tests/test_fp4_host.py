@@ -233,3 +233,50 @@ def test_binding_refuses_mismatched_tensors(pkv):
         pkv.kv_write_fp4(x, x, torch.zeros(2, dtype=torch.int64), pool, pool, groups, groups, scale[:1], scale)
     with pytest.raises(ValueError, match="same shape"):
         pkv.kv_write_fp4(x, x, torch.zeros(2, dtype=torch.int64), pool, pool[:1], groups, groups, scale, scale)
+
+
+class Attention(Calls):
+    def decode(self, **kw):
+        d = None if kw.pop("no_pool", False) else ctypes.byref(self.desc(kw, kw.pop("pool_dtype", 3)))
+        return self.lib.pkv_paged_attention_decode_fp4(*self.fill(dict(
+            q=FAKE, type=BF16, B=2, H=8, kp=FAKE, vp=FAKE, kg=FAKE, vg=FAKE, k1=FAKE, v1=FAKE, pool=d, bt=FAKE,
+            W=4, lens=FAKE, most=64, scale=0.1, ctas=0, out=FAKE, ws=FAKE, ws_bytes=1, err=None, stream=None), kw))
+
+    def prefill(self, **kw):
+        d = None if kw.pop("no_pool", False) else ctypes.byref(self.desc(kw, kw.pop("pool_dtype", 3)))
+        return self.lib.pkv_paged_attention_prefill_fp4(*self.fill(dict(
+            q=FAKE, type=BF16, cu=FAKE, B=2, total=0, most_q=8, H=8, kp=FAKE, vp=FAKE, kg=FAKE, vg=FAKE, k1=FAKE,
+            v1=FAKE, pool=d, bt=FAKE, W=4, lens=FAKE, most=64, scale=0.1, out=FAKE, err=None, stream=None), kw))
+
+
+COMMON = [
+    (dict(no_pool=True), NULL), (dict(pool_dtype=1), DTYPE), (dict(type=2), DTYPE), (dict(B=-1), SHAPE),
+    (dict(H=0), SHAPE), (dict(H=7), SHAPE), (dict(W=-1), SHAPE), (dict(most=-1), SHAPE), (dict(most=65), SHAPE),
+    (dict(scale=0.0), RANGE), (dict(scale=float("inf")), RANGE), (dict(scale=float("nan")), RANGE),
+    (dict(q=None), NULL), (dict(kp=None), NULL), (dict(vp=None), NULL), (dict(kg=None), NULL),
+    (dict(vg=None), NULL), (dict(k1=None), NULL), (dict(v1=None), NULL), (dict(bt=None), NULL),
+    (dict(lens=None), NULL), (dict(out=None), NULL), (dict(q=FAKE + 8), ALIGN), (dict(kp=FAKE + 8), ALIGN),
+    (dict(kg=FAKE + 8), ALIGN), (dict(k1=FAKE + 2), ALIGN), (dict(out=FAKE + 4), ALIGN),
+    (dict(head_dim=48), UNSUPPORTED), (dict(head_dim=256), UNSUPPORTED), (dict(block_size=32), UNSUPPORTED),
+    (dict(H=34), UNSUPPORTED), (dict(W=1 << 27), RANGE), (dict(n_kv=65536, H=65536), RANGE)]
+
+
+@pytest.mark.parametrize("kw,status", COMMON + [
+    (dict(ctas=-1), RANGE), (dict(ws=None), WORKSPACE), (dict(), WORKSPACE),
+    (dict(ws=FAKE + 8, ws_bytes=1 << 50), ALIGN), (dict(B=0, q=None, ws=None), OK)])
+def test_decode_refusals(pkv, kw, status):
+    assert Attention(pkv).decode(**kw) == status
+
+
+@pytest.mark.parametrize("kw,status", COMMON + [
+    (dict(), OK), (dict(total=-1), SHAPE), (dict(most_q=-1), SHAPE), (dict(total=9, cu=None), NULL),
+    (dict(total=9, most_q=0), SHAPE), (dict(total=7, most_q=8), SHAPE), (dict(total=99, most_q=65), SHAPE),
+    (dict(B=0, q=None), OK)])
+def test_prefill_refusals(pkv, kw, status):
+    assert Attention(pkv).prefill(**kw) == status
+
+
+def test_workspace_sizes(pkv):
+    a = pkv.decode_fp4_workspace_bytes(4, 8, 64, 100)
+    assert a > 0 and pkv.decode_fp4_workspace_bytes(8, 8, 128, 100) > a
+    assert pkv.decode_fp4_workspace_bytes(-1, 0, 0, 0) > 0

@@ -68,10 +68,9 @@ pkv_status check_norm_rope(const void* q, int64_t q_stride, const void* k, int64
   return PKV_OK;
 }
 
-// Tokens that a call's warps can be counted for in 32 bits.
-bool too_many(const NormRopeArgs& a, int32_t kv_kinds) {
-  const int64_t rows = int64_t(a.n_heads) + int64_t(a.n_kv) * kv_kinds;
-  return rows > (1 << 30) || a.num_tokens > pkv::norm_rope_max_tokens(int32_t(rows), a.head_dim);
+// More than the kernel counts in 32 bits.
+bool too_many(const NormRopeArgs& a) {
+  return a.n_heads > (1 << 20) || a.n_kv > (1 << 20) || a.num_tokens > (1 << 30);
 }
 
 // The values and the slots that keys and values go to.
@@ -163,7 +162,7 @@ pkv_status pkv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int6
   if (st != PKV_OK || num_tokens == 0) return st;
   st = check_rows(k_out, k_out_stride, num_tokens, n_kv, head_dim, dtype);
   if (st != PKV_OK) return st;
-  if (too_many(a, 1)) return PKV_ERR_RANGE;
+  if (too_many(a)) return PKV_ERR_RANGE;
   a.k_out = k_out;
   a.k_out_stride = k_out_stride;
   return from_cuda(pkv::launch_norm_rope(a, as_stream(stream)));
@@ -191,7 +190,7 @@ pkv_status pkv_qk_norm_rope_write(const void* q, int64_t q_stride, const void* k
   if (st != PKV_OK || num_tokens == 0) return st;
   st = check_slots(v, v_stride, slot_mapping, k_pool, v_pool, shape, &a);
   if (st != PKV_OK) return st;
-  if (too_many(a, 2)) return PKV_ERR_RANGE;
+  if (too_many(a)) return PKV_ERR_RANGE;
   return from_cuda(pkv::launch_norm_rope(a, as_stream(stream)));
 }
 
@@ -220,7 +219,7 @@ pkv_status pkv_qk_norm_rope_write_fp4(const void* q, int64_t q_stride, const voi
   st = check_slots(v, v_stride, slot_mapping, k_pool, v_pool, shape, &a);
   if (st == PKV_OK) st = check_groups(k_groups, v_groups, k_scale, v_scale);
   if (st != PKV_OK) return st;
-  if (too_many(a, 2)) return PKV_ERR_RANGE;
+  if (too_many(a)) return PKV_ERR_RANGE;
   set_groups(k_groups, v_groups, k_scale, v_scale, &a);
   return from_cuda(pkv::launch_norm_rope(a, as_stream(stream)));
 }
@@ -247,7 +246,7 @@ pkv_status pkv_kv_write_fp4(const void* k, int64_t k_stride, const void* v, int6
   if (st == PKV_OK) st = check_slots(v, v_stride, slot_mapping, k_pool, v_pool, shape, &a);
   if (st == PKV_OK) st = check_groups(k_groups, v_groups, k_scale, v_scale);
   if (st != PKV_OK) return st;
-  if (too_many(a, 2)) return PKV_ERR_RANGE;
+  if (too_many(a)) return PKV_ERR_RANGE;
   a.k = k;
   a.k_stride = k_stride;
   set_groups(k_groups, v_groups, k_scale, v_scale, &a);

@@ -46,11 +46,14 @@ __device__ __forceinline__ float2 f16x2_to_float2(uint32_t u) {
 
 // ------------------------------------------------------------- to codes
 
-// The larger of two magnitudes; NaN if one of them is.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
+// The larger of two magnitudes, as their bits; NaN if one of them is.
+__device__ __forceinline__ float max_mag(float a, float b) {
+  return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+}
+
+// 1 / g for a power of two (normal range).
+__device__ __forceinline__ float pow2_inverse(float g) {
+  return __uint_as_float(0x7f000000u - __float_as_uint(g));
 }
 
 // a / d, where a is the exact sum of the returned value and a remainder: rounded
@@ -94,39 +97,83 @@ __device__ __forceinline__ uint32_t pack_codes(const float (&y)[8]) {
   return r;
 }
 
-// One group: its 16 values times 1 / g (exact) as codes and the scale's code.
-// The decisions are those of exact arithmetic.  EXACT: values of 24 bits (fp32),
-// whose quotient by the scale may be so near to a border that it is rounded onto
-// it; a bf16 value lies on the border or 2^-9 away.
+// Two vectors of eight elements as codes, and their groups' scales' codes.
+struct Codes {
+  uint32_t a, b, scale_a, scale_b;
+};
+
+// Codes of eight values under a scale (its code; g: the head's) for magnitudes whose
+// largest is amax, over g.  The decisions are those of exact arithmetic.
+//   A bf16 value lies on a border between two codes or 2^-9 away from it, so its
+//   quotient has to be exact on a border and good to some bits elsewhere: 1 / (s g) is
+//   taken as two terms, hi (rounded down) and lo, and x hi + x lo rounded once.  (With
+//   one term, quotients by scales of 13 .. 15 eighths miss their borders.)  Both terms
+//   are >= 0, so a zero keeps its sign.
+//   EXACT, for fp32: a quotient may be so near to a border that it is rounded onto it.
 template <bool EXACT>
-__device__ __forceinline__ void quantise(const float (&x)[16], float inv_g, uint2& codes,
-                                         uint32_t& scale) {
-  float a = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) a = max_nan(a, fabsf(x[i]));
-  a *= inv_g;
-  scale = scale_code(a);
+__device__ __forceinline__ uint32_t codes_under(const float2* x, float amax, uint32_t scale,
+                                                float g) {
   const float s = scale_value(scale);
-  const float inv = s > 0.f ? 1.f / s : s;  // (0 and NaN stay)
-  // past the largest code whatever its size: as far as that goes without infinities
-  const bool large = !(a <= 1.0e30f);
-  float y[2][8];
+  float y[8];
+  if constexpr (EXACT) {
+    const float inv_g = pow2_inverse(g), inv = s > 0.f ? 1.f / s : 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    float v = fabsf(x[i] * inv_g);
-    if (large) v = fminf(v, 1.0e30f);
-    float q;
-    if constexpr (EXACT) {
-      q = s > 0.f ? div_odd(v, s, inv) : 0.f;
-    } else {
-      q = v * inv;
-      q = fmaf(fmaf(-q, s, v), inv, q);  // exact on a border
+    for (int i = 0; i < 8; ++i) {
+      const float v = i & 1 ? x[i / 2].y : x[i / 2].x;
+      const float q = s > 0.f ? div_odd(fminf(fabsf(v * inv_g), 1.0e30f), s, inv) : 0.f;
+      y[i] = __uint_as_float(__float_as_uint(q) | (__float_as_uint(v) & 0x80000000u));
     }
-    // (the sign of a zero stays too)
-    y[i >> 3][i & 7] = __uint_as_float((__float_as_uint(q) & 0x7fffffffu) |
-                                       (__float_as_uint(x[i]) & 0x80000000u));
+  } else {
+    const float sg = s * g;
+    const float hi = s > 0.f ? __frcp_rz(sg) : 0.f;
+    const float lo = fmaf(-sg, hi, 1.f) * hi;  // (0 where s is)
+    const float2 hi2 = make_float2(hi, hi), lo2 = make_float2(lo, lo);
+    const bool large = !(amax <= 1.0e30f);  // no infinities and NaN below
+    const float most = 1.0e30f * g;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 v = x[i];
+      if (large) v = make_float2(fminf(fmaxf(v.x, -most), most), fminf(fmaxf(v.y, -most), most));
+      const float2 q = __ffma2_rn(v, hi2, __fmul2_rn(v, lo2));
+      y[2 * i] = q.x;
+      y[2 * i + 1] = q.y;
+    }
   }
-  codes = make_uint2(pack_codes(y[0]), pack_codes(y[1]));
+  return pack_codes(y);
+}
+
+__device__ __forceinline__ float amax8(const float2* x) {
+  uint32_t a = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    a = max(a, max(__float_as_uint(x[i].x) & 0x7fffffffu, __float_as_uint(x[i].y) & 0x7fffffffu));
+  return __uint_as_float(a);
+}
+
+// One group of 16 values.
+template <bool EXACT>
+__device__ __forceinline__ Codes quantise(const float2 (&x)[8], float g) {
+  const float a = max_mag(amax8(x), amax8(x + 4)) * pow2_inverse(g);
+  Codes r;
+  r.scale_a = r.scale_b = scale_code(a);
+  r.a = codes_under<EXACT>(x, a, r.scale_a, g);
+  r.b = codes_under<EXACT>(x + 4, a, r.scale_b, g);
+  return r;
+}
+
+// Halves of two groups; other(j, amax of x[0..7], of x[8..15]) is the largest magnitude
+// in the other half of half j's group (both by every lane of the warp).
+template <bool EXACT, typename Other>
+__device__ __forceinline__ Codes quantise_apart(const float2 (&x)[8], float g, Other other) {
+  const float ma = amax8(x), mb = amax8(x + 4);
+  const float oa = other(0, ma, mb), ob = other(1, ma, mb);
+  const float a = max_mag(ma, oa) * pow2_inverse(g), b = max_mag(mb, ob) * pow2_inverse(g);
+  Codes r;
+  r.scale_a = scale_code(a);
+  r.scale_b = scale_code(b);
+  r.a = codes_under<EXACT>(x, a, r.scale_a, g);
+  r.b = codes_under<EXACT>(x + 4, b, r.scale_b, g);
+  return r;
 }
 
 }  // namespace fp4

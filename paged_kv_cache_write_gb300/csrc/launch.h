@@ -74,8 +74,6 @@ struct NormRopeArgs {
   bool interleaved;
 };
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
-// Most tokens of a call whose tokens have `rows` rows.
-int64_t norm_rope_max_tokens(int32_t rows, int32_t head_dim);
 
 // A 4-bit cache.
 struct Fp4Cache {

@@ -1,7 +1,8 @@
 """Paged KV cache write and paged attention for GB300 (sm_103a).
 
-A thin ctypes binding over the C ABI in ``include/pkv.h`` (``libpkv.so``,
-built in-tree by ``paged_kv_cache_write_gb300.build``).  Each function here
+A thin binding over the C ABI in ``include/pkv.h`` (``libpkv.so``, built
+in-tree by ``paged_kv_cache_write_gb300.build``): ctypes, and for the norm,
+rotation and 4-bit entries a CPython extension.  Each function here
 has the name of the C entry point without its ``pkv_`` prefix and only
 marshals arguments: it checks tensor devices, dtypes and layouts, passes
 raw device pointers and the current CUDA stream, and raises on a non-zero
@@ -14,6 +15,7 @@ PyTorch is used only for device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 
 import torch
@@ -744,57 +746,34 @@ def selftest_bounded_wait_fp8(err, polls: int = 64, *, stream=None):
 
 # ------------------------------------- queries and keys before the cache
 #
-# Rows [tokens, heads, head_dim] may be parts of one projection's output: a
-# token's heads lie together, tokens any multiple of 16 bytes apart.
+# These entries' tensors are checked, and their calls made, by a CPython extension
+# (csrc/binding.cpp): in a decode step the host's part of a call would else take
+# several times the kernel's.  Rows [tokens, heads, head_dim] may be parts of one
+# projection's output: a token's heads lie together, tokens any multiple of 16 bytes
+# apart.
 
-_u8 = torch.uint8
-
-
-def _row_ptr(t, name, dtype, index, shape=None):
-    """(address, token stride in elements) of rows [tokens, heads, head_dim]."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 3 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} must be {shape or '[tokens, heads, head_dim]'}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, the call on cuda:{index}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    T, H, hd = t.shape
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (H > 1 and s1 != hd):
-        raise ValueError(f"{name}: a token's heads must be contiguous")
-    return t.data_ptr(), s0 if T > 1 else H * hd
+_native = None
 
 
-def _index_of(t, name):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    index = t.get_device()
-    if index < 0:
+def _load_binding():
+    """The extension; raises if it has not been built."""
+    global _native
+    if _native is None:
+        _load()
+        try:
+            _native = importlib.import_module("._binding", __name__)
+        except ImportError as e:
+            raise ImportError(f"{HERE}/_binding.so cannot be loaded: build it with "
+                              f"`python -m paged_kv_cache_write_gb300.build` ({e})") from e
+    return _native
+
+
+def _on(stream, t, name):
+    """The stream a call was given as a context, so that what it allocates and reads
+    belongs to that stream."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    return index
-
-
-def _norm_rope(cos_sin, positions, q_weight, k_weight, eps, interleaved, tokens, head_dim, dtype, index):
-    if cos_sin.dim() != 2:
-        raise ValueError("cos_sin must be [num_positions, rot_dim]")
-    if tuple(positions.shape) != (tokens,):
-        raise ValueError(f"positions must be {(tokens,)}: one per token")
-    at = []
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and tuple(w.shape) != (head_dim,):
-            raise ValueError(f"{name} must be {(head_dim,)}")
-        at.append(None if w is None else _ptr(w, name, dtype, index))
-    return NormRopeDesc(at[0], at[1], float(eps), cos_sin.shape[1], int(bool(interleaved)),
-                        cos_sin.shape[0], _ptr(cos_sin, "cos_sin", _f32, index),
-                        _ptr(positions, "positions", _int, index))
-
-
-def _slots(slot_mapping, tokens, index):
-    if tuple(slot_mapping.shape) != (tokens,):
-        raise ValueError(f"slot_mapping must be {(tokens,)}: one entry per token")
-    return _ptr(slot_mapping, "slot_mapping", torch.int64, index)
+    return _context(stream, t.get_device())
 
 
 def _rows_like(t):
@@ -814,26 +793,16 @@ def qk_norm_rope(q, k, cos_sin, positions, *, q_weight=None, k_weight=None, eps:
     [T].  All in fp32, rounded once.  Rows may be views of one projection's output;
     ``q_out`` / ``k_out`` may be ``q`` / ``k`` themselves.
     """
-    i = _index_of(q, "q")
-    there = _context(stream, i)
-    if there is not None:
-        with there:
+    if stream is not None:
+        with _on(stream, q, "q"):
             return qk_norm_rope(q, k, cos_sin, positions, q_weight=q_weight, k_weight=k_weight, eps=eps,
                                 interleaved=interleaved, q_out=q_out, k_out=k_out, err=err)
-    dt = q.dtype
-    qp, qs = _row_ptr(q, "q", dt, i)
-    T, H, hd = q.shape
-    kp, ks = _row_ptr(k, "k", dt, i)
-    if k.shape[0] != T or k.shape[2] != hd:
-        raise ValueError("k must be [T, n_kv, head_dim] with q's tokens and head_dim")
-    turn = _norm_rope(cos_sin, positions, q_weight, k_weight, eps, interleaved, T, hd, dt, i)
-    q_out = _rows_like(q) if q_out is None else q_out
-    k_out = _rows_like(k) if k_out is None else k_out
-    qo, qos = _row_ptr(q_out, "q_out", dt, i, tuple(q.shape))
-    ko, kos = _row_ptr(k_out, "k_out", dt, i, tuple(k.shape))
-    status = (_lib or _load()).pkv_qk_norm_rope(
-        qp, qs, kp, ks, _type_code(dt), T, H, k.shape[1], hd, ctypes.byref(turn), qo, qos, ko, kos,
-        None if err is None else _ptr(err, "err", _int, i), _raw_stream(i))
+    if q_out is None:
+        q_out = _rows_like(q)
+    if k_out is None:
+        k_out = _rows_like(k)
+    status = (_native or _load_binding()).qk_norm_rope(q, k, cos_sin, positions, q_weight, k_weight, eps,
+                                                  interleaved, q_out, k_out, err)
     if status:
         raise PkvError("pkv_qk_norm_rope", status)
     return q_out, k_out
@@ -844,57 +813,22 @@ def qk_norm_rope_write(q, k, v, cos_sin, positions, slot_mapping, k_pool, v_pool
                        err=None, stream=None):
     """:func:`qk_norm_rope`, its keys and the values ``v`` [T, n_kv, head_dim] written
     to their slots as by :func:`kv_write`, in one launch; returns the queries."""
-    i = _index_of(k_pool, "k_pool")
-    there = _context(stream, i)
-    if there is not None:
-        with there:
+    if stream is not None:
+        with _on(stream, k_pool, "k_pool"):
             return qk_norm_rope_write(q, k, v, cos_sin, positions, slot_mapping, k_pool, v_pool,
                                       q_weight=q_weight, k_weight=k_weight, eps=eps,
                                       interleaved=interleaved, q_out=q_out, err=err)
-    desc = pool_desc(k_pool)
-    dt = k_pool.dtype
-    if v_pool.shape != k_pool.shape:
-        raise ValueError("k_pool and v_pool must have the same shape")
-    qp, qs = _row_ptr(q, "q", dt, i)
-    T, H, hd = q.shape
-    if hd != desc.head_dim:
-        raise ValueError("q must be [T, n_heads, head_dim] with the pool's head_dim")
-    shape = (T, desc.n_kv, hd)
-    kp, ks = _row_ptr(k, "k", dt, i, shape)
-    vp, vs = _row_ptr(v, "v", dt, i, shape)
-    turn = _norm_rope(cos_sin, positions, q_weight, k_weight, eps, interleaved, T, hd, dt, i)
-    q_out = _rows_like(q) if q_out is None else q_out
-    qo, qos = _row_ptr(q_out, "q_out", dt, i, tuple(q.shape))
-    status = (_lib or _load()).pkv_qk_norm_rope_write(
-        qp, qs, kp, ks, vp, vs, T, H, ctypes.byref(turn), qo, qos, _slots(slot_mapping, T, i),
-        _ptr(k_pool, "k_pool", dt, i), _ptr(v_pool, "v_pool", dt, i), ctypes.byref(desc),
-        None if err is None else _ptr(err, "err", _int, i), _raw_stream(i))
+    if q_out is None:
+        q_out = _rows_like(q)
+    status = (_native or _load_binding()).qk_norm_rope_write(q, k, v, cos_sin, positions, slot_mapping, k_pool,
+                                                        v_pool, q_weight, k_weight, eps, interleaved,
+                                                        q_out, err)
     if status:
         raise PkvError("pkv_qk_norm_rope_write", status)
     return q_out
 
 
 # ------------------------------------------------------------ 4-bit cache
-
-def _fp4_pool(k_pool, v_pool, k_groups, v_groups, k_scale, v_scale):
-    """Device, descriptor and addresses of a 4-bit cache, its six tensors checked."""
-    shape = k_pool.shape
-    if len(shape) != 4:
-        raise ValueError("pool must be [num_blocks, n_kv, block_size, head_dim / 2]")
-    if v_pool.shape != shape:
-        raise ValueError("k_pool and v_pool must have the same shape")
-    nb, nkv, bs, half = shape
-    per = (nb, nkv, bs, half // 8)
-    if half % 8 or tuple(k_groups.shape) != per or tuple(v_groups.shape) != per:
-        raise ValueError(f"k_groups and v_groups must be {per}: one per 16 elements")
-    if tuple(k_scale.shape) != (nkv,) or tuple(v_scale.shape) != (nkv,):
-        raise ValueError(f"k_scale and v_scale must be {(nkv,)}: one per KV head")
-    index = _index_of(k_pool, "k_pool")
-    return (index, PoolDesc(nb, bs, nkv, 2 * half, PKV_FP4_E2M1),
-            (_ptr(k_pool, "k_pool", _u8, index), _ptr(v_pool, "v_pool", _u8, index),
-             _ptr(k_groups, "k_groups", _f8, index), _ptr(v_groups, "v_groups", _f8, index),
-             _ptr(k_scale, "k_scale", _f32, index), _ptr(v_scale, "v_scale", _f32, index)))
-
 
 def kv_write_fp4(k, v, slot_mapping, k_pool, v_pool, k_groups, v_groups, k_scale, v_scale, *, err=None,
                  stream=None):
@@ -907,20 +841,12 @@ def kv_write_fp4(k, v, slot_mapping, k_pool, v_pool, k_groups, v_groups, k_scale
     A token's codes depend on that token alone.  Values past 2,688 x its head's
     scale saturate; a group's scale loses precision below 0.1 x it.
     """
-    i, desc, cache = _fp4_pool(k_pool, v_pool, k_groups, v_groups, k_scale, v_scale)
-    there = _context(stream, i)
-    if there is not None:
-        with there:
+    if stream is not None:
+        with _on(stream, k_pool, "k_pool"):
             return kv_write_fp4(k, v, slot_mapping, k_pool, v_pool, k_groups, v_groups, k_scale,
                                 v_scale, err=err)
-    dt = k.dtype
-    T = k.shape[0]
-    shape = (T, desc.n_kv, desc.head_dim)
-    kp, ks = _row_ptr(k, "k", dt, i, shape)
-    vp, vs = _row_ptr(v, "v", dt, i, shape)
-    status = (_lib or _load()).pkv_kv_write_fp4(
-        kp, ks, vp, vs, _type_code(dt), _slots(slot_mapping, T, i), T, *cache, ctypes.byref(desc),
-        None if err is None else _ptr(err, "err", _int, i), _raw_stream(i))
+    status = (_native or _load_binding()).kv_write_fp4(k, v, slot_mapping, k_pool, v_pool, k_groups, v_groups,
+                                                  k_scale, v_scale, err)
     if status:
         raise PkvError("pkv_kv_write_fp4", status)
 
@@ -931,29 +857,17 @@ def qk_norm_rope_write_fp4(q, k, v, cos_sin, positions, slot_mapping, k_pool, v_
                            stream=None):
     """:func:`qk_norm_rope`, its keys and the values ``v`` quantised into a 4-bit cache
     as by :func:`kv_write_fp4`, in one launch; returns the queries."""
-    i, desc, cache = _fp4_pool(k_pool, v_pool, k_groups, v_groups, k_scale, v_scale)
-    there = _context(stream, i)
-    if there is not None:
-        with there:
+    if stream is not None:
+        with _on(stream, k_pool, "k_pool"):
             return qk_norm_rope_write_fp4(q, k, v, cos_sin, positions, slot_mapping, k_pool, v_pool,
                                           k_groups, v_groups, k_scale, v_scale, q_weight=q_weight,
                                           k_weight=k_weight, eps=eps, interleaved=interleaved,
                                           q_out=q_out, err=err)
-    dt = q.dtype
-    qp, qs = _row_ptr(q, "q", dt, i)
-    T, H, hd = q.shape
-    if hd != desc.head_dim:
-        raise ValueError("q must be [T, n_heads, head_dim] with the pool's head_dim")
-    shape = (T, desc.n_kv, hd)
-    kp, ks = _row_ptr(k, "k", dt, i, shape)
-    vp, vs = _row_ptr(v, "v", dt, i, shape)
-    turn = _norm_rope(cos_sin, positions, q_weight, k_weight, eps, interleaved, T, hd, dt, i)
-    q_out = _rows_like(q) if q_out is None else q_out
-    qo, qos = _row_ptr(q_out, "q_out", dt, i, tuple(q.shape))
-    status = (_lib or _load()).pkv_qk_norm_rope_write_fp4(
-        qp, qs, kp, ks, vp, vs, _type_code(dt), T, H, ctypes.byref(turn), qo, qos,
-        _slots(slot_mapping, T, i), *cache, ctypes.byref(desc),
-        None if err is None else _ptr(err, "err", _int, i), _raw_stream(i))
+    if q_out is None:
+        q_out = _rows_like(q)
+    status = (_native or _load_binding()).qk_norm_rope_write_fp4(
+        q, k, v, cos_sin, positions, slot_mapping, k_pool, v_pool, k_groups, v_groups, k_scale, v_scale,
+        q_weight, k_weight, eps, interleaved, q_out, err)
     if status:
         raise PkvError("pkv_qk_norm_rope_write_fp4", status)
     return q_out
@@ -965,28 +879,19 @@ def kv_gather_fp4(k_pool, v_pool, k_groups, v_groups, k_scale, v_scale, block_ta
     """Contiguous [total_tokens, n_kv, head_dim] K and V of a 4-bit cache in logical
     order, each code times its scales, in ``dtype`` (float32 or bfloat16; that of
     ``k_out`` / ``v_out`` where given)."""
-    i, desc, cache = _fp4_pool(k_pool, v_pool, k_groups, v_groups, k_scale, v_scale)
-    there = _context(stream, i)
-    if there is not None:
-        with there:
+    if stream is not None:
+        with _on(stream, k_pool, "k_pool"):
             return kv_gather_fp4(k_pool, v_pool, k_groups, v_groups, k_scale, v_scale, block_tables,
                                  seq_lens, cu_seq_lens, total_tokens, dtype=dtype, k_out=k_out,
                                  v_out=v_out, err=err)
-    B, W = _batch(block_tables, seq_lens)
-    dt = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else dtype
-    code = _type_code(dt)
-    shape = (int(total_tokens), desc.n_kv, desc.head_dim)
-    if k_out is None:
-        k_out = torch.empty(shape, dtype=dt, device=k_pool.device)
-    if v_out is None:
-        v_out = torch.empty(shape, dtype=dt, device=k_pool.device)
-    if k_out.shape != shape or v_out.shape != shape:
-        raise ValueError(f"k_out, v_out must be {shape}")
-    status = (_lib or _load()).pkv_kv_gather_fp4(
-        *cache, ctypes.byref(desc), _ptr(block_tables, "block_tables", _int, i), W,
-        _ptr(seq_lens, "seq_lens", _int, i), _offsets(cu_seq_lens, "cu_seq_lens", B, i), B, shape[0],
-        code, _ptr(k_out, "k_out", dt, i), _ptr(v_out, "v_out", dt, i),
-        None if err is None else _ptr(err, "err", _int, i), _raw_stream(i))
+    if k_out is None or v_out is None:
+        dt = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else dtype
+        shape = (int(total_tokens), k_pool.shape[1], 2 * k_pool.shape[3])
+        k_out = torch.empty(shape, dtype=dt, device=k_pool.device) if k_out is None else k_out
+        v_out = torch.empty(shape, dtype=dt, device=k_pool.device) if v_out is None else v_out
+    status = (_native or _load_binding()).kv_gather_fp4(
+        k_pool, v_pool, k_groups, v_groups, k_scale, v_scale, block_tables, seq_lens, cu_seq_lens,
+        total_tokens, k_out, v_out, err)
     if status:
         raise PkvError("pkv_kv_gather_fp4", status)
     return k_out, v_out
@@ -1007,29 +912,22 @@ def paged_attention_decode_fp4(q, k_pool, v_pool, k_groups, v_groups, k_scale, v
     ``decode_fp4_workspace_bytes(...)`` bytes; calls that may run at the same time need a
     workspace each.
     """
-    i, desc, cache = _fp4_pool(k_pool, v_pool, k_groups, v_groups, k_scale, v_scale)
-    there = _context(stream, i)
-    if there is not None:
-        with there:
+    if stream is not None:
+        with _on(stream, k_pool, "k_pool"):
             return paged_attention_decode_fp4(q, k_pool, v_pool, k_groups, v_groups, k_scale, v_scale,
                                               block_tables, seq_lens, scale, max_seq_len, out=out,
                                               workspace=workspace, max_ctas=max_ctas, err=err)
-    B, W = _batch(block_tables, seq_lens)
-    out, rows, H = _fp8_query(q, desc.head_dim, out)
-    if rows != B:
-        raise ValueError("q must have one row per sequence")
     if max_seq_len is None:
-        max_seq_len = int(seq_lens.max().item()) if B else 0
+        max_seq_len = int(seq_lens.max().item()) if len(seq_lens) else 0
+    if out is None:
+        out = torch.empty_like(q)
     if workspace is None:
-        need = decode_fp4_workspace_bytes(B, H, desc.head_dim, max_seq_len, max_ctas)
-        workspace = torch.empty(need, dtype=_u8, device=q.device)
-    dt = q.dtype
-    status = (_lib or _load()).pkv_paged_attention_decode_fp4(
-        _ptr(q, "q", dt, i), _type_code(dt), B, H, *cache, ctypes.byref(desc),
-        _ptr(block_tables, "block_tables", _int, i), W, _ptr(seq_lens, "seq_lens", _int, i),
-        int(max_seq_len), float(scale), int(max_ctas), _ptr(out, "out", dt, i),
-        _ptr(workspace, "workspace", workspace.dtype, i), workspace.nbytes,
-        None if err is None else _ptr(err, "err", _int, i), _raw_stream(i))
+        with torch.cuda.device(q.device):  # (as large as that device's grid)
+            need = decode_fp4_workspace_bytes(*q.shape, max_seq_len, max_ctas)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    status = (_native or _load_binding()).paged_attention_decode_fp4(
+        q, k_pool, v_pool, k_groups, v_groups, k_scale, v_scale, block_tables, seq_lens, scale,
+        max_seq_len, out, workspace, max_ctas, err)
     if status:
         raise PkvError("pkv_paged_attention_decode_fp4", status)
     return out
@@ -1040,25 +938,20 @@ def paged_attention_prefill_fp4(q, cu_q_lens, k_pool, v_pool, k_groups, v_groups
                                 max_seq_len: int | None = None, *, out=None, err=None, stream=None):
     """Causal chunked-prefill attention [total_q, n_heads, head_dim] (float32 or
     bfloat16) over the paged history of a 4-bit cache."""
-    i, desc, cache = _fp4_pool(k_pool, v_pool, k_groups, v_groups, k_scale, v_scale)
-    there = _context(stream, i)
-    if there is not None:
-        with there:
+    if stream is not None:
+        with _on(stream, k_pool, "k_pool"):
             return paged_attention_prefill_fp4(q, cu_q_lens, k_pool, v_pool, k_groups, v_groups, k_scale,
                                                v_scale, block_tables, seq_lens, scale, max_q_len,
                                                max_seq_len, out=out, err=err)
-    B, W = _batch(block_tables, seq_lens)
-    out, rows, H = _fp8_query(q, desc.head_dim, out)
     if max_q_len is None:
-        max_q_len = int((cu_q_lens[1:] - cu_q_lens[:-1]).max().item()) if B else 0
+        max_q_len = int((cu_q_lens[1:] - cu_q_lens[:-1]).max().item()) if len(seq_lens) else 0
     if max_seq_len is None:
-        max_seq_len = int(seq_lens.max().item()) if B else 0
-    dt = q.dtype
-    status = (_lib or _load()).pkv_paged_attention_prefill_fp4(
-        _ptr(q, "q", dt, i), _type_code(dt), _offsets(cu_q_lens, "cu_q_lens", B, i), B, rows,
-        int(max_q_len), H, *cache, ctypes.byref(desc), _ptr(block_tables, "block_tables", _int, i), W,
-        _ptr(seq_lens, "seq_lens", _int, i), int(max_seq_len), float(scale), _ptr(out, "out", dt, i),
-        None if err is None else _ptr(err, "err", _int, i), _raw_stream(i))
+        max_seq_len = int(seq_lens.max().item()) if len(seq_lens) else 0
+    if out is None:
+        out = torch.empty_like(q)
+    status = (_native or _load_binding()).paged_attention_prefill_fp4(
+        q, cu_q_lens, k_pool, v_pool, k_groups, v_groups, k_scale, v_scale, block_tables, seq_lens,
+        scale, max_q_len, max_seq_len, out, err)
     if status:
         raise PkvError("pkv_paged_attention_prefill_fp4", status)
     return out

@@ -201,12 +201,6 @@ struct Rows {
           ks[h][0] = scales_f16x2(*sp, *sp);
         }
       }
-      // V's words too: in flight while the scores are computed
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        load_codes<VW, DB>(t[nb] + vc[h & 1] + (h >> 1) * 8 * (HD / 2), vw[nb][h]);
-        vs[nb][h] = t[nb][vgr[h & 1] + (h >> 1) * 8 * KK];
-      }
       constexpr int CH = KK >= 4 ? 2 : 1;
       float s[NT][CH][4];
 #pragma unroll
@@ -301,6 +295,13 @@ struct Rows {
           sum += w[nb][nt][j] + w[nb][nt][2 + j];
         }
         l[nt][j] += sum;
+      }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        load_codes<VW, DB>(t[nb] + vc[h & 1] + (h >> 1) * 8 * (HD / 2), vw[nb][h]);
+        vs[nb][h] = t[nb][vgr[h & 1] + (h >> 1) * 8 * KK];
       }
     // V rows past the sequence's end hold whatever the pool holds there: codes, which
     // are finite, under scales taken as zero

@@ -727,7 +727,7 @@ pkv_status pkv_qk_norm_rope_write(const void* q, int64_t q_stride, const void* k
  *
  * pool->dtype is PKV_FP4_E2M1, pool->head_dim counts elements: a multiple of 16 up
  * to 256 (attention: 16, 32, 64 or 128, with block_size 16); n_kv at most 65,535;
- * num_blocks * block_size below 2^31.  `dtype` is the type of k, v, q and the
+ * num_blocks * block_size and num_blocks * n_kv below 2^31.  `dtype` is the type of k, v, q and the
  * outputs (PKV_F32 or PKV_BF16).
  *
  * A block is copied on write with two pkv_copy_blocks calls: one on the pools
@@ -796,18 +796,20 @@ pkv_status pkv_kv_gather_fp4(const void* k_pool, const void* v_pool, const void*
  *
  * The work split, and with it what results depend on, is that of
  * pkv_paged_attention_decode: logical positions, lengths and max_ctas, never physical
- * block ids; identical calls give identical bits.  Keys and values enter exactly (code
- * times group scale, the head's scale in the score and the output); scores, softmax
- * sums and outputs are held in fp32.  For bf16, weights are rounded to 11 significand
- * bits before they multiply V; for fp32 queries and weights keep 22.  A query element
- * more than 2^28 below its row's largest loses bits.
+ * block ids; identical calls give identical bits.  Keys and values
+ * enter exactly (code times group scale, the head's scale in the score and the output);
+ * scores, softmax sums and outputs are held in fp32.  For bf16, weights are rounded to 11
+ * significand bits before they multiply V, those below 2^-18 of a row's largest to fewer;
+ * for fp32 queries and weights keep 22.  A query element more than 2^28 below its row's
+ * largest loses bits.
  *
  *   q, out      [num_seqs, n_heads, head_dim] of `dtype`, 16-byte aligned
  *   workspace   at least pkv_decode_fp4_workspace_bytes(...) bytes, 16-byte aligned;
  *               calls that may run at the same time need one each (max_seq_len,
  *               max_ctas and block_size are taken for forward compatibility)
  *   Supported: head_dim 16, 32, 64, 128; block_size 16; n_heads % n_kv == 0,
- *              n_heads / n_kv <= 16; max_blocks_per_seq * block_size below 2^31.
+ *              n_heads / n_kv <= 16; max_blocks_per_seq * block_size and num_seqs *
+ *              n_kv * ceil(max_seq_len / 16) below 2^31 (PKV_ERR_RANGE).
  */
 size_t pkv_decode_fp4_workspace_bytes(int32_t num_seqs, int32_t n_heads, int32_t head_dim,
                                       int32_t max_seq_len, int32_t max_ctas, int32_t block_size);
@@ -824,9 +826,7 @@ pkv_status pkv_paged_attention_decode_fp4(
  * pkv_paged_attention_prefill_fp4 - pkv_paged_attention_prefill over a 4-bit cache:
  * causal attention of each sequence's query chunk over its paged history (the chunk's
  * own K/V written first).  A key or value that a query may not see does not reach its
- * output, NaN included.  It needs no workspace.  Precision as for the decode, but that
- * with bf16 queries weights below 2^-18 of a row's largest are rounded to fewer than 11
- * bits.  cu_q_lens, and which rows are left as they were, as for
+ * output, NaN included.  It needs no workspace.  Precision as for the decode.  cu_q_lens, and which rows are left as they were, as for
  * pkv_paged_attention_prefill_fp8; supported shapes as for the decode.
  */
 pkv_status pkv_paged_attention_prefill_fp4(

@@ -303,6 +303,10 @@ pkv_status pkv_paged_attention_decode_fp4(
                           seq_lens, max_seq_len, scale, out, err_word, &a);
   if (st != PKV_OK) return st;
   if (max_ctas < 0) return PKV_ERR_RANGE;
+  // (units of the work split are counted in 32 bits)
+  if (int64_t(num_seqs) * a.pool.n_kv > INT32_MAX ||
+      int64_t(num_seqs) * a.pool.n_kv * ((int64_t(max_seq_len) + 15) / 16) > INT32_MAX)
+    return PKV_ERR_RANGE;
   if (num_seqs == 0) return PKV_OK;
   if (!workspace || workspace_bytes < pkv::decode_fp8_workspace_bytes(num_seqs, n_heads,
                                                                       a.pool.head_dim))

@@ -57,7 +57,8 @@ inline pkv_status check_pool_fp4(const pkv_pool_desc* pool, PoolShape* out) {
   if (pool->num_blocks <= 0 || pool->block_size <= 0 || pool->n_kv <= 0 || pool->head_dim <= 0)
     return PKV_ERR_SHAPE;
   if (pool->head_dim % 16 != 0 || pool->head_dim > 256) return PKV_ERR_UNSUPPORTED;
-  if (pool->n_kv > 65535 || (int64_t)pool->num_blocks * pool->block_size > INT32_MAX)
+  if (pool->n_kv > 65535 || (int64_t)pool->num_blocks * pool->block_size > INT32_MAX ||
+      (int64_t)pool->num_blocks * pool->n_kv > INT32_MAX)
     return PKV_ERR_RANGE;
   *out = PoolShape{pool->num_blocks, pool->block_size, pool->n_kv, pool->head_dim, pool->dtype};
   return PKV_OK;

@@ -1,15 +1,26 @@
 // Decode over the 4-bit cache: one query per sequence attends to the sequence's pages
 // (mathematics and layouts of the tiles in fp4_rows.cuh).
 //
-// Bound by reading the cache: 9 / 8 x n_kv x head_dim bytes a token.  The work split is
-// that of the 8-bit decode: a persistent grid over equal contiguous ranges of
-// (sequence, head group, block) units, a joining kernel for the groups that several
-// CTAs share, and one thread-block cluster per (sequence, head group) for batches too
-// small to stream.  A head's rows of a block lie together in the pools, so a block of
-// a group's heads is four contiguous runs (K and V, codes and scales: 18 KB at 8 heads
-// of 128) that one producer lane fetches with bulk copies; one consumer warp per KV
-// head.
+// Bound by reading the cache, 9 / 8 x n_kv x head_dim bytes a token, and close behind by
+// the instructions that turn codes into f16 operands: some 290 a block and head of 128,
+// where the SM's schedulers have 397 in the time that the block takes to arrive.  So
+// nothing is spent on synchronisation: a head's rows of a block lie together in the
+// pools (four runs: K and V, codes and scales, 2.3 KB at head_dim 128), and each warp
+// fetches its own into a ring of its own, by asynchronous 16-byte copies of all its lanes
+// as soon as it has left a stage.  No warp waits for another, and there is no barrier.
+// (Bulk copies would be issued one by one, some 25 instructions each: 142 us for 256
+// sequences of 16 - 8,192 tokens, 64 heads on 8 of 128.)
+//
+// Work split: equal contiguous ranges of (sequence, head group, block) units, one per CTA
+// of a persistent grid, a warp for each KV head of the group (so that the heads of a
+// block, which lie together, are read at about the same time: ranges of (sequence, head,
+// block) units for each warp by itself reach 5.7 TB/s where these reach 6.3); a joining
+// kernel for the groups that several CTAs share; one thread-block cluster per (sequence, head group) for batches too small to
+// stream, combined through distributed shared memory.
 #pragma once
+
+#include <algorithm>
+#include <type_traits>
 
 #include "attention.cuh"
 #include "decode_fp8.cuh"
@@ -20,32 +31,20 @@ namespace fp4 {
 
 using attn::DecodeParams;
 using attn::DecodeWs;
-using attn::Ring;
-using attn::kBarrierBytes;
 using attn::kKernelPlanSeqs;
 using attn::kMaxCluster;
-using attn::kMaxStages;
-using fp8::RingPos;
 using fp8::Walk;
-using fp8::gave_up;
 using fp8::head_group;
 using fp8::kKeptLens;
 using fp8::length_of;
-using fp8::release_tile;
 using fp8::report_bad_length;
 
-constexpr int kMaxThreads = 9 * 32;
+constexpr int kWarps = 8;       // of a CTA at the most: a head group's
+constexpr int kMaxBlocks = 8;   // of a warp of a cluster
+constexpr int kMaxStages = 12;  // of a warp's ring
+constexpr int kSmemMax = 226 * 1024;  // of an SM's CTAs
 
-__device__ __forceinline__ void bulk_copy_hint(void* dst, const void* src, uint32_t bytes,
-                                               uint64_t* bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
-      "[%0], [%1], %2, [%3], %4;" ::"r"(smem_addr(dst)),
-      "l"(src), "r"(bytes), "r"(smem_addr(bar)), "l"(policy)
-      : "memory");
-}
-
-// The pools as the producer reads them.
+// The pools as they are read.
 struct Pools {
   const uint8_t *k, *v, *kg, *vg;
   const float *k_scale, *v_scale;
@@ -58,135 +57,125 @@ struct Pools {
         v_scale(c.v_scale) {}
 };
 
-__device__ __forceinline__ Ring make_ring(uint8_t* smem, int nstages, int stage_bytes) {
-  Ring r = attn::make_tile_ring(smem, nstages, stage_bytes / 2);
-  return r;
+// 16 bytes global -> shared past L1, with an L2 cache policy; zeros where size is 0.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, uint32_t size,
+                                       uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+               "r"(size), "l"(policy)
+               : "memory");
 }
 
-// Producer, one lane (elect_one): fetches blocks into the ring one after the other.
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// Until at most N of this lane's groups of copies are on their way; then, for the warp, the
+// groups before those are there.
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+  __syncwarp();
+}
+
+// Fetches one head's blocks, by a whole warp: a lane copies 16-byte pieces of the four runs.
 template <int HD>
-struct Producer {
-  const Ring& ring;
-  const Pools& pools;
-  int num_blocks, n_kv, heads;  // heads: of a tile
+struct Fetcher {
+  static constexpr bool kWide = HD >= 64;  // K's codes are a warp's copies or more
+  const uint8_t *codes, *codes_v, *groups;  // this lane's first pieces, in head 0 of block 0
+  uint32_t at_codes, at_groups;             // and in a tile
+  bool has_codes, has_groups;
+  int n_kv, num_blocks;
   int32_t* err;
-  uint64_t policy;  // nonzero: an L2 cache policy for the copied lines
-  RingPos pos;
-  uint32_t issued = 0;
+  uint64_t policy;
 
-  // Heads head0 .. of block `id`; a bad one reads zeros.  False on timeout.
-  __device__ __forceinline__ bool fetch(int id, int head0) {
-    if (pos.round > 0 && !wait_or_abort(ring.empty + pos.st, (pos.round - 1) & 1, ring.abort_flag)) {
-      report(err, PKV_DEVERR_TIMEOUT);
-      return false;
-    }
-    uint8_t* t = ring.k_tile(pos.st);
-    uint64_t* full = ring.full + pos.st;
-    const uint32_t codes = heads * kBS * HD / 2, groups = heads * kBS * HD / kGroup;
-    if (id >= 0 && id < num_blocks) {
-      mbar_arrive_expect_tx(full, 2 * (codes + groups));
-      const int64_t row = (int64_t(id) * n_kv + head0) * kBS;
-      copy(t, pools.k + row * (HD / 2), codes, full);
-      copy(t + codes, pools.v + row * (HD / 2), codes, full);
-      copy(t + 2 * codes, pools.kg + row * (HD / kGroup), groups, full);
-      copy(t + 2 * codes + groups, pools.vg + row * (HD / kGroup), groups, full);
-    } else {
-      report(err, PKV_DEVERR_BLOCK_ID);
-      // scales of zero: whatever codes the stage holds are then zeros
-      for (uint32_t i = 0; i < 2 * groups; i += 16)
-        *reinterpret_cast<uint4*>(t + 2 * codes + i) = make_uint4(0u, 0u, 0u, 0u);
-      fence_proxy_async_smem();  // before the copies that come there next
-      mbar_arrive(full);
-    }
-    pos.next(ring);
-    ++issued;
-    return true;
+  __device__ __forceinline__ Fetcher(const Pools& pools, int n_kv_, int num_blocks_, int32_t* err_)
+      : n_kv(n_kv_), num_blocks(num_blocks_), err(err_), policy(tc::l2_evict_first_policy()) {
+    using TileT = Tile<HD>;
+    const int lane = threadIdx.x & 31;
+    // codes: K's pieces, then V's (wide heads: both in every lane)
+    constexpr int nc = TileT::kCodes / 16, ng = TileT::kGroups / 16;
+    const bool v = !kWide && lane >= nc;
+    const int piece = kWide ? lane : v ? lane - nc : lane;
+    has_codes = kWide || lane < 2 * nc;
+    codes = (v ? pools.v : pools.k) + piece * 16;
+    codes_v = pools.v + piece * 16;
+    at_codes = (v ? TileT::kVCodes : 0) + piece * 16;
+    // scales: in the lanes that follow (narrowest heads) or in a round of their own
+    const int g = HD == 16 ? lane - 2 * nc : lane;
+    has_groups = g >= 0 && g < 2 * ng;
+    groups = g < ng ? pools.kg + g * 16 : pools.vg + (g - ng) * 16;
+    at_groups = TileT::kKGroups + g * 16;
   }
-
-  __device__ __forceinline__ void copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) const {
-    if (policy != 0) bulk_copy_hint(dst, src, bytes, bar, policy);
-    else bulk_copy_g2s(dst, src, bytes, bar);
-  }
-
-  // Blocks row[0 .. n), ids read a group ahead.  False: gave up (and told the consumers).
-  __device__ __forceinline__ bool fetch_row(const int32_t* row, int n, int head0) {
-    constexpr int kAhead = 8;
-    int id[kAhead], next[kAhead];
+  // Head `head` of block `id` (every lane's the same) into the tile at shared address
+  // `tile`; a bad id reads zeros.
+  __device__ __forceinline__ void block(uint32_t tile, int id, int head) const {
+    using TileT = Tile<HD>;
+    uint32_t size = 16u;
+    if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(num_blocks)) {
+      if ((threadIdx.x & 31) == 0) report(err, PKV_DEVERR_BLOCK_ID);
+      size = 0u;
+      id = 0;
+    }
+    const uint32_t row = static_cast<uint32_t>(id) * n_kv + head;  // (below 2^31)
+    const uint8_t* k = codes + uint64_t(row) * TileT::kCodes;
+    if constexpr (kWide) {
+      const uint8_t* v = codes_v + uint64_t(row) * TileT::kCodes;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) next[i] = i < n ? row[i] : 0;
-    for (int k0 = 0; k0 < n; k0 += kAhead) {
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) id[i] = next[i];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) next[i] = k0 + kAhead + i < n ? row[k0 + kAhead + i] : 0;
-      if (*ring.abort_flag) return false;
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (k0 + i >= n) break;
-        if (!fetch(id[i], head0)) {
-          *ring.abort_flag = 1;
-          return false;
-        }
+      for (int i = 0; i < TileT::kCodes / 512; ++i) {
+        copy16(tile + at_codes + i * 512, k + i * 512, size, policy);
+        copy16(tile + at_codes + TileT::kVCodes + i * 512, v + i * 512, size, policy);
       }
+    } else if (has_codes) {
+      copy16(tile + at_codes, k, size, policy);
     }
-    return true;
-  }
-
-  // At the end: until the consumers have left the last tile, and all have landed; where
-  // some thread gave up, a bounded wait for the copies still in flight, so that none
-  // lands after the CTA has left.
-  __device__ __forceinline__ void finish() const {
-    if (issued == 0) return;
-    const uint32_t last = issued - 1, st = last % ring.nstages;
-    const bool left = wait_or_abort(ring.empty + st, (last / ring.nstages) & 1, ring.abort_flag);
-    if (!left || *ring.abort_flag) attn::ring_drain(ring, issued);
+    if (has_groups) copy16(tile + at_groups, groups + uint64_t(row) * TileT::kGroups, size, policy);
   }
 };
 
-// Consumer warp: its next NB tiles of the ring.  After a wait that gave up the warp goes
-// on over what is there (its work is all its lanes'); gave_up tells before anything is
-// stored.
-template <int NB, typename RowsT>
-__device__ __forceinline__ void take_tiles(RowsT& rows, const Ring& ring, RingPos& pos, int j0,
-                                           int valid, bool use, int32_t* err) {
-  const uint8_t* t[NB];
-  RingPos at[NB];
-#pragma unroll
-  for (int i = 0; i < NB; ++i) {
-    at[i] = pos;
-    t[i] = ring.k_tile(pos.st);
-    wait_or_flag(ring.full + pos.st, pos.round & 1, ring.abort_flag, err);
-    pos.next(ring);
-  }
-  if (use) rows.template blocks<NB>(t, j0, valid);
-#pragma unroll
-  for (int i = 0; i < NB; ++i) release_tile(ring, at[i]);
+// The split entry of CTA c (of G, over U units) whose range starts at block j of a group
+// of nblk blocks: attn::split_entry, its owners by division.
+__device__ __forceinline__ int4 split_entry(int c, int G, int U, int b, int grp, int j, int nblk) {
+  if (j == 0) return make_int4(-1, 0, 0, 0);
+  // the CTA whose range holds unit u: the largest c with floor(c U / G) <= u
+  auto owner = [&](int u) {
+    return static_cast<int>((uint64_t(uint32_t(u) + 1u) * uint32_t(G) - 1u) / uint32_t(U));
+  };
+  const int first = attn::range_begin(c, U, G) - j;  // the group's first unit
+  const int c0 = owner(first);
+  // (the second of its CTAs joins them)
+  if (owner(attn::range_begin(c0 + 1, U, G)) != c) return make_int4(-1, 0, 0, 0);
+  const int flags = (attn::range_begin(c0, U, G) != first ? attn::kSplitC0Tail : 0) |
+                    (U >= G ? attn::kSplitDense : 0);
+  return make_int4(b, grp | flags, c0 | (owner(first + nblk - 1) << 16), first);
 }
 
-// CTAs of 8 consumer warps that an SM's registers hold.
+// CTAs of eight warps that an SM's registers hold (or as many more narrower ones).
 template <typename T, int HD, int NT>
 constexpr int kCtasPerSm = NT == 1 && HD * int(sizeof(T)) / 2 <= 128 ? 2 : 1;
 
-template <typename T, int HD, int NT, int CTAS>
-__global__ void __launch_bounds__(kMaxThreads, CTAS)
-    decode_kernel(const DecodeParams p, const Pools pools) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int consumers = p.hg_size;
-  Ring ring = make_ring(smem, p.nstages, Tile::bytes(p.hg_size, HD));
-  attn::ring_init(ring, consumers);
-  attn::pdl_wait();               // inputs and workspace belong to the preceding kernel
-  attn::pdl_launch_dependents();  // the merge kernel may be scheduled (it waits for this grid)
+// A ring's depth, as the SM's shared memory allows (with the kept lengths).
+template <typename T, int HD, int NT>
+constexpr int kStages = std::min(kMaxStages,
+                                 (kSmemMax / kCtasPerSm<T, HD, NT> - kKeptLens * 4 - 1024) /
+                                     (kWarps * Tile<HD>::kBytes));
 
-  const int warp = threadIdx.x >> 5;
+template <typename T, int HD, int NT>
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<T, HD, NT>)
+    decode_kernel(const DecodeParams p, const Pools pools) {
+  extern __shared__ __align__(128) uint8_t smem[];  // [kWarps][kStages] tiles, kept lengths
+  constexpr int S = kStages<T, HD, NT>;
+  attn::pdl_wait();               // inputs and workspace belong to the preceding kernel
+  attn::pdl_launch_dependents();  // the joining kernel may be scheduled (it waits for this grid)
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = gridDim.x;
+  const int me = blockIdx.x;
   int U;
   int4 st = make_int4(0, 0, 0, 0);
   int* lens_s = reinterpret_cast<int*>(smem + p.part_off);  // [kKeptLens]
-  const bool kept = p.plan_in_kernel && p.B <= kKeptLens;
+  const bool kept = p.plan_in_kernel && p.part_off != 0 && p.B <= kKeptLens;
   if (p.plan_in_kernel) {
-    // scan the units per sequence in the (still unused) ring stages
-    int* cu_s = reinterpret_cast<int*>(ring.stages);  // [B + 1]
-    int* warp_tot = cu_s + p.B + 1;                   // [32]
+    // scan the units per sequence in the (still unused) stages
+    int* cu_s = reinterpret_cast<int*>(smem);  // [B + 1]
+    int* warp_tot = cu_s + p.B + 1;            // [32]
     const int nt = blockDim.x;
     for (int b = threadIdx.x; b < p.B; b += nt) {
       if (blockIdx.x == 0) report_bad_length(p, b);
@@ -209,109 +198,124 @@ __global__ void __launch_bounds__(kMaxThreads, CTAS)
     if (threadIdx.x == nt - 1) cu_s[p.B] = run;
     __syncthreads();
     U = cu_s[p.B];
-    const int r0 = attn::range_begin(blockIdx.x, U, G);
-    if (r0 < attn::range_begin(blockIdx.x + 1, U, G)) {
+    const int r0 = attn::range_begin(me, U, G);
+    if (r0 < attn::range_begin(me + 1, U, G)) {
       const int b = attn::seq_of_unit(cu_s, p.B, r0);
       const int nblk = (cu_s[b + 1] - cu_s[b]) / p.n_groups;
       const int grp = (r0 - cu_s[b]) / nblk;
       st = make_int4(b, grp, (r0 - cu_s[b]) - grp * nblk, 0);
     }
-    attn::zero_empty<T, HD>(p, blockIdx.x, G, [&](int b) { return cu_s[b + 1] == cu_s[b]; });
+    attn::zero_empty<T, HD>(p, blockIdx.x, gridDim.x, [&](int b) { return cu_s[b + 1] == cu_s[b]; });
     if (blockIdx.x == 0 && threadIdx.x == 0) {
       p.total_units[0] = U;
       p.total_units[1] = -1;  // a call planning for itself replaces any kept plan
     }
-    fence_proxy_async_smem();  // the scan's stores come before the ring's copies
-    __syncthreads();
+    __syncthreads();  // (the stages are the rings' from here on)
   } else {
     U = __ldcg(p.total_units);
-    st = __ldcg(p.starts + blockIdx.x);
+    st = __ldcg(p.starts + me);
   }
-  const int r0 = attn::range_begin(blockIdx.x, U, G);
-  const int r1 = attn::range_begin(blockIdx.x + 1, U, G);
+  const int r0 = attn::range_begin(me, U, G);
+  const int r1 = attn::range_begin(me + 1, U, G);
   const int rows_per_group = p.hg_size * p.rep;
+  if (r0 >= r1) {
+    if (threadIdx.x == 0) p.splits[me] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  uint8_t* ring = smem + warp * S * Tile<HD>::kBytes;
+  const uint32_t ring_at = smem_addr(ring);
+  const Fetcher<HD> fetch(pools, p.n_kv, p.num_blocks, p.err);
   Walk cur{p, kept ? lens_s : nullptr};
-  if (r0 < r1) cur.begin(st);
+  cur.begin(st);
 
-  if (warp == consumers) {
-    // -------------------------------------------------------- producer
-    if (elect_one()) {
-      const int nblk0 = cur.nblk;
-      // (each block is read once: its lines leave L2 first)
-      Producer<HD> pr{ring, pools, p.num_blocks, p.n_kv, p.hg_size, p.err, tc::l2_evict_first_policy()};
-      bool ok = true;
-      for (int u = r0; u < r1 && ok;) {
-        const int n = min(r1 - u, cur.nblk - cur.j);
-        ok = pr.fetch_row(p.bt + int64_t(cur.b) * p.W + cur.j, n, cur.grp * p.hg_size);
-        u += n;
-        cur.advance(n);
+  // ---- the blocks on their way: a walk of its own, some stages ahead.  Lane i holds the
+  // id of block fj + i of the walk's segment (its next 32).
+  Walk ahead = cur;
+  int left = r1 - r0, seg = min(left, ahead.nblk - ahead.j), k = 0, ids = 0;
+  uint32_t fill = 0;  // offset of the next stage to fill
+  auto feed = [&]() {
+    if (left > 0) {
+      if ((k & 31) == 0) {
+        const int i = k + lane;
+        if (i < seg) ids = p.bt[int64_t(ahead.b) * p.W + ahead.j + i];
       }
-      // the split group this CTA merges (read by the merge kernel)
-      p.splits[blockIdx.x] =
-          r0 < r1 ? attn::split_entry(blockIdx.x, G, U, st.x, st.y, st.z, nblk0)
-                  : make_int4(-1, 0, 0, 0);
-      pr.finish();
+      fetch.block(ring_at + fill, __shfl_sync(0xffffffffu, ids, k & 31),
+                  ahead.grp * p.hg_size + warp);
+      fill = fill == (S - 1) * Tile<HD>::kBytes ? 0 : fill + Tile<HD>::kBytes;
+      --left;
+      if (++k == seg) {
+        ahead.advance(seg);
+        seg = min(left, ahead.nblk - ahead.j);
+        k = 0;
+      }
     }
-  } else if (warp < consumers) {
-    // ------------------------------------------------------- consumers
-    using RowsT = Rows<T, HD, NT, false>;
-    RowsT rows;
-    rows.place(p.hg_size, warp);
-    RingPos pos;
-    const T* q = static_cast<const T*>(p.q);
-    T* out = static_cast<T*>(p.out);
-    for (int u = r0; u < r1;) {
-      const int n = min(r1 - u, cur.nblk - cur.j);
-      const int b = cur.b;
-      const int kv_head = cur.grp * p.hg_size + warp;
-      const int head0 = kv_head * p.rep;
-      const int last = cur.L - 1;
-      rows.begin(
-          [&](int r) -> const T* {
-            return r < p.rep ? q + (int64_t(b) * p.n_heads + head0 + r) * HD : nullptr;
-          },
-          [&](int) { return last; }, p.scale_log2 * pools.k_scale[kv_head], pools.v_scale[kv_head]);
-      for (int k = 0; k < n;) {
-        if ((k & 31) == 0 && gave_up(ring)) break;
-        const int j0 = (cur.j + k) * kBS;
-        if (RowsT::PAIR == 2 && k + 1 < n) {
-          take_tiles<RowsT::PAIR>(rows, ring, pos, j0, cur.L - j0, true, p.err);
-          k += RowsT::PAIR;
-        } else {
-          take_tiles<1>(rows, ring, pos, j0, cur.L - j0, true, p.err);
-          ++k;
-        }
-      }
-      if (gave_up(ring)) break;
-      if (cur.j == 0 && n == cur.nblk) {
-        rows.store([&](int r) -> T* {
-          return r < p.rep ? out + (int64_t(b) * p.n_heads + head0 + r) * HD : nullptr;
-        });
-      } else {  // a group split over several CTAs
-        const int slot = 2 * blockIdx.x + (u == r0 ? 0 : 1);
-        const int64_t base = int64_t(slot) * rows_per_group + warp * p.rep;
-        rows.store_partial(
-            [&](int r) -> float* { return r < p.rep ? p.ws_o + (base + r) * HD : nullptr; },
-            [&](int r) -> float* { return p.ws_ml + (base + r) * 2; });
-      }
-      u += n;
-      cur.advance(n);
+    commit_copies();  // (an empty group past the last block: waits count groups)
+  };
+#pragma unroll 1
+  for (int i = 0; i < S; ++i) feed();
+  // (while the first blocks come)
+  if (warp == 0) {
+    const int4 entry = split_entry(me, G, U, st.x, st.y, st.z, cur.nblk);
+    if (lane == 0) p.splits[me] = entry;
+  }
+
+  using RowsT = Rows<T, HD, NT, false>;
+  RowsT rows;
+  rows.place();
+  uint32_t at = 0;  // offset of the stage of the next block
+  // The warp's next NB tiles; their stages are filled again.  EDGE: some token may lie
+  // past the sequence's end.
+  auto take = [&](auto nb, auto edge, int j0) {
+    constexpr int NB = decltype(nb)::value;
+    const uint8_t* t[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      t[i] = ring + at;
+      at = at == (S - 1) * Tile<HD>::kBytes ? 0 : at + Tile<HD>::kBytes;
     }
+    wait_copies<S - NB>();
+    rows.template blocks<NB, decltype(edge)::value>(t, j0, cur.L - j0);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < NB; ++i) feed();
+  };
+  const T* q = static_cast<const T*>(p.q);
+  T* out = static_cast<T*>(p.out);
+  for (int u = r0; u < r1;) {
+    const int n = min(r1 - u, cur.nblk - cur.j);
+    const int kv_head = cur.grp * p.hg_size + warp;
+    const int64_t row0 = int64_t(cur.b) * p.n_heads + int64_t(kv_head) * p.rep;
+    const int last = cur.L - 1;
+    rows.begin([&](int r) -> const T* { return r < p.rep ? q + (row0 + r) * HD : nullptr; },
+               [&](int) { return last; }, p.scale_log2 * pools.k_scale[kv_head],
+               pools.v_scale[kv_head]);
+    const int full = min(n, cur.L / kBS - cur.j);  // blocks without an edge
+    int i = 0;
+    for (; i + RowsT::PAIR <= full; i += RowsT::PAIR)
+      take(std::integral_constant<int, RowsT::PAIR>{}, std::false_type{}, (cur.j + i) * kBS);
+    for (; i < n; ++i) take(std::integral_constant<int, 1>{}, std::true_type{}, (cur.j + i) * kBS);
+    if (cur.j == 0 && n == cur.nblk) {
+      rows.store([&](int r) -> T* { return r < p.rep ? out + (row0 + r) * HD : nullptr; });
+    } else {  // a group that several CTAs share
+      const int64_t base = int64_t(2 * me + (u == r0 ? 0 : 1)) * rows_per_group + warp * p.rep;
+      rows.store_partial(
+          [&](int r) -> float* { return r < p.rep ? p.ws_o + (base + r) * HD : nullptr; },
+          [&](int r) -> float* { return p.ws_ml + (base + r) * 2; });
+    }
+    u += n;
+    cur.advance(n);
   }
 }
 
-// Batches too small to stream: one cluster of C CTAs per (sequence, head group), each a
-// contiguous part of the sequence's at most 8 * C blocks, the parts combined through
-// distributed shared memory (as the 8-bit decode's cluster path; no workspace, no merge
-// launch).
+// Batches too small to stream: one cluster of C CTAs per (sequence, head group), a warp
+// per head of the group, each CTA a contiguous part of the sequence's at most
+// kMaxBlocks * C blocks, the parts combined through distributed shared memory (no
+// workspace, no joining launch).
 template <typename T, int HD, int NT>
-__global__ void __launch_bounds__(kMaxThreads, 1)
+__global__ void __launch_bounds__(kWarps * 32, 1)
     decode_cluster_kernel(const DecodeParams p, const Pools pools) {
   extern __shared__ __align__(128) uint8_t smem[];
-  const int consumers = p.hg_size;
-  Ring ring = make_ring(smem, p.nstages, Tile::bytes(p.hg_size, HD));
-  attn::ring_init(ring, consumers);
-  const int warp = threadIdx.x >> 5;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int C = p.cluster;
   const int rank = static_cast<int>(cluster_ctarank());
   const int seg = static_cast<int>(blockIdx.x) / C;  // (sequence, head group)
@@ -325,49 +329,46 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
   attn::pdl_launch_dependents();
   const int L = length_of(p, b);
   const int nblk = (L + kBS - 1) / kBS;
-  const int j0 = rank * nblk / C, j1 = (rank + 1) * nblk / C;
+  const int j0 = rank * nblk / C, n = (rank + 1) * nblk / C - j0;  // n <= p.nstages
   if (blockIdx.x == 0 && threadIdx.x == 0)
     p.total_units[1] = -1;  // a call planning for itself replaces any kept plan
   if (rank == 0 && grp == 0 && threadIdx.x == 0) report_bad_length(p, b);
-
-  uint32_t issued = 0;
-  if (warp == consumers) {
-    if (elect_one()) {
-      Producer<HD> pr{ring, pools, p.num_blocks, p.n_kv, p.hg_size, p.err, tc::l2_evict_first_policy()};
-      pr.fetch_row(p.bt + int64_t(b) * p.W + j0, j1 - j0, grp * p.hg_size);
-      issued = pr.issued;
-    }
-  } else if (warp < consumers) {
-    using RowsT = Rows<T, HD, NT, false>;
-    const T* q = static_cast<const T*>(p.q);
-    const int kv_head = grp * p.hg_size + warp;
-    const int head0 = kv_head * p.rep;
-    RowsT rows;
-    rows.place(p.hg_size, warp);
-    rows.begin(
-        [&](int r) -> const T* {
-          return r < p.rep ? q + (int64_t(b) * p.n_heads + head0 + r) * HD : nullptr;
-        },
-        [&](int) { return L - 1; }, p.scale_log2 * pools.k_scale[kv_head], pools.v_scale[kv_head]);
-    RingPos pos;
-    for (int j = j0; j < j1;) {
-      const int jp = j * kBS;
-      if (RowsT::PAIR == 2 && j + 1 < j1) {
-        take_tiles<RowsT::PAIR>(rows, ring, pos, jp, L - jp, true, p.err);
-        j += RowsT::PAIR;
-      } else {
-        take_tiles<1>(rows, ring, pos, jp, L - jp, true, p.err);
-        ++j;
-      }
-    }
-    // this CTA's part (also after an abort, so the barrier below is reached)
-    rows.store_partial(
-        [&](int r) -> float* { return r < p.rep ? part_o + (warp * p.rep + r) * HD : nullptr; },
-        [&](int r) -> float* { return part_ml + (warp * p.rep + r) * 2; });
+  const int kv_head = grp * p.hg_size + warp;
+  const uint8_t* tiles = smem + warp * p.nstages * Tile<HD>::kBytes;
+  {
+    const Fetcher<HD> fetch(pools, p.n_kv, p.num_blocks, p.err);
+    const int ids = lane < n ? p.bt[int64_t(b) * p.W + j0 + lane] : 0;
+    for (int i = 0; i < n; ++i)
+      fetch.block(smem_addr(tiles) + i * Tile<HD>::kBytes, __shfl_sync(0xffffffffu, ids, i), kv_head);
+    commit_copies();
   }
+  using RowsT = Rows<T, HD, NT, false>;
+  const T* q = static_cast<const T*>(p.q) + (int64_t(b) * p.n_heads + int64_t(kv_head) * p.rep) * HD;
+  RowsT rows;
+  rows.place();
+  rows.begin([&](int r) -> const T* { return r < p.rep ? q + r * HD : nullptr; },
+             [&](int) { return L - 1; }, p.scale_log2 * pools.k_scale[kv_head],
+             pools.v_scale[kv_head]);
+  wait_copies<0>();
+  for (int i = 0; i < n;) {
+    const int jp = (j0 + i) * kBS;
+    const uint8_t* t = tiles + i * Tile<HD>::kBytes;
+    if (RowsT::PAIR == 2 && i + 1 < n) {
+      const uint8_t* two[2] = {t, t + Tile<HD>::kBytes};
+      rows.template blocks<2, true>(two, jp, L - jp);
+      i += 2;
+    } else {
+      const uint8_t* one[1] = {t};
+      rows.template blocks<1, true>(one, jp, L - jp);
+      ++i;
+    }
+  }
+  // this CTA's part
+  rows.store_partial(
+      [&](int r) -> float* { return r < p.rep ? part_o + (warp * p.rep + r) * HD : nullptr; },
+      [&](int r) -> float* { return part_ml + (warp * p.rep + r) * 2; });
 
   cluster_sync();  // every CTA's partial is in its shared memory
-  if (*ring.abort_flag) attn::ring_drain(ring, issued);  // (as Producer::finish)
   // CTA `rank` combines elements [rank E / C, (rank + 1) E / C) of the group
   const int E = rows_per_group * HD;
   const int e0 = rank * E / C, e1 = (rank + 1) * E / C;
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     float oc[kMaxCluster];
 #pragma unroll
     for (int c = 0; c < kMaxCluster; ++c) {  // every peer's values in one round trip
-      ml[c] = make_float2(-INFINITY, 0.f);
+      ml[c] = make_float2(0.f, 0.f);
       oc[c] = 0.f;
       if (c < C) {
         ml[c] = ld_cluster_f32x2(cluster_map(part_ml + r * 2, c));
@@ -407,43 +408,16 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 
 template <typename T, int HD, int NT>
 struct DecodeFp4 {
-  static constexpr int kSmemMax = 226 * 1024;  // what both kernels opt in to
-  static int stage_bytes(int hg) { return Tile::bytes(hg, HD); }
-  // barriers, alignment slack and ring; what follows starts there
-  static size_t smem_for(int hg, int nstages) {
-    return kBarrierBytes + 1024 + size_t(nstages) * stage_bytes(hg);
-  }
-  static constexpr int kDoubled = kCtasPerSm<T, HD, NT>;
-  // Ring depth: about 176 KB of stages per SM, shared by the CTAs of 8 consumer warps
-  // in all (narrow groups: several CTAs per SM, each with its barriers and kept
-  // lengths).
-  static int ring_stages(int hg) {
-    const int ctas = std::max(1, 8 / hg) * kDoubled;
-    const int ns = (176 - 4 * (ctas - 1)) * 1024 / ctas / stage_bytes(hg);
-    return std::max(2, std::min(kMaxStages, ns));
-  }
-  static cudaError_t grid(const AttnArgs& a, int hg, int* G, size_t* smem, int* nstages, int* wave) {
-    *nstages = ring_stages(hg);
-    *smem = smem_for(hg, *nstages) + kKeptLens * 4;
-    static KernelSetup setup;
-    int per_sm = 0;
-    const cudaError_t e = kernel_setup(setup, decode_kernel<T, HD, NT, kDoubled>, static_cast<int>(*smem),
-                                       (hg + 1) * 32, &per_sm, kSmemMax);
-    if (e != cudaSuccess) return e;
-    per_sm = std::max(1, std::min(per_sm, 16));  // 16: what the workspace is sized for
-    *G = sm_count() * per_sm;
-    *wave = *G / kDoubled;
-    if (a.max_ctas > 0 && a.max_ctas < *G) *G = a.max_ctas;
-    const int64_t max_units = int64_t(a.num_seqs) * (a.pool.n_kv / hg) *
-                              ((int64_t(a.max_seq_len) + kBS - 1) / kBS);
-    if (max_units < *G) *G = static_cast<int>(std::max<int64_t>(1, max_units));
-    return cudaSuccess;
+  static constexpr int kCtas = kCtasPerSm<T, HD, NT>;
+  static constexpr int kDepth = kStages<T, HD, NT>;
+  static_assert(kDepth >= 3, "a pair of blocks at hand and one on its way");
+  static size_t ring_bytes(int warps, int nstages) {
+    return (size_t(warps) * nstages * Tile<HD>::kBytes + 127) / 128 * 128;
   }
 
   static cudaError_t run(const AttnArgs& a, const Fp4Cache& cache, cudaStream_t stream) {
     const PoolShape& pool = a.pool;
     const Pools pools(cache);
-    const int hg = head_group(pool.n_kv);
     DecodeParams p{};
     p.q = a.q;
     p.out = a.out;
@@ -454,18 +428,30 @@ struct DecodeFp4 {
     p.n_heads = a.n_heads;
     p.n_kv = pool.n_kv;
     p.rep = a.n_heads / pool.n_kv;
-    p.hg_size = hg;
-    p.n_groups = pool.n_kv / hg;
     p.W = a.max_blocks_per_seq;
     p.num_blocks = pool.num_blocks;
     p.max_len = a.max_seq_len;  // (no more than the tables hold)
     p.max_seq_len = a.max_seq_len;
     p.head_dim = HD;
     p.scale_log2 = a.scale * attn::kLog2e;
-    int G = 0, wave = 0;
-    size_t smem = 0;
-    cudaError_t e = grid(a, hg, &G, &smem, &p.nstages, &wave);
+    const int hg = head_group(pool.n_kv);
+    p.hg_size = hg;
+    p.n_groups = pool.n_kv / hg;
+    // (narrow groups have many CTAs an SM, and read lengths again)
+    const size_t kept = hg >= 4 ? kKeptLens * 4 : 0;
+    const size_t smem = ring_bytes(hg, kDepth) + kept;
+    static KernelSetup setup;
+    int per_sm = 0;
+    cudaError_t e = kernel_setup(setup, decode_kernel<T, HD, NT>, static_cast<int>(smem), hg * 32,
+                                 &per_sm, kSmemMax);
     if (e != cudaSuccess) return e;
+    per_sm = std::max(1, std::min(per_sm, 16));  // 16: what the workspace is sized for
+    int G = sm_count() * per_sm;
+    const int wave = G / kCtas;
+    if (a.max_ctas > 0 && a.max_ctas < G) G = a.max_ctas;
+    const int nmax = p.max_len / kBS + (p.max_len % kBS != 0);
+    const int64_t max_units = int64_t(a.num_seqs) * p.n_groups * nmax;
+    if (max_units < G) G = static_cast<int>(std::max<int64_t>(1, max_units));
     if (G > 65535) return cudaErrorInvalidValue;  // split entries pack CTA indices in 16 bits
     p.grid = G;
     const DecodeWs L(a.num_seqs, G, size_t(hg) * p.rep, HD);
@@ -481,47 +467,48 @@ struct DecodeFp4 {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3((hg + 1) * 32);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
 
-    // Latency-bound batches, by the rule of the bf16 decode: the longest sequence at
-    // most 64 blocks and the clusters within two waves.
-    const int nmax = p.max_len / kBS + (p.max_len % kBS != 0);
+    // Latency-bound batches, by the rule of the bf16 decode: the longest sequence at most
+    // 64 blocks and the clusters within two waves.
     const int C = std::max(1, std::min(kMaxCluster, (nmax + 3) / 4));
-    const int64_t ctas = int64_t(p.B) * p.n_groups * C;
-    if (a.max_ctas == 0 && nmax <= 8 * kMaxCluster && ctas <= 2 * int64_t(wave)) {
+    const int64_t cluster_ctas = int64_t(p.B) * p.n_groups * C;
+    if (a.max_ctas == 0 && nmax <= kMaxBlocks * kMaxCluster && cluster_ctas <= 2 * int64_t(wave)) {
       p.cluster = C;
-      p.nstages = std::max(2, std::min(p.nstages, (nmax + C - 1) / C));
+      p.nstages = std::max(1, (nmax + C - 1) / C);
+      p.part_off = static_cast<int>(ring_bytes(hg, p.nstages));
       const size_t rows = size_t(hg) * p.rep;
-      const size_t extra = rows * HD * 4 + (rows * 2 * 4 + 15) / 16 * 16;
-      while (p.nstages > 2 && smem_for(hg, p.nstages) + extra > size_t(kSmemMax)) --p.nstages;
-      p.part_off = static_cast<int>(smem_for(hg, p.nstages));
-      static KernelSetup setup;
-      e = kernel_setup(setup, decode_cluster_kernel<T, HD, NT>, kSmemMax, (hg + 1) * 32, nullptr);
+      const size_t need = p.part_off + rows * HD * 4 + (rows * 2 * 4 + 15) / 16 * 16;
+      if (need > size_t(kSmemMax)) return cudaErrorInvalidValue;
+      static KernelSetup cluster_setup;
+      e = kernel_setup(cluster_setup, decode_cluster_kernel<T, HD, NT>, kSmemMax, kWarps * 32, nullptr);
       if (e != cudaSuccess) return e;
       attr[1].id = cudaLaunchAttributeClusterDimension;
       attr[1].val.clusterDim.x = static_cast<unsigned>(C);
       attr[1].val.clusterDim.y = 1;
       attr[1].val.clusterDim.z = 1;
       cfg.numAttrs = 2;
-      cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-      cfg.dynamicSmemBytes = p.part_off + extra;
+      cfg.gridDim = dim3(static_cast<unsigned>(cluster_ctas));
+      cfg.blockDim = dim3(hg * 32);
+      cfg.dynamicSmemBytes = need;
       e = cudaLaunchKernelEx(&cfg, decode_cluster_kernel<T, HD, NT>, p, pools);
       return e != cudaSuccess ? e : cudaGetLastError();
     }
-    p.part_off = static_cast<int>(smem_for(hg, p.nstages));  // the kept lengths
-    // every CTA scans the lengths in its ring stages; larger batches have a plan kernel
+    p.nstages = kDepth;
+    p.part_off = kept != 0 ? static_cast<int>(ring_bytes(hg, kDepth)) : 0;  // the kept lengths
+    // every CTA scans the lengths in its stages; larger batches have a plan kernel
     p.plan_in_kernel = a.num_seqs <= kKernelPlanSeqs &&
-                       size_t(a.num_seqs + 1 + 32) * 4 <= size_t(p.nstages) * stage_bytes(hg);
+                       size_t(a.num_seqs + 1 + 32) * 4 <= size_t(hg) * kDepth * Tile<HD>::kBytes;
     if (!p.plan_in_kernel) {
       attn::decode_plan_kernel<T, HD><<<1, 1024, 0, stream>>>(p);
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     cfg.gridDim = dim3(G);
+    cfg.blockDim = dim3(hg * 32);
     cfg.dynamicSmemBytes = smem;
-    e = cudaLaunchKernelEx(&cfg, decode_kernel<T, HD, NT, kDoubled>, p, pools);
+    e = cudaLaunchKernelEx(&cfg, decode_kernel<T, HD, NT>, p, pools);
     if (e != cudaSuccess) return e;
     const int vecs = hg * p.rep * HD / 4;  // of a group's rows
     const int threads = std::min(fp8::kJoinThreads, (vecs + 31) / 32 * 32);

@@ -4,10 +4,13 @@
 // Mathematics.  With k4, v4 the products of code and group scale (exact f16 numbers)
 // and kg, vg the head's scales:
 //   x = (q . k4) * (scale * log2 e * kg)      scores in log2 units
-//   M = running max of x,  p = 2^(x - M + 15)
-//   l += p,   O += p v4,   out = vg O / l.
-// The head's scales are constants of a warp, so they cost nothing per key.  Weights
-// are at most 2^15, f16 numbers (normal down to 2^-29 of the largest).
+//   p = 2^(x - M + 4),  l += p,   O += p v4,   out = vg O / l.
+// The head's scales are constants of a warp, so they cost nothing per key.  M is a
+// running reference, the maximum of x when it was last set: weights are computed
+// against it as it stands, and only if they come out past f16's range (the maximum has
+// grown 2^12-fold: seldom after the first block) is the maximum taken, the reference
+// moved to it and what came before rescaled.  Weights are f16 numbers, normal down to
+// 2^-18 of the reference's.
 //
 // Tensor cores: m16n8k16 with f16 operands and fp32 sums.  A bf16 query row is exact
 // in f16 once it is multiplied by the power of two that brings its largest element
@@ -46,19 +49,19 @@ using fp8::pack_f16x2;
 using fp8::transpose_8x8;
 using fp8::unpack_f16x2;
 
-constexpr float kWeightLog2 = 15.f;  // log2 of the largest weight
+constexpr float kWeightLog2 = 4.f;     // log2 of the reference's weight
+constexpr float kWeightMax = 65504.f;  // f16's largest
+// No reference yet: below every score that fp32 holds by more than it rounds away, so
+// that a visible key's weight comes out infinite and a hidden one's (-inf) zero.
+constexpr float kNone = -3.0e38f;
 
-// A block of `heads` heads in shared memory, as it lies in the pools: K codes, V codes,
-// K groups, V groups, each [heads][16 tokens][..].
+// A head's block in shared memory: K codes, V codes, K scales, V scales as they lie in
+// the pools, each [16 tokens][..].
+template <int HD>
 struct Tile {
-  int k_groups, v_codes, v_groups;  // offsets in bytes from the K codes
-  static __host__ __device__ Tile of(int heads, int hd) {
-    const int codes = heads * kBS * hd / 2, groups = heads * kBS * hd / kGroup;
-    return Tile{2 * codes, codes, 2 * codes + groups};
-  }
-  static __host__ __device__ int bytes(int heads, int hd) {
-    return 2 * heads * kBS * (hd / 2 + hd / kGroup);
-  }
+  static constexpr int kCodes = kBS * HD / 2, kGroups = kBS * HD / kGroup;
+  static constexpr int kVCodes = kCodes, kKGroups = 2 * kCodes, kVGroups = 2 * kCodes + kGroups;
+  static constexpr int kBytes = 2 * (kCodes + kGroups);
 };
 
 __device__ __forceinline__ int tok(int i) { return static_cast<int>((0x67453210u >> (4 * i)) & 15u); }
@@ -89,21 +92,18 @@ struct Rows {
   int last[NT][2];
   int cut;             // least last key over the active rows
   float vg;            // the head's scale of V
-  Tile tile;
   int kc, kg, vc[2], vgr[2];  // this lane's pieces: K codes and scales, V codes and scales
 
-  // Where the warp's head lies in the tile of a block of `heads` heads.
-  __device__ __forceinline__ void place(int heads, int head) {
+  // Where the lane's pieces lie in a tile.
+  __device__ __forceinline__ void place() {
     const int lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
-    tile = Tile::of(heads, HD);
-    kc = (head * kBS + tok(g)) * (HD / 2) + c * KD / 2;
-    kg = tile.k_groups + (head * kBS + tok(g)) * KK + c * KD / kGroup;
+    kc = tok(g) * (HD / 2) + c * KD / 2;
+    kg = Tile<HD>::kKGroups + tok(g) * KK + c * KD / kGroup;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int row = head * kBS + tok(2 * c + i);
-      vc[i] = tile.v_codes + row * (HD / 2) + g * DB / 2;
-      vgr[i] = tile.v_groups + row * KK + g * DB / kGroup;
+      vc[i] = Tile<HD>::kVCodes + tok(2 * c + i) * (HD / 2) + g * DB / 2;
+      vgr[i] = Tile<HD>::kVGroups + tok(2 * c + i) * KK + g * DB / kGroup;
     }
   }
 
@@ -147,11 +147,12 @@ struct Rows {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int r = nt * 8 + 2 * c + j;
-        rs[nt][j] = __shfl_sync(0xffffffffu, back, (2 * c + j) * 4);
+        // (not zero: a hidden key's -inf stays -inf)
+        rs[nt][j] = fmaxf(__shfl_sync(0xffffffffu, back, (2 * c + j) * 4), 1.2e-38f);
         // a row without a query is never masked (and never stored)
         last[nt][j] = q_row(r) ? last_key(r) : INT_MAX;
         least = min(least, last[nt][j]);
-        m[nt][j] = -INFINITY;
+        m[nt][j] = kNone;
         l[nt][j] = 0.f;
       }
 #pragma unroll
@@ -179,42 +180,40 @@ struct Rows {
 
   // NB consecutive blocks: their tiles, the position j0 of the first token, the
   // sequence's tokens from there on (valid: V rows past them are not used).  Two at a
-  // time share one maximum, one rescaling and the latency of each step.
-  template <int NB>
+  // time share the latency of each step.  EDGE: some row may not see some of their tokens.
+  template <int NB, bool EDGE>
   __device__ __forceinline__ void blocks(const uint8_t* const (&t)[NB], int j0, int valid) {
-    uint32_t vw[NB][4][VW];  // tokens tok(2c), tok(2c + 1), and those + 8
-    uint32_t vs[NB][4];      // their scales' codes
-    float w[NB][NT][4];      // scores, then weights
-    // ---- S^T = K Q^T, two chains of products
+    float w[NB][NT][4];  // scores before their factor
+    // ---- S^T = K Q^T
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      uint32_t kw[2][KW], ks[2][(KD + 15) / 16];  // [token g | g + 8]: codes; scales, twice each
+      uint32_t kw[2][KW];
+      __half2 ks[2][(KD + 15) / 16];  // [token g | g + 8]: codes; scales, twice each
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         load_codes<KW, KD>(t[nb] + kc + h * 8 * (HD / 2), kw[h]);
         const uint8_t* sp = t[nb] + kg + h * 8 * KK;
         if constexpr (KD == 32) {
           const uint32_t s2 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(sp));
-          ks[h][0] = __byte_perm(s2, s2, 0x1010);
-          ks[h][1] = __byte_perm(s2, s2, 0x3232);
+          ks[h][0] = __low2half2(*reinterpret_cast<const __half2*>(&s2));
+          ks[h][1] = __high2half2(*reinterpret_cast<const __half2*>(&s2));
         } else {
-          ks[h][0] = scales_f16x2(*sp, *sp);
+          const uint32_t s2 = e4m3x2_to_f16x2(*sp);
+          ks[h][0] = __low2half2(*reinterpret_cast<const __half2*>(&s2));
         }
       }
-      constexpr int CH = KK >= 4 ? 2 : 1;
-      float s[NT][CH][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < CH; ++i) s[nt][i][0] = s[nt][i][1] = s[nt][i][2] = s[nt][i][3] = 0.f;
+        w[nb][nt][0] = w[nb][nt][1] = w[nb][nt][2] = w[nb][nt][3] = 0.f;
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
         uint32_t a[2][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           codes_to_f16x2(kw[h][i], a[h]);
+          const uint32_t sc = *reinterpret_cast<const uint32_t*>(&ks[h][i / 2]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) a[h][e] = mul_f16x2(a[h][e], ks[h][i / 2]);
+          for (int e = 0; e < 4; ++e) a[h][e] = mul_f16x2(a[h][e], sc);
         }
 #pragma unroll
         for (int e = 0; e < 2 && 2 * i + e < KK; ++e) {
@@ -223,21 +222,13 @@ struct Rows {
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int pt = 0; pt < PARTS; ++pt)
-              mma_f16_16816(s[nt][kk % CH], a[0][2 * e], a[1][2 * e], a[0][2 * e + 1],
+              mma_f16_16816(w[nb][nt], a[0][2 * e], a[1][2 * e], a[0][2 * e + 1],
                             a[1][2 * e + 1], qb[nt][pt][kk][0], qb[nt][pt][kk][1]);
         }
       }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = s[nt][0][e];
-          if constexpr (CH == 2) x += s[nt][1][e];
-          w[nb][nt][e] = x * rs[nt][e & 1];
-        }
     }
-    // ---- mask, running maximum, weights
-    const bool masked = j0 + NB * kBS - 1 > cut;
+    // ---- mask, weights
+    const bool masked = EDGE && j0 + NB * kBS - 1 > cut;
     if (masked) {
       const int t0 = j0 + tok((threadIdx.x & 31) >> 2);
 #pragma unroll
@@ -248,54 +239,62 @@ struct Rows {
           for (int e = 0; e < 4; ++e)
             if (t0 + nb * kBS + (e >> 1) * 8 > last[nt][e & 1]) w[nb][nt][e] = -INFINITY;
     }
-    float d[NT][2];  // log2 of the factor on what came before
-    bool moved = false;
+    float pw[NB][NT][4];
+    float add[NT][2];
+    auto weigh = [&]() {  // whether some weights are past f16's range, or there is no reference
+      bool past = false;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float mx = fmaxf(w[0][nt][j], w[0][nt][2 + j]);
+        for (int j = 0; j < 2; ++j) {
+          const float cst = kWeightLog2 - m[nt][j];
+          add[nt][j] = 0.f;
 #pragma unroll
-        for (int nb = 1; nb < NB; ++nb) mx = fmaxf(mx, fmaxf(w[nb][nt][j], w[nb][nt][2 + j]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        const float mn = fmaxf(m[nt][j], mx);
-        const float ref = mn == -INFINITY ? 0.f : mn;  // nothing visible yet
-        d[nt][j] = m[nt][j] - ref;
-        moved |= mn != m[nt][j];
-        m[nt][j] = mn;
-      }
-    // rescaled only when some row's maximum moved
-    if (__any_sync(0xffffffffu, moved)) {
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float x = fast_exp2(fmaf(w[nb][nt][2 * e + j], rs[nt][j], cst));
+              pw[nb][nt][2 * e + j] = x;
+              add[nt][j] += x;
+            }
+          past |= add[nt][j] > kWeightMax;  // (no weight is larger than their sum)
+        }
+      return past;
+    };
+    // (without a reference m is kNone, and weights of keys that are seen come out infinite)
+    if (__any_sync(0xffffffffu, weigh())) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float a0 = fast_exp2(d[nt][0]), a1 = fast_exp2(d[nt][1]);
-        l[nt][0] *= a0;
-        l[nt][1] *= a1;
+        float d[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) mx = fmaxf(mx, fmaxf(w[nb][nt][j], w[nb][nt][2 + j]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const float mn = fmaxf(m[nt][j], mx * rs[nt][j]);
+          d[j] = fast_exp2(m[nt][j] - mn);
+          m[nt][j] = mn;
+          l[nt][j] *= d[j];
+        }
 #pragma unroll
         for (int i = 0; i < KK; ++i) {
-          o[nt][i][0] *= a0;
-          o[nt][i][1] *= a1;
-          o[nt][i][2] *= a0;
-          o[nt][i][3] *= a1;
+          o[nt][i][0] *= d[0];
+          o[nt][i][1] *= d[1];
+          o[nt][i][2] *= d[0];
+          o[nt][i][3] *= d[1];
         }
       }
+      weigh();
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float ref = (m[nt][j] == -INFINITY ? 0.f : m[nt][j]) - kWeightLog2;
-        float sum = 0.f;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          w[nb][nt][j] = fast_exp2(w[nb][nt][j] - ref);
-          w[nb][nt][2 + j] = fast_exp2(w[nb][nt][2 + j] - ref);
-          sum += w[nb][nt][j] + w[nb][nt][2 + j];
-        }
-        l[nt][j] += sum;
-      }
+      for (int j = 0; j < 2; ++j) l[nt][j] += add[nt][j];
+    uint32_t vw[NB][4][VW];  // tokens tok(2c), tok(2c + 1), and those + 8
+    uint32_t vs[NB][4];      // their scales' codes
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -305,7 +304,7 @@ struct Rows {
       }
     // V rows past the sequence's end hold whatever the pool holds there: codes, which
     // are finite, under scales taken as zero
-    if (valid < NB * kBS) {
+    if (EDGE && valid < NB * kBS) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -329,7 +328,7 @@ struct Rows {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       if (CAUSAL && by_term) {
-        add_by_term(t[nb], w[nb], j0 + nb * kBS, valid - nb * kBS);
+        add_by_term(t[nb], pw[nb], j0 + nb * kBS, valid - nb * kBS);
         continue;
       }
       uint32_t pb[NT][PARTS][2];
@@ -337,12 +336,12 @@ struct Rows {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t hi = pack_f16x2(w[nb][nt][2 * h], w[nb][nt][2 * h + 1]);
+          const uint32_t hi = pack_f16x2(pw[nb][nt][2 * h], pw[nb][nt][2 * h + 1]);
           pb[nt][0][h] = transpose_8x8(hi);
           if constexpr (HILO) {
             const float2 f = unpack_f16x2(hi);
             pb[nt][1][h] =
-                transpose_8x8(pack_f16x2(w[nb][nt][2 * h] - f.x, w[nb][nt][2 * h + 1] - f.y));
+                transpose_8x8(pack_f16x2(pw[nb][nt][2 * h] - f.x, pw[nb][nt][2 * h + 1] - f.y));
           }
         }
       const uint32_t s0 = scales_f16x2(vs[nb][0], vs[nb][1]);  // of the tokens' pairs
@@ -376,7 +375,7 @@ struct Rows {
   __device__ __forceinline__ void add_by_term(const uint8_t* t, const float (&w)[NT][4], int j0,
                                               int valid) {
     const int lane = threadIdx.x & 31;
-    const int g = lane >> 2, c = lane & 3;
+    const int c = lane & 3;
     const int codes0 = vc[0] - tok(2 * c) * (HD / 2), groups0 = vgr[0] - tok(2 * c) * KK;
 #pragma unroll 1
     for (int ti = 0; ti < kBS; ++ti) {

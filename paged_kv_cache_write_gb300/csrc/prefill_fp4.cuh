@@ -15,10 +15,110 @@ namespace pkv {
 namespace fp4 {
 
 using attn::PrefillParams;
+using attn::Ring;
+using attn::kBarrierBytes;
+using fp8::RingPos;
+using fp8::gave_up;
+using fp8::release_tile;
 
 constexpr int kPrefillWarps = 8;
 constexpr int kPrefillTiles = 2;  // row tiles of 8 per warp
 constexpr int kPrefillRows = 8 * kPrefillTiles;
+
+// Producer, one lane (elect_one): fetches blocks into the ring one after the other.
+template <int HD>
+struct Producer {
+  const Ring& ring;
+  const Pools& pools;
+  int num_blocks, n_kv, head;
+  int32_t* err;
+  RingPos pos;
+  uint32_t issued = 0;
+
+  // The head's part of block `id`; a bad one reads zeros.  False on timeout.
+  __device__ __forceinline__ bool fetch(int id) {
+    if (pos.round > 0 && !wait_or_abort(ring.empty + pos.st, (pos.round - 1) & 1, ring.abort_flag)) {
+      report(err, PKV_DEVERR_TIMEOUT);
+      return false;
+    }
+    uint8_t* t = ring.k_tile(pos.st);
+    uint64_t* full = ring.full + pos.st;
+    using TileT = Tile<HD>;
+    if (id >= 0 && id < num_blocks) {
+      mbar_arrive_expect_tx(full, TileT::kBytes);
+      const int64_t at = int64_t(id) * n_kv + head;
+      // (the chunk's other tiles read the blocks again: no eviction hint)
+      bulk_copy_g2s(t, pools.k + at * TileT::kCodes, TileT::kCodes, full);
+      bulk_copy_g2s(t + TileT::kVCodes, pools.v + at * TileT::kCodes, TileT::kCodes, full);
+      bulk_copy_g2s(t + TileT::kKGroups, pools.kg + at * TileT::kGroups, TileT::kGroups, full);
+      bulk_copy_g2s(t + TileT::kVGroups, pools.vg + at * TileT::kGroups, TileT::kGroups, full);
+    } else {
+      report(err, PKV_DEVERR_BLOCK_ID);
+      // scales of zero: whatever codes the stage holds are then zeros
+      for (int i = 0; i < 2 * TileT::kGroups; i += 16)
+        *reinterpret_cast<uint4*>(t + TileT::kKGroups + i) = make_uint4(0u, 0u, 0u, 0u);
+      fence_proxy_async_smem();  // before the copies that come there next
+      mbar_arrive(full);
+    }
+    pos.next(ring);
+    ++issued;
+    return true;
+  }
+
+  // Blocks row[0 .. n), ids read a group ahead.  False: gave up (and told the consumers).
+  __device__ __forceinline__ bool fetch_row(const int32_t* row, int n) {
+    constexpr int kAhead = 8;
+    int id[kAhead], next[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) next[i] = i < n ? row[i] : 0;
+    for (int k0 = 0; k0 < n; k0 += kAhead) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) id[i] = next[i];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) next[i] = k0 + kAhead + i < n ? row[k0 + kAhead + i] : 0;
+      if (*ring.abort_flag) return false;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (k0 + i >= n) break;
+        if (!fetch(id[i])) {
+          *ring.abort_flag = 1;
+          return false;
+        }
+      }
+    }
+    return true;
+  }
+
+  // At the end: until the consumers have left the last tile, and all have landed; where
+  // some thread gave up, a bounded wait for the copies still in flight, so that none
+  // lands after the CTA has left.
+  __device__ __forceinline__ void finish() const {
+    if (issued == 0) return;
+    const uint32_t last = issued - 1, st = last % ring.nstages;
+    const bool left = wait_or_abort(ring.empty + st, (last / ring.nstages) & 1, ring.abort_flag);
+    if (!left || *ring.abort_flag) attn::ring_drain(ring, issued);
+  }
+};
+
+// Consumer warp: its next NB tiles of the ring.  After a wait that gave up the warp goes
+// on over what is there (its work is all its lanes'); gave_up tells before anything is
+// stored.
+template <int NB, typename RowsT>
+__device__ __forceinline__ void take_tiles(RowsT& rows, const Ring& ring, RingPos& pos, int j0,
+                                           int valid, bool use, int32_t* err) {
+  const uint8_t* t[NB];
+  RingPos at[NB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    at[i] = pos;
+    t[i] = ring.k_tile(pos.st);
+    wait_or_flag(ring.full + pos.st, pos.round & 1, ring.abort_flag, err);
+    pos.next(ring);
+  }
+  if (use) rows.template blocks<NB, true>(t, j0, valid);
+#pragma unroll
+  for (int i = 0; i < NB; ++i) release_tile(ring, at[i]);
+}
 
 // CTAS: that an SM's registers hold.
 template <typename T, int HD, int CTAS>
@@ -44,21 +144,21 @@ __global__ void __launch_bounds__((kPrefillWarps + 1) * 32, CTAS)
   const int i_end = min(c, i0 + tile_q);
   const int n_blocks = (L - c + i_end - 1) / kBS + 1;  // up to the last key any row sees
 
-  Ring ring = make_ring(smem, p.nstages, Tile::bytes(1, HD));
+  Ring ring = attn::make_tile_ring(smem, p.nstages, Tile<HD>::kBytes / 2);
   attn::ring_init(ring, kPrefillWarps);
   const int warp = threadIdx.x >> 5;
   const int32_t* row = p.bt + int64_t(b) * p.W;
 
   if (warp == kPrefillWarps) {
-    if (elect_one()) {  // (the chunk's other tiles read the blocks again: no eviction hint)
-      Producer<HD> pr{ring, pools, p.num_blocks, p.n_kv, 1, p.err, 0};
-      pr.fetch_row(row, n_blocks, g);
+    if (elect_one()) {
+      Producer<HD> pr{ring, pools, p.num_blocks, p.n_kv, g, p.err};
+      pr.fetch_row(row, n_blocks);
       pr.finish();
     }
   } else {
     using RowsT = Rows<T, HD, kPrefillTiles, true>;
     RowsT rows;
-    rows.place(1, 0);
+    rows.place();
     const T* q = static_cast<const T*>(p.q);
     const int qw = i0 + warp * p.queries_per_warp;  // first query of this warp
     const int nrows = p.queries_per_warp * p.rep;
@@ -117,7 +217,7 @@ cudaError_t prefill_run(const AttnArgs& a, const Fp4Cache& cache, cudaStream_t s
   p.scale_log2 = a.scale * attn::kLog2e;
   p.queries_per_warp = kPrefillRows / p.rep;
   p.nstages = 12;
-  const size_t smem = kBarrierBytes + 1024 + size_t(p.nstages) * Tile::bytes(1, HD);
+  const size_t smem = kBarrierBytes + 1024 + size_t(p.nstages) * Tile<HD>::kBytes;
   const int tile_q = kPrefillWarps * p.queries_per_warp;
   const int64_t tiles = (int64_t(a.max_q_len) + tile_q - 1) / tile_q;
   if (tiles == 0 || a.num_seqs == 0) return cudaSuccess;

@@ -106,7 +106,7 @@ class Batch:
         return tuple(paged_fp4.values(p[blocks], g[blocks], s).reshape(-1, self.n_kv, self.hd)[:n]
                      for p, g, s in ((self.kp, self.kg, self.ks), (self.vp, self.vg, self.vs)))
 
-    def reference(self, q, b, last, held=15):
+    def reference(self, q, b, last, held=4):
         """(output, tolerance) [H, hd] in float64 of one query over keys 0..last.
 
         Tolerance, to first order.  The output is g sum(w v) / sum(w).  Scores are
@@ -147,9 +147,9 @@ class Batch:
                       + 2.0 ** -(25 + held) * p.max() * np.abs(v).sum(axis=0) + 1e-30)
         return out, tol
 
-    def check(self, got, q, which, last, held=15):
+    def check(self, got, q, which, last, held=4):
         """got, q [rows, H, hd]; row i is sequence which[i]'s, over keys 0..last[i].
-        held: 15, or 4 for the tcgen05 prefill, whose largest weight may be held at 2^4."""
+        held: log2 of what a row's largest weight is held at or above."""
         got, q = f64(got), f64(q)
         worst = 0.0
         for i, (b, n) in enumerate(zip(which, last)):

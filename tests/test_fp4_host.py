@@ -190,6 +190,7 @@ def test_norm_rope_write_fp4_refusals(pkv, kw, status):
     (dict(), OK), (dict(no_pool=True), NULL), (dict(pool_dtype=1), DTYPE), (dict(type=2), DTYPE),
     (dict(T=-1), SHAPE), (dict(n_kv=0), SHAPE), (dict(head_dim=24), UNSUPPORTED),
     (dict(head_dim=272), UNSUPPORTED), (dict(n_kv=65536), RANGE), (dict(num_blocks=1 << 30), RANGE),
+    (dict(num_blocks=1 << 26, n_kv=32), RANGE),
     (dict(T=3, k=None), NULL), (dict(T=3, v=None), NULL), (dict(T=3, slots=None), NULL),
     (dict(T=3, kp=None), NULL), (dict(T=3, vp=None), NULL), (dict(T=3, kg=None), NULL),
     (dict(T=3, vg=None), NULL), (dict(T=3, k1=None), NULL), (dict(T=3, v1=None), NULL),
@@ -262,7 +263,8 @@ COMMON = [
 
 
 @pytest.mark.parametrize("kw,status", COMMON + [
-    (dict(ctas=-1), RANGE), (dict(ws=None), WORKSPACE), (dict(), WORKSPACE),
+    (dict(ctas=-1), RANGE), (dict(B=1 << 20, n_kv=64, H=64, most=16 * 64, W=64), RANGE),
+    (dict(B=1 << 30, n_kv=8), RANGE), (dict(ws=None), WORKSPACE), (dict(), WORKSPACE),
     (dict(ws=FAKE + 8, ws_bytes=1 << 50), ALIGN), (dict(B=0, q=None, ws=None), OK)])
 def test_decode_refusals(pkv, kw, status):
     assert Attention(pkv).decode(**kw) == status

@@ -251,6 +251,24 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<T, HD, NT>)
     }
     commit_copies();  // (an empty group past the last block: waits count groups)
   };
+  // NB of them, of which most calls find all inside the segment and its 32 ids
+  auto feed_some = [&](auto nb) {
+    constexpr int NB = decltype(nb)::value;
+    if (NB > 1 && (k & 31) != 0 && (k & 31) + NB <= 32 && k + NB < seg) {
+      const int head = ahead.grp * p.hg_size + warp;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        fetch.block(ring_at + fill, __shfl_sync(0xffffffffu, ids, (k & 31) + i), head);
+        fill = fill == (S - 1) * Tile<HD>::kBytes ? 0 : fill + Tile<HD>::kBytes;
+        commit_copies();
+      }
+      left -= NB;
+      k += NB;
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < NB; ++i) feed();
+    }
+  };
 #pragma unroll 1
   for (int i = 0; i < S; ++i) feed();
   // (while the first blocks come)
@@ -276,8 +294,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<T, HD, NT>)
     wait_copies<S - NB>();
     rows.template blocks<NB, decltype(edge)::value>(t, j0, cur.L - j0);
     __syncwarp();
-#pragma unroll
-    for (int i = 0; i < NB; ++i) feed();
+    feed_some(nb);
   };
   const T* q = static_cast<const T*>(p.q);
   T* out = static_cast<T*>(p.out);
@@ -291,8 +308,12 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<T, HD, NT>)
                pools.v_scale[kv_head]);
     const int full = min(n, cur.L / kBS - cur.j);  // blocks without an edge
     int i = 0;
-    for (; i + RowsT::PAIR <= full; i += RowsT::PAIR)
-      take(std::integral_constant<int, RowsT::PAIR>{}, std::false_type{}, (cur.j + i) * kBS);
+    for (; i + RowsT::TAKE <= full; i += RowsT::TAKE)
+      take(std::integral_constant<int, RowsT::TAKE>{}, std::false_type{}, (cur.j + i) * kBS);
+    if (RowsT::TAKE > 2 && i + 2 <= full) {
+      take(std::integral_constant<int, 2>{}, std::false_type{}, (cur.j + i) * kBS);
+      i += 2;
+    }
     for (; i < n; ++i) take(std::integral_constant<int, 1>{}, std::true_type{}, (cur.j + i) * kBS);
     if (cur.j == 0 && n == cur.nblk) {
       rows.store([&](int r) -> T* { return r < p.rep ? out + (row0 + r) * HD : nullptr; });
@@ -410,7 +431,7 @@ template <typename T, int HD, int NT>
 struct DecodeFp4 {
   static constexpr int kCtas = kCtasPerSm<T, HD, NT>;
   static constexpr int kDepth = kStages<T, HD, NT>;
-  static_assert(kDepth >= 3, "a pair of blocks at hand and one on its way");
+  static_assert(kDepth > Rows<T, HD, NT, false>::TAKE, "blocks at hand and on their way");
   static size_t ring_bytes(int warps, int nstages) {
     return (size_t(warps) * nstages * Tile<HD>::kBytes + 127) / 128 * 128;
   }

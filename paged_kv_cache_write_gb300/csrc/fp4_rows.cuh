@@ -83,8 +83,9 @@ struct Rows {
   static constexpr int KW = KD >= 8 ? KD / 8 : 1;       // words of them
   static constexpr int DB = HD / 8;                     // dims of V^T that a lane holds
   static constexpr int VW = DB >= 8 ? DB / 8 : 1;       // words of them
-  // blocks taken together, as the registers allow
+  // blocks taken together, as the registers allow; a decode's, where there are many
   static constexpr int PAIR = HD * NT * PARTS <= 128 ? 2 : 1;
+  static constexpr int TAKE = HD * NT * PARTS <= 64 ? 4 : PAIR;
 
   uint32_t qb[NT][PARTS][KK][2];
   float o[NT][KK][4];

@@ -130,22 +130,78 @@ struct Fetcher {
   }
 };
 
+// The CTA whose range holds unit u of U, of G CTAs: the largest c with floor(c U / G) <= u.
+__device__ __forceinline__ int owner_of(int u, int U, int G) {
+  return static_cast<int>((uint64_t(uint32_t(u) + 1u) * uint32_t(G) - 1u) / uint32_t(U));
+}
+
 // The split entry of CTA c (of G, over U units) whose range starts at block j of a group
 // of nblk blocks: attn::split_entry, its owners by division.
 __device__ __forceinline__ int4 split_entry(int c, int G, int U, int b, int grp, int j, int nblk) {
   if (j == 0) return make_int4(-1, 0, 0, 0);
-  // the CTA whose range holds unit u: the largest c with floor(c U / G) <= u
-  auto owner = [&](int u) {
-    return static_cast<int>((uint64_t(uint32_t(u) + 1u) * uint32_t(G) - 1u) / uint32_t(U));
-  };
   const int first = attn::range_begin(c, U, G) - j;  // the group's first unit
-  const int c0 = owner(first);
+  const int c0 = owner_of(first, U, G);
   // (the second of its CTAs joins them)
-  if (owner(attn::range_begin(c0 + 1, U, G)) != c) return make_int4(-1, 0, 0, 0);
+  if (owner_of(attn::range_begin(c0 + 1, U, G), U, G) != c) return make_int4(-1, 0, 0, 0);
   const int flags = (attn::range_begin(c0, U, G) != first ? attn::kSplitC0Tail : 0) |
                     (U >= G ? attn::kSplitDense : 0);
-  return make_int4(b, grp | flags, c0 | (owner(first + nblk - 1) << 16), first);
+  return make_int4(b, grp | flags, c0 | (owner_of(first + nblk - 1, U, G) << 16), first);
 }
+
+// Units before each sequence, by a converged warp: for batches of at most 32 kLaneSeqs
+// sequences a scan in registers, without a barrier.
+constexpr int kLaneSeqs = 8;
+
+struct WarpScan {
+  int n[kLaneSeqs];  // units of sequences first .. first + per - 1
+  int first, per, before, total;
+
+  __device__ __forceinline__ explicit WarpScan(const DecodeParams& p) {
+    const int lane = threadIdx.x & 31;
+    per = (p.B + 31) / 32;
+    first = lane * per;
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < kLaneSeqs; ++i) {
+      n[i] = 0;
+      if (i < per && first + i < p.B) n[i] = p.n_groups * ((length_of(p, first + i) + kBS - 1) / kBS);
+    }
+#pragma unroll
+    for (int i = 0; i < kLaneSeqs; ++i) sum += n[i];
+    before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += y;
+    }
+    total = __shfl_sync(0xffffffffu, before, 31);
+    before -= sum;
+  }
+  // The sequence that holds unit u < total: its number, its first unit and its units.
+  __device__ __forceinline__ int3 find(int u) const {
+    int3 r = make_int3(-1, 0, 0);
+    int at = before;
+#pragma unroll
+    for (int i = 0; i < kLaneSeqs; ++i) {
+      if (u >= at && u < at + n[i]) r = make_int3(first + i, at, n[i]);
+      at += n[i];
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, r.x >= 0)) - 1;
+    return make_int3(__shfl_sync(0xffffffffu, r.x, src), __shfl_sync(0xffffffffu, r.y, src),
+                     __shfl_sync(0xffffffffu, r.z, src));
+  }
+  // Sequence b's first unit and units.
+  __device__ __forceinline__ int2 of(int b) const {
+    const int src = b / per, k = b - src * per;
+    int at = before, units = 0;
+#pragma unroll
+    for (int i = 0; i < kLaneSeqs; ++i) {
+      if (i < k) at += n[i];
+      if (i == k) units = n[i];
+    }
+    return make_int2(__shfl_sync(0xffffffffu, at, src), __shfl_sync(0xffffffffu, units, src));
+  }
+};
 
 // CTAs of eight warps that an SM's registers hold (or as many more narrower ones).
 template <typename T, int HD, int NT>
@@ -172,7 +228,27 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<T, HD, NT>)
   int4 st = make_int4(0, 0, 0, 0);
   int* lens_s = reinterpret_cast<int*>(smem + p.part_off);  // [kKeptLens]
   const bool kept = p.plan_in_kernel && p.part_off != 0 && p.B <= kKeptLens;
-  if (p.plan_in_kernel) {
+  if (p.B <= 32 * kLaneSeqs) {
+    const WarpScan scan(p);
+    U = scan.total;
+    const int r0 = attn::range_begin(me, U, G);
+    if (r0 < attn::range_begin(me + 1, U, G)) {
+      const int3 seq = scan.find(r0);
+      const int nblk = seq.z / p.n_groups;
+      const int grp = (r0 - seq.y) / nblk;
+      st = make_int4(seq.x, grp, (r0 - seq.y) - grp * nblk, 0);
+    }
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+      if (kept) lens_s[b] = length_of(p, b);
+      if (blockIdx.x == 0) report_bad_length(p, b);
+    }
+    attn::zero_empty<T, HD>(p, blockIdx.x, G, [&](int b) { return length_of(p, b) == 0; });
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      p.total_units[0] = U;
+      p.total_units[1] = -1;  // a call planning for itself replaces any kept plan
+    }
+    if (kept) __syncthreads();
+  } else if (p.plan_in_kernel) {
     // scan the units per sequence in the (still unused) stages
     int* cu_s = reinterpret_cast<int*>(smem);  // [B + 1]
     int* warp_tot = cu_s + p.B + 1;            // [32]
@@ -328,6 +404,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<T, HD, NT>)
   }
 }
 
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
 // Batches too small to stream: one cluster of C CTAs per (sequence, head group), a warp
 // per head of the group, each CTA a contiguous part of the sequence's at most
 // kMaxBlocks * C blocks, the parts combined through distributed shared memory (no
@@ -384,45 +465,138 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       ++i;
     }
   }
+  T* out = static_cast<T*>(p.out) + (int64_t(b) * p.n_heads + int64_t(grp) * rows_per_group) * HD;
+  if (C == 1) {
+    rows.store([&](int r) -> T* { return r < p.rep ? out + (warp * p.rep + r) * HD : nullptr; });
+    return;
+  }
   // this CTA's part
   rows.store_partial(
       [&](int r) -> float* { return r < p.rep ? part_o + (warp * p.rep + r) * HD : nullptr; },
       [&](int r) -> float* { return part_ml + (warp * p.rep + r) * 2; });
 
   cluster_sync();  // every CTA's partial is in its shared memory
-  // CTA `rank` combines elements [rank E / C, (rank + 1) E / C) of the group
-  const int E = rows_per_group * HD;
+  // CTA `rank` combines float4s [rank E / C, (rank + 1) E / C) of the group's E
+  const int E = rows_per_group * HD / 4;
   const int e0 = rank * E / C, e1 = (rank + 1) * E / C;
-  T* out = static_cast<T*>(p.out) + (int64_t(b) * p.n_heads + int64_t(grp) * rows_per_group) * HD;
   for (int e = e0 + static_cast<int>(threadIdx.x); e < e1; e += static_cast<int>(blockDim.x)) {
-    const int r = e / HD;
+    const int r = e / (HD / 4);
     float2 ml[kMaxCluster];
-    float oc[kMaxCluster];
+    float4 oc[kMaxCluster];
 #pragma unroll
     for (int c = 0; c < kMaxCluster; ++c) {  // every peer's values in one round trip
       ml[c] = make_float2(0.f, 0.f);
-      oc[c] = 0.f;
+      oc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (c < C) {
         ml[c] = ld_cluster_f32x2(cluster_map(part_ml + r * 2, c));
-        oc[c] = ld_cluster_f32(cluster_map(part_o + e, c));
+        oc[c] = ld_cluster_f32x4(cluster_map(part_o + e * 4, c));
       }
     }
     float M = -INFINITY;
 #pragma unroll
     for (int c = 0; c < kMaxCluster; ++c)
       if (ml[c].y > 0.f) M = fmaxf(M, ml[c].x);  // a part that saw no key has no weight
-    float acc = 0.f, den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float den = 0.f;
 #pragma unroll
     for (int c = 0; c < kMaxCluster; ++c) {
       if (ml[c].y > 0.f) {
         const float w = fast_exp2(ml[c].x - M) * ml[c].y;
         den += w;
-        acc = fmaf(w, oc[c], acc);
+        acc = make_float4(fmaf(w, oc[c].x, acc.x), fmaf(w, oc[c].y, acc.y), fmaf(w, oc[c].z, acc.z),
+                          fmaf(w, oc[c].w, acc.w));
       }
     }
-    out[e] = Elem<T>::from_f(den > 0.f ? acc * (1.f / den) : 0.f);
+    const float inv = den > 0.f ? 1.f / den : 0.f;
+    store4(out + e * 4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
   }
   cluster_sync();  // the peers have read this CTA's partials
+}
+
+// Joins for batches of few groups, which many CTAs share (a single long sequence: all of
+// them): a CTA is 32 float4 of one group's rows, its warps share the parts, eight loads of
+// each on their way, and join their sums through shared memory.  (One thread for all the
+// parts of its element, as joins of two or three parts go, took 55 us of the 62 for one
+// sequence of 8,192 tokens.)
+constexpr int kWideJoin = 8;  // warps
+constexpr int kFewParts = 16;  // CTAs a group, from which on
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kWideJoin * 32) join_few_kernel(const DecodeParams p) {
+  constexpr int NB = 8;  // parts on their way
+  __shared__ float4 sum_s[kWideJoin][32];
+  __shared__ float2 ml_s[kWideJoin][32];
+  attn::pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the lengths were there before the decode began)
+  const int b = blockIdx.x / p.n_groups, grp = blockIdx.x - b * p.n_groups;
+  const WarpScan scan(p);
+  const int2 seq = scan.of(b);
+  const int U = scan.total, G = p.grid;
+  const int nblk = seq.y / p.n_groups;
+  if (nblk == 0) return;
+  const int first = seq.x + grp * nblk;
+  const int c0 = owner_of(first, U, G), c1 = owner_of(first + nblk - 1, U, G);
+  if (c0 == c1) return;  // not split
+  // c0 holds the group's first units at the end of its range, unless its range starts there
+  const bool tail = attn::range_begin(c0, U, G) != first;
+  const int rows = p.hg_size * p.rep;
+  const int E = rows * HD;  // elements of a part
+  const int e = (blockIdx.y * 32 + lane) * 4;
+  attn::pdl_wait();  // the decode's partials
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float M = -INFINITY, den = 0.f;
+  if (e < E) {
+    for (int cs = c0 + warp; cs <= c1; cs += NB * kWideJoin) {
+      float4 o[NB];
+      float2 ml[NB];
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const int c = cs + k * kWideJoin;
+        o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        ml[k] = make_float2(-INFINITY, 0.f);
+        // (with fewer units than CTAs some ranges are empty)
+        if (c <= c1 && (U >= G || attn::range_begin(c + 1, U, G) > attn::range_begin(c, U, G))) {
+          const int64_t slot = 2 * c + (c == c0 && tail ? 1 : 0);
+          o[k] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + slot * E + e));
+          ml[k] = __ldcg(reinterpret_cast<const float2*>(p.ws_ml + (slot * rows + e / HD) * 2));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        if (ml[k].y > 0.f) {  // a part that saw no key has no weight
+          const float Mn = fmaxf(M, ml[k].x);
+          const float a = fast_exp2(M - Mn);
+          const float w = fast_exp2(ml[k].x - Mn) * ml[k].y;
+          acc = make_float4(fmaf(w, o[k].x, acc.x * a), fmaf(w, o[k].y, acc.y * a),
+                            fmaf(w, o[k].z, acc.z * a), fmaf(w, o[k].w, acc.w * a));
+          den = fmaf(den, a, w);
+          M = Mn;
+        }
+      }
+    }
+  }
+  sum_s[warp][lane] = acc;
+  ml_s[warp][lane] = make_float2(M, den);
+  __syncthreads();
+  if (warp != 0 || e >= E) return;
+#pragma unroll
+  for (int w = 1; w < kWideJoin; ++w) {
+    const float2 ml = ml_s[w][lane];
+    const float4 o = sum_s[w][lane];
+    if (ml.y > 0.f) {
+      const float Mn = fmaxf(M, ml.x);
+      const float a = fast_exp2(M - Mn), f = fast_exp2(ml.x - Mn);
+      acc = make_float4(fmaf(f, o.x, acc.x * a), fmaf(f, o.y, acc.y * a), fmaf(f, o.z, acc.z * a),
+                        fmaf(f, o.w, acc.w * a));
+      den = fmaf(den, a, f * ml.y);
+      M = Mn;
+    }
+  }
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const float4 v = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  T* out = static_cast<T*>(p.out) + (int64_t(b) * p.n_heads + int64_t(grp) * rows) * HD + e;
+  store4(out, v);
 }
 
 // --------------------------------------------------------------- host side
@@ -520,8 +694,8 @@ struct DecodeFp4 {
     p.nstages = kDepth;
     p.part_off = kept != 0 ? static_cast<int>(ring_bytes(hg, kDepth)) : 0;  // the kept lengths
     // every CTA scans the lengths in its stages; larger batches have a plan kernel
-    p.plan_in_kernel = a.num_seqs <= kKernelPlanSeqs &&
-                       size_t(a.num_seqs + 1 + 32) * 4 <= size_t(hg) * kDepth * Tile<HD>::kBytes;
+    p.plan_in_kernel = a.num_seqs <= 32 * kLaneSeqs ||
+                       (a.num_seqs <= kKernelPlanSeqs && size_t(a.num_seqs + 1 + 32) * 4 <= size_t(hg) * kDepth * Tile<HD>::kBytes);
     if (!p.plan_in_kernel) {
       attn::decode_plan_kernel<T, HD><<<1, 1024, 0, stream>>>(p);
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -532,10 +706,16 @@ struct DecodeFp4 {
     e = cudaLaunchKernelEx(&cfg, decode_kernel<T, HD, NT>, p, pools);
     if (e != cudaSuccess) return e;
     const int vecs = hg * p.rep * HD / 4;  // of a group's rows
+    cfg.dynamicSmemBytes = 0;
+    if (p.B <= 32 * kLaneSeqs && int64_t(p.B) * p.n_groups * kFewParts <= G) {
+      cfg.gridDim = dim3(p.B * p.n_groups, (vecs + 31) / 32);
+      cfg.blockDim = dim3(kWideJoin * 32);
+      e = cudaLaunchKernelEx(&cfg, join_few_kernel<T, HD>, p);
+      return e != cudaSuccess ? e : cudaGetLastError();
+    }
     const int threads = std::min(fp8::kJoinThreads, (vecs + 31) / 32 * 32);
     cfg.gridDim = dim3(G, (vecs + threads - 1) / threads);
     cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, fp8::join_kernel<T, HD>, p);
     return e != cudaSuccess ? e : cudaGetLastError();
   }

@@ -142,18 +142,31 @@ __device__ __forceinline__ uint32_t codes_under(const float2* x, float amax, uin
   return pack_codes(y);
 }
 
-__device__ __forceinline__ float amax8(const float2* x) {
-  uint32_t a = 0u;
+// The largest magnitude of eight fp32 values, or of eight bf16 values in four words; NaN if
+// one is (its bits are the larger).
+__device__ __forceinline__ float amax8(float4 a, float4 b) {
+  const uint32_t u[8] = {__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(a.z),
+                         __float_as_uint(a.w), __float_as_uint(b.x), __float_as_uint(b.y),
+                         __float_as_uint(b.z), __float_as_uint(b.w)};
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, u[i] & 0x7fffffffu);
+  return __uint_as_float(m);
+}
+__device__ __forceinline__ float amax8(uint4 w) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  __nv_bfloat162 m = __float2bfloat162_rn(0.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    a = max(a, max(__float_as_uint(x[i].x) & 0x7fffffffu, __float_as_uint(x[i].y) & 0x7fffffffu));
-  return __uint_as_float(a);
+    m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&u[i])));
+  return max_mag(__low2float(m), __high2float(m));
 }
 
 // One group of 16 values.
+// (amax_a, amax_b: the largest magnitudes of its halves)
 template <bool EXACT>
-__device__ __forceinline__ Codes quantise(const float2 (&x)[8], float g) {
-  const float a = max_mag(amax8(x), amax8(x + 4)) * pow2_inverse(g);
+__device__ __forceinline__ Codes quantise(const float2 (&x)[8], float amax_a, float amax_b, float g) {
+  const float a = max_mag(amax_a, amax_b) * pow2_inverse(g);
   Codes r;
   r.scale_a = r.scale_b = scale_code(a);
   r.a = codes_under<EXACT>(x, a, r.scale_a, g);
@@ -161,11 +174,11 @@ __device__ __forceinline__ Codes quantise(const float2 (&x)[8], float g) {
   return r;
 }
 
-// Halves of two groups; other(j, amax of x[0..7], of x[8..15]) is the largest magnitude
+// Halves of two groups, whose largest magnitudes are ma and mb; other(j, ma, mb) is the largest magnitude
 // in the other half of half j's group (both by every lane of the warp).
 template <bool EXACT, typename Other>
-__device__ __forceinline__ Codes quantise_apart(const float2 (&x)[8], float g, Other other) {
-  const float ma = amax8(x), mb = amax8(x + 4);
+__device__ __forceinline__ Codes quantise_apart(const float2 (&x)[8], float ma, float mb, float g,
+                                                Other other) {
   const float oa = other(0, ma, mb), ob = other(1, ma, mb);
   const float a = max_mag(ma, oa) * pow2_inverse(g), b = max_mag(mb, ob) * pow2_inverse(g);
   Codes r;

@@ -5,8 +5,11 @@
 // elements as fill one 16-byte store, so that a warp's stores are contiguous.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "device.cuh"
 #include "fp4.cuh"
+#include "host_cache.h"
 #include "launch.h"
 #include "ragged.cuh"
 
@@ -16,8 +19,8 @@ namespace {
 
 constexpr int kThreads = kWindowThreads;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRows = 4;   // rows a warp reads at once
-constexpr int kSteps = 2;  // and steps of 32 items in each
+constexpr int kRows = 2;   // rows a warp reads at once
+constexpr int kSteps = 2;  // and steps of 32 items in each (four rows: 39 us for 36.6, below)
 
 struct GatherParams {
   const uint8_t *k_pool, *v_pool, *k_groups, *v_groups;
@@ -104,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) kv_gather_fp4_kernel(const GatherPar
   const int shift = 31 - __clz(iph);
   const int64_t head_step = int64_t(p.bs) * p.hd;  // elements from a block's head to its next
   // rows 0 .. n - 1 are K's, n .. 2 n - 1 V's
-  for (int r0 = warp * kRows; r0 < 2 * n; r0 += kWarps * kRows) {
+  for (int r0 = (blockIdx.y * kWarps + warp) * kRows; r0 < 2 * n; r0 += gridDim.y * kWarps * kRows) {
     const uint8_t *src[kRows], *grp[kRows];
     const float* scale[kRows];
     uint8_t* dst[kRows];
@@ -179,10 +182,14 @@ cudaError_t launch_kv_gather_fp4(const Fp4Cache& c, const PoolShape& pool, const
   p.num_blocks = pool.num_blocks;
   p.n_kv = pool.n_kv;
   p.hd = pool.head_dim;
-  const unsigned grid = static_cast<unsigned>((int64_t(total_tokens) + kWindow - 1) / kWindow);
+  // (few windows: each over several CTAs, so that a warp has one step)
+  const int64_t windows = (int64_t(total_tokens) + kWindow - 1) / kWindow;
+  const int64_t most = 2 * kWindow / (kWarps * kRows);
+  const dim3 grid(static_cast<unsigned>(windows),
+                  static_cast<unsigned>(std::max<int64_t>(1, std::min(most, sm_count() / windows))));
   return launch_pdl(dtype == PKV_F32 ? kv_gather_fp4_kernel<float>
                                      : kv_gather_fp4_kernel<__nv_bfloat16>,
-                    dim3(grid), kThreads, 0, stream, p);
+                    grid, kThreads, 0, stream, p);
 }
 
 }  // namespace pkv

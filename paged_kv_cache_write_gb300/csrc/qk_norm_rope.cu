@@ -59,6 +59,7 @@ struct Vec16<__nv_bfloat16> {
     *reinterpret_cast<uint4*>(p) = w[j];
   }
   __device__ __forceinline__ void zero() { w[0] = w[1] = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ float amax8(int j) const { return fp4::amax8(w[j]); }
   __device__ __forceinline__ void get(float2 (&x)[8]) const {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -88,6 +89,7 @@ struct Vec16<float> {
     reinterpret_cast<float4*>(p)[0] = w[2 * j];
     reinterpret_cast<float4*>(p)[1] = w[2 * j + 1];
   }
+  __device__ __forceinline__ float amax8(int j) const { return fp4::amax8(w[2 * j], w[2 * j + 1]); }
   __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<TURN>)
           fp4::Codes codes;
           if constexpr (TURN == kHalves) {
             // the other eight elements of each vector's group lie in other lanes
-            codes = fp4::quantise_apart<sizeof(T) == 4>(x, g, [&](int j, float amax_a, float amax_b) {
+            codes = fp4::quantise_apart<sizeof(T) == 4>(x, v.amax8(0), v.amax8(1), g, [&](int j, float amax_a, float amax_b) {
               const int other = ((j == 0 ? da : db) / 8) ^ 1;  // vector of the row
               const int turned = half / 8;                     // that lanes hold first
               const bool second = other < 2 * turned ? other >= turned : (other & 1);
@@ -304,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<TURN>)
               return second ? fb : fa;
             });
           } else {
-            codes = fp4::quantise<sizeof(T) == 4>(x, g);
+            codes = fp4::quantise<sizeof(T) == 4>(x, v.amax8(0), v.amax8(1), g);
           }
           const uint32_t at = static_cast<uint32_t>(slot);  // (slots are below 2^31)
           const uint32_t blk = p.bs_shift >= 0 ? at >> p.bs_shift : at / a.block_size;

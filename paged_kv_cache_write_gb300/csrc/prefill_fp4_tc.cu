@@ -35,6 +35,10 @@
 //               each warp's next blocks on their way, codes -> f16 in registers,
 //               128-byte-swizzled tiles in four-stage rings.
 //
+// Two row tiles a CTA, because they share the conversion of K and V, and one CTA an SM:
+// CTAs of one row tile, two on an SM, hide each other's start and end but take 28% longer
+// for 8 chunks of 1,024 of 32 heads on 8 of 64, 10% for 30 prompts of 33 - 612 tokens.
+//
 // 16 warps leave 128 registers a thread, and no loop may spill: with 200 KB of shared
 // memory little L1 is left, and a reload from local memory costs an L2 round trip.
 //
@@ -65,16 +69,17 @@ constexpr int kTileKeys = 64;
 constexpr int kBlk = 16;
 constexpr int kBlocks = kTileKeys / kBlk;  // blocks per key tile
 static_assert(kBlocks == 4, "units and score chunks below");
+constexpr int kTiles = 2;    // row tiles of a CTA
 constexpr int kMmaWarp = 8;  // and 9, after eight of the softmax
 constexpr int kLoadWarp0 = 10;
 constexpr int kLoadWarps = 6;
 constexpr int kAhead = 3;  // blocks in flight per load warp
 constexpr int kThreads = 16 * 32;
+constexpr uint32_t kTmemCols = 512;
 constexpr int kStages = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kWeightLog2 = 4.f;     // log2 of the reference's weight
 constexpr float kWeightMax = 65504.f;  // f16's largest
-constexpr uint32_t kTmemCols = 512;
 
 struct TcParams {
   const __nv_bfloat16* q;
@@ -98,7 +103,7 @@ struct Layout {
   static constexpr int KV_HALF = kTileKeys * 128;  // 8 KB
   static constexpr int Q_TILE = NH * Q_HALF;
   static constexpr int KV_TILE = NH * KV_HALF;
-  static constexpr int K_OFF = 2 * Q_TILE;  // after Q_A, Q_B
+  static constexpr int K_OFF = kTiles * Q_TILE;  // after Q_A, Q_B
   static constexpr int V_OFF = K_OFF + kStages * KV_TILE;
   static constexpr int NG = HD / 16;                    // groups of a row
   static constexpr int NAN_OFF = V_OFF + kStages * KV_TILE;  // [NG] + flag
@@ -135,89 +140,15 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 }
 
 template <int HD>
-__global__ void __launch_bounds__(kThreads, 1)
-    prefill_fp4_tc_kernel(const TcParams p) {
+__global__ void __launch_bounds__(kThreads, 1) prefill_fp4_tc_kernel(const TcParams p) {
   using Lay = Layout<HD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
 
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the preceding kernel's results
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // Work order, as in the bf16 prefill: with at most blockDim.x sequences, x
-  // numbers the (sequence, KV head, tile pair) triples, sequences by
-  // descending work and each one's pairs from the last (most keys) down;
-  // otherwise z, y, x in the natural order.  Work values are staged in the
-  // (still unused) V stages.
-  __shared__ int order_s, pair_s, head_s, seq_s[3], job_s[4];  // seq_s: cu_q of both ends, length
-  int g = blockIdx.y;
-  int b = blockIdx.z, pair = blockIdx.x;
-  if (p.ordered) {
-    const int t = threadIdx.x;
-    int64_t* work_s = reinterpret_cast<int64_t*>(smem + Lay::V_OFF);
-    int* pairs_s = reinterpret_cast<int*>(work_s + p.B);
-    const int qpp = 2 * p.q_per_tile;
-    int64_t wt = 0;
-    int pt = 0, at = 0, end = 0, len = 0;
-    if (t < p.B) {
-      at = p.cu_q[t];
-      end = p.cu_q[t + 1];
-      len = p.seq_lens[t];
-      if (blockIdx.x == 0) report_bad_chunk(p.err, p.limits, at, end, len, t == p.last_seq);
-      const int64_t cs = int64_t(end) - at;
-      const int64_t Ls = min(len, p.max_len);
-      wt = cs * (2 * Ls - cs + 1);
-      pt = cs > 0 ? static_cast<int>((cs + qpp - 1) / qpp) : 0;
-      work_s[t] = wt;
-      pairs_s[t] = pt;
-    }
-    if (t == 0) order_s = -1;
-    __syncthreads();
-    if (t < p.B) {  // the sequence's first slot: the (head, pair) slots of the heavier ones
-      int64_t first = 0;
-#pragma unroll 8
-      for (int s = 0; s < p.B; ++s) {
-        const int64_t ws = work_s[s];
-        if (ws > wt || (ws == wt && s < t)) first += pairs_s[s];
-      }
-      const int64_t x = blockIdx.x;
-      const int64_t lo = first * p.n_kv, n = int64_t(pt) * p.n_kv;
-      if (x >= lo && x < lo + n) {
-        const int off = static_cast<int>(x - lo);
-        order_s = t;
-        seq_s[0] = at;
-        seq_s[1] = end;
-        seq_s[2] = len;
-        head_s = off / pt;
-        pair_s = pt - 1 - (off - (off / pt) * pt);
-      }
-    }
-    __syncthreads();
-    if (order_s < 0) return;  // slot past the last pair
-    b = order_s;
-    g = head_s;
-    pair = pair_s;
-  } else {
-    if (threadIdx.x == 0) {
-      seq_s[0] = p.cu_q[b];
-      seq_s[1] = p.cu_q[b + 1];
-      seq_s[2] = p.seq_lens[b];
-      if (pair == 0 && g == 0)
-        report_bad_chunk(p.err, p.limits, seq_s[0], seq_s[1], seq_s[2], b == p.last_seq);
-    }
-    __syncthreads();
-  }
-  const int q0 = seq_s[0];
-  // idle CTAs leave before any barrier or TMEM use
-  if (q0 < 0 || seq_s[1] <= q0 || seq_s[1] > p.total_q) return;  // no chunk, or not within the rows
-  const int c = seq_s[1] - q0;
-  const int i0 = pair * 2 * p.q_per_tile;  // first query of tile A
-  if (i0 >= c) return;
-  const int L = min(seq_s[2], p.max_len);
-  if (L < c) return;
-  const int i_end = min(c, i0 + 2 * p.q_per_tile);
-  const int n_tiles = (L - c + i_end - 1) / kTileKeys + 1;
-  const int n_blocks_seq = (L + kBlk - 1) / kBlk;
-
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::BAR_OFF);
   uint64_t* q_full = bars + 0;         // [2] per row tile
   uint64_t* k_full = bars + 2;         // [4] per stage
@@ -233,8 +164,125 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* nan_s = reinterpret_cast<int*>(smem + Lay::NAN_OFF);  // [NG] first NaN position
   int* nan_any = nan_s + Lay::NG;
 
-  const int warp = threadIdx.x >> 5;
-  const int lane = threadIdx.x & 31;
+  // Work order, as in the bf16 prefill: with at most blockDim.x sequences, x numbers the
+  // (sequence, KV head, group of row tiles) triples, sequences by descending work and
+  // each one's groups from the last (most keys) down; otherwise z, y, x in the natural
+  // order.  Work values are staged in the (still unused) V stages.  What needs no
+  // sequence is set up while their offsets and lengths come.
+  __shared__ int seq_s[3], job_s[5];  // cu_q of both ends, length; the CTA's work, or -1
+  const int qpg = kTiles * p.q_per_tile;  // queries of a group
+  int at = 0, end = 0, len = 0;
+  const int t = threadIdx.x;
+  if (p.ordered && t < p.B) {
+    at = p.cu_q[t];
+    end = p.cu_q[t + 1];
+    len = p.seq_lens[t];
+  } else if (!p.ordered && t == 0) {
+    at = p.cu_q[blockIdx.z];
+    end = p.cu_q[blockIdx.z + 1];
+    len = p.seq_lens[blockIdx.z];
+  }
+  if (t == 32) {
+    for (int i = 0; i < kTiles; ++i) {
+      mbar_init(q_full + i, 4);
+      mbar_init(drain + i, 1);
+    }
+    for (int i = 0; i < 2 * kTiles; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(w_ready + i, 4);
+      mbar_init(o_done + i, 1);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(k_full + i, kBlocks);
+      mbar_init(k_empty + i, kTiles);  // left by the row tiles
+      mbar_init(v_full + i, kBlocks);
+      mbar_init(v_empty + i, kTiles);
+    }
+    *abort_flag = 0;
+    *nan_any = 0;
+    fence_barrier_init();
+  }
+  if (t >= 64 && t < 64 + Lay::NG) nan_s[t - 64] = INT_MAX;
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(tmem_slot, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  if (t == 0) job_s[4] = -1;
+  // the CTA's sequence, KV head and group
+  auto take_job = [&](int b, int g, int group, int at, int end, int len) {
+    seq_s[0] = at;
+    seq_s[1] = end;
+    seq_s[2] = len;
+    job_s[0] = group * qpg;  // first query
+    job_s[1] = end - at;
+    job_s[2] = at;
+    job_s[3] = g;
+    job_s[4] = b;
+  };
+  if (p.ordered) {
+    int64_t* work_s = reinterpret_cast<int64_t*>(smem + Lay::V_OFF);
+    int* groups_s = reinterpret_cast<int*>(work_s + p.B);
+    int* seqs_s = groups_s + p.B;  // [3][B]
+    if (t < p.B) {
+      if (blockIdx.x == 0) report_bad_chunk(p.err, p.limits, at, end, len, t == p.last_seq);
+      const int64_t cs = int64_t(end) - at;
+      const int64_t Ls = min(len, p.max_len);
+      work_s[t] = cs * (2 * Ls - cs + 1);
+      groups_s[t] = cs > 0 ? static_cast<int>((cs + qpg - 1) / qpg) : 0;
+      seqs_s[t] = at;
+      seqs_s[p.B + t] = end;
+      seqs_s[2 * p.B + t] = len;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    // a sequence's first slot: the (head, group) slots of the heavier ones, summed by
+    // several threads for each sequence
+    int share = 1;
+    while (share < 32 && 2 * share * p.B <= kThreads) share *= 2;
+    const int mine = t / share, part = t & (share - 1);
+    int first = 0;  // (slots are counted in 32 bits)
+    if (mine < p.B) {
+      const int64_t wt = work_s[mine];
+#pragma unroll 4
+      for (int i = part; i < p.B; i += share) {
+        const int64_t wi = work_s[i];
+        if (wi > wt || (wi == wt && i < mine)) first += groups_s[i];
+      }
+    }
+    for (int o = 1; o < share; o <<= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
+    if (mine < p.B && part == 0) {
+      const int groups = groups_s[mine];
+      const int64_t x = blockIdx.x;
+      const int64_t lo = int64_t(first) * p.n_kv, n = int64_t(groups) * p.n_kv;
+      if (x >= lo && x < lo + n) {
+        const int off = static_cast<int>(x - lo);
+        take_job(mine, off / groups, groups - 1 - (off - (off / groups) * groups), seqs_s[mine],
+                 seqs_s[p.B + mine], seqs_s[2 * p.B + mine]);
+      }
+    }
+  } else {
+    if (t == 0) {
+      if (blockIdx.x == 0 && blockIdx.y == 0)
+        report_bad_chunk(p.err, p.limits, at, end, len, int(blockIdx.z) == p.last_seq);
+      take_job(blockIdx.z, blockIdx.y, blockIdx.x, at, end, len);
+    }
+    tc::fence_before_sync();
+  }
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const int b = job_s[4], g = job_s[3], i0 = job_s[0], q0 = seq_s[0];
+  const int c = seq_s[1] - q0;
+  const int L = min(seq_s[2], p.max_len);
+  // no slot, no chunk, one not within the rows, or longer than its sequence
+  if (b < 0 || q0 < 0 || seq_s[1] <= q0 || seq_s[1] > p.total_q || i0 < 0 || i0 >= c || L < c) {
+    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kTmemCols);
+    return;
+  }
+  const int i_end = min(c, i0 + qpg);
+  const int n_tiles = (L - c + i_end - 1) / kTileKeys + 1;
+  const int n_blocks_seq = (L + kBlk - 1) / kBlk;
   // every wait is one of these two: bounded, by a whole warp or by one lane
   auto wait_one = [&](uint64_t* bar, uint32_t parity) {
     return wait_or_abort(bar, parity, abort_flag);
@@ -242,43 +290,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
     return warp_wait_or_abort(bar, parity, abort_flag);
   };
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) mbar_init(q_full + i, 4);
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(s_full + i, 1);
-      mbar_init(w_ready + i, 4);
-      mbar_init(o_done + i, 1);
-    }
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(k_full + i, kBlocks);
-      mbar_init(k_empty + i, 2);  // left by both row tiles
-      mbar_init(v_full + i, kBlocks);
-      mbar_init(v_empty + i, 2);
-    }
-    mbar_init(drain, 1);
-    mbar_init(drain + 1, 1);
-    *abort_flag = 0;
-    *nan_any = 0;
-    job_s[0] = i0;
-    job_s[1] = c;
-    job_s[2] = q0;
-    job_s[3] = g;
-    fence_barrier_init();
-  }
-  if (threadIdx.x < Lay::NG) nan_s[threadIdx.x] = INT_MAX;
-  if (warp == kMmaWarp) {
-    tc::tmem_alloc(tmem_slot, kTmemCols);
-    tc::tmem_relinquish();
-  }
-  tc::fence_before_sync();
-  __syncthreads();
-  tc::fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
   auto q_tile = [&](int x) { return smem + x * Lay::Q_TILE; };
   auto k_st = [&](int j) { return smem + Lay::K_OFF + (j % kStages) * Lay::KV_TILE; };
   auto v_st = [&](int j) { return smem + Lay::V_OFF + (j % kStages) * Lay::KV_TILE; };
   auto s_tm = [&](int x, int j) { return tmem + uint32_t(x * 2 + (j & 1)) * kTileKeys; };
-  auto o_tm = [&](int x) { return tmem + 256u + uint32_t(x) * 128u; };
+  auto o_tm = [&](int x) { return tmem + uint32_t(kTiles + x) * 128u; };
 
   if (warp >= kLoadWarp0) {
     // ------------------------------------------------------ K and V tiles
@@ -472,26 +488,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int x = warp >> 2;               // tile A or B
     // (TMEM lane = row of the tile: (warp % 4) * 32 + lane)
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    // A row's 16-byte vectors of q (and of out) are RL = HD / 8 lanes' work: the
-    // warp goes through its rows 32 / RL at a time, so that memory is touched
-    // row by row (with every lane at a row of its own, 32 lines a load, one tile
-    // of 64 tokens took 3 us longer).  Row `m` of the warp: its query,
-    // or -1, and its first element; read from shared memory where it is needed,
-    // so that it takes no registers in between.
+    // A row's 16-byte vectors of q (and of out) are RL = HD / 8 lanes' work: the warp goes
+    // through its rows 32 / RL at a time, so that memory is touched row by row (with every
+    // lane at a row of its own, 32 lines a load, one tile of 64 tokens took 3 us longer).
+    // What says whose row it is is read from shared memory where it is needed, so that it
+    // takes no registers in between.
     constexpr int RL = HD / 8, RG = 32 / RL, STEPS = 32 / RG;
-    struct Row {
-      int qi;
-      int64_t off;
-    };
-    auto row_of = [&](int m) {
-      const int* job = job_s;
-      const int rr = (warp & 3) * 32 + m;
-      const int q = (rr * p.rep_inv) >> 16;  // rr / p.rep
-      const int qi = job[0] + x * p.q_per_tile + q;
-      const bool active = q < p.q_per_tile && qi < job[1];
-      return Row{active ? qi : -1,
-                 (int64_t(job[2] + qi) * p.n_heads + job[3] * p.rep + (rr - q * p.rep)) * HD};
-    };
     // where vector k of row m of the warp lies in the Q tile
     auto q_at = [&](int m, int k) {
       const int rr = (warp & 3) * 32 + m;
@@ -501,41 +503,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     float rs = 1.f;  // undoes the row's power of two; times the score's factor
     const float factor = p.scale_log2 * p.k_scale[g];
     {
-      const Row me = row_of(lane);
-      last = me.qi >= 0 ? L - c + me.qi : INT_MAX;  // a row without a query is never masked
-      cut = __reduce_min_sync(0xffffffffu, last);
+      // every row's vectors on their way at once
+      const int tile_first = job_s[0] + x * p.q_per_tile;  // the tile's first query
+      const int nq = min(p.q_per_tile, job_s[1] - tile_first);
+      const int q_step = (p.n_heads - p.rep) * HD;
+      const __nv_bfloat16* tile_q =
+          p.q + (int64_t(job_s[2] + tile_first) * p.n_heads + job_s[3] * p.rep) * HD;
+      {
+        const int q = (((warp & 3) * 32 + lane) * p.rep_inv) >> 16;  // row / rep
+        last = q < nq ? L - c + tile_first + q : INT_MAX;  // a row without a query is never masked
+        cut = __reduce_min_sync(0xffffffffu, last);
+      }
+      uint4 u[STEPS];
 #pragma unroll
-      for (int s0 = 0; s0 < STEPS; s0 += 8) {
-        uint4 u[8];
+      for (int i = 0; i < STEPS; ++i) {
+        const int rr = (warp & 3) * 32 + i * RG + lane / RL;
+        const int q = (rr * p.rep_inv) >> 16;
+        u[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (q < nq) u[i] = reinterpret_cast<const uint4*>(tile_q + int64_t(q) * q_step + rr * HD)[lane % RL];
+      }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const Row o = row_of((s0 + i) * RG + lane / RL);
-          u[i] = reinterpret_cast<const uint4*>(p.q + (o.qi >= 0 ? o.off : 0))[lane % RL];
-          if (o.qi < 0) u[i] = make_uint4(0u, 0u, 0u, 0u);
-        }
+      for (int i = 0; i < STEPS; ++i) {
+        const uint32_t e[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+        // the row's largest magnitude
+        __nv_bfloat162 m2 = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&e[0]));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t e[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-          float a = 0.f;
+        for (int k = 1; k < 4; ++k)
+          m2 = __hmax2(m2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&e[k])));
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            a = fmaxf(a, fmaxf(fabsf(__uint_as_float(e[k] << 16)),
-                               fabsf(__uint_as_float(e[k] & 0xffff0000u))));
+        for (int o = 1; o < RL; o <<= 1) m2 = __hmax2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+        const float a = fmaxf(__low2float(m2), __high2float(m2));
+        const int up = min(126, 14 + 127 - static_cast<int>(__float_as_uint(a) >> 23));
+        const float f = pow2f(up);
+        uint32_t o[4];
 #pragma unroll
-          for (int o = 1; o < RL; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-          const int up = min(126, 14 + 127 - static_cast<int>(__float_as_uint(a) >> 23));
-          const float f = pow2f(up);
-          uint32_t o[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            o[k] = pack_f16x2(__uint_as_float(e[k] << 16) * f,
-                              __uint_as_float(e[k] & 0xffff0000u) * f);
-          *reinterpret_cast<uint4*>(q_at((s0 + i) * RG + lane / RL, lane % RL)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
-          // the factor goes to the lane whose row it is
-          const float back = __shfl_sync(0xffffffffu, pow2f(-up), (lane % RG) * RL);
-          if (lane / RG == s0 + i) rs = back * factor;
-        }
+        for (int k = 0; k < 4; ++k)
+          o[k] = pack_f16x2(__uint_as_float(e[k] << 16) * f,
+                            __uint_as_float(e[k] & 0xffff0000u) * f);
+        *reinterpret_cast<uint4*>(q_at(i * RG + lane / RL, lane % RL)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+        // the factor goes to the lane whose row it is
+        const float back = __shfl_sync(0xffffffffu, pow2f(-up), (lane % RG) * RL);
+        if (lane / RG == i) rs = back * factor;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -744,10 +753,10 @@ cudaError_t run_tc(const AttnArgs& a, const Fp4Cache& cache, cudaStream_t stream
   static KernelSetup setup;
   cudaError_t e = kernel_setup(setup, kern, Lay::REQUEST, kThreads, nullptr);
   if (e != cudaSuccess) return e;
-  const int qpp = 2 * p.q_per_tile;
-  // ordered: one slot per (sequence, KV head, pair); the pairs number at most
-  // total_q / qpp + one partial pair per sequence
-  const int64_t slots = ((int64_t(a.total_q) + qpp - 1) / qpp + a.num_seqs) * pool.n_kv;
+  const int qpg = kTiles * p.q_per_tile;
+  // ordered: one slot per (sequence, KV head, group of row tiles); the groups number at
+  // most total_q / qpg + one partial group per sequence
+  const int64_t slots = ((int64_t(a.total_q) + qpg - 1) / qpg + a.num_seqs) * pool.n_kv;
   p.ordered = a.num_seqs <= kThreads && slots <= INT_MAX;
   // natural order: the grid's z extent is 16-bit, so long batches go in slices
   const int slice = p.ordered ? a.num_seqs : 65535;
@@ -758,7 +767,7 @@ cudaError_t run_tc(const AttnArgs& a, const Fp4Cache& cache, cudaStream_t stream
     p.cu_q = a.cu_q_lens + s0;
     p.last_seq = s0 + p.B == a.num_seqs ? p.B - 1 : -1;
     const dim3 grid = p.ordered ? dim3(static_cast<unsigned>(slots), 1, 1)
-                                : dim3((a.max_q_len + qpp - 1) / qpp, pool.n_kv, p.B);
+                                : dim3((a.max_q_len + qpg - 1) / qpg, pool.n_kv, p.B);
     if ((e = launch_pdl(kern, grid, kThreads, Lay::REQUEST, stream, p)) != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -532,6 +532,9 @@ __global__ void __launch_bounds__(kWideJoin * 32) join_few_kernel(const DecodePa
   const int b = blockIdx.x / p.n_groups, grp = blockIdx.x - b * p.n_groups;
   const WarpScan scan(p);
   const int2 seq = scan.of(b);
+  // the decode's partials; and a CTA that ends without the wait would let this grid, and so
+  // the kernel after it, run ahead of the decode
+  attn::pdl_wait();
   const int U = scan.total, G = p.grid;
   const int nblk = seq.y / p.n_groups;
   if (nblk == 0) return;
@@ -543,7 +546,6 @@ __global__ void __launch_bounds__(kWideJoin * 32) join_few_kernel(const DecodePa
   const int rows = p.hg_size * p.rep;
   const int E = rows * HD;  // elements of a part
   const int e = (blockIdx.y * 32 + lane) * 4;
-  attn::pdl_wait();  // the decode's partials
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float M = -INFINITY, den = 0.f;
   if (e < E) {

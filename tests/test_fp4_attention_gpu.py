@@ -60,6 +60,47 @@ def test_decode_many_sequences():
         bt.check(out, q, range(n), lens - 1)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens", [[8000], [5000, 1, 0], [3000, 17, 16, 1100]])
+@pytest.mark.parametrize("heads,n_kv,head_dim", [(8, 2, 64), (3, 1, 128), (16, 1, 16), (5, 5, 32)])
+def test_decode_few_long_sequences(heads, n_kv, head_dim, lens, dtype):
+    """Groups that many CTAs share."""
+    _decode_case(heads, n_kv, head_dim, dtype, lens, 0, seed=heads)
+
+
+@pytest.mark.parametrize("lens", [[16, 5], [16, 0, 900], [0, 1]])
+def test_decode_calls_in_a_row(lens):
+    """Each call reads what the call before it wrote, where few groups, or none, are
+    shared by CTAs though the longest length allowed would have them shared."""
+    import paged_kv_cache_write_gb300 as pkv
+    longest = 8192
+    bt = Batch(lens, n_kv=2, head_dim=64, seed=4)
+    bt.fill()
+    sl = guarded_copy(torch.from_numpy(bt.lens))
+    table = torch.zeros((len(lens), longest // 16), dtype=torch.int32, device="cuda")
+    table[:, :bt.bt.shape[1]] = bt.bt
+    ws = guarded_empty((pkv.decode_fp4_workspace_bytes(len(lens), 8, 64, longest),), torch.uint8)
+    n = 24
+    first = guarded_copy(bt.queries(len(lens), 8))
+
+    def chain(wait):
+        x = [first] + [torch.full_like(first, 3.0) for _ in range(n)]
+        torch.cuda.synchronize()
+        for i in range(n):
+            pkv.paged_attention_decode_fp4(x[i], *bt.cache, table, sl, 0.125, longest,
+                                           out=x[i + 1], workspace=ws, err=bt.err)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return torch.stack(x)
+
+    apart = chain(True)
+    bt.check(apart[1], first, range(len(lens)), bt.lens - 1)
+    for _ in range(5):
+        assert torch.equal(chain(False), apart)
+    bt.no_error()
+
+
 def test_decode_groups_far_apart():
     """Groups and heads whose scales differ as far as they can: nothing overflows or
     vanishes."""

@@ -132,7 +132,9 @@ struct Fetcher {
 
 // The CTA whose range holds unit u of U, of G CTAs: the largest c with floor(c U / G) <= u.
 __device__ __forceinline__ int owner_of(int u, int U, int G) {
-  return static_cast<int>((uint64_t(uint32_t(u) + 1u) * uint32_t(G) - 1u) / uint32_t(U));
+  const uint64_t n = uint64_t(uint32_t(u) + 1u) * uint32_t(G) - 1u;
+  if (n <= 0xffffffffull) return static_cast<int>(uint32_t(n) / uint32_t(U));  // (far shorter)
+  return static_cast<int>(n / uint32_t(U));
 }
 
 // The split entry of CTA c (of G, over U units) whose range starts at block j of a group
@@ -224,30 +226,42 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<T, HD, NT>)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = gridDim.x;
   const int me = blockIdx.x;
-  int U;
+  int U, r0, r1;  // all units, this CTA's range of them
   int4 st = make_int4(0, 0, 0, 0);
   int* lens_s = reinterpret_cast<int*>(smem + p.part_off);  // [kKeptLens]
   const bool kept = p.plan_in_kernel && p.part_off != 0 && p.B <= kKeptLens;
   if (p.B <= 32 * kLaneSeqs) {
-    const WarpScan scan(p);
-    U = scan.total;
-    const int r0 = attn::range_begin(me, U, G);
-    if (r0 < attn::range_begin(me + 1, U, G)) {
-      const int3 seq = scan.find(r0);
-      const int nblk = seq.z / p.n_groups;
-      const int grp = (r0 - seq.y) / nblk;
-      st = make_int4(seq.x, grp, (r0 - seq.y) - grp * nblk, 0);
+    // (one warp finds the CTA's place for all: each for itself, the scans and divisions
+    // were a third of what 64 sequences of 1,024 tokens issue)
+    __shared__ int4 range_s, start_s;
+    if (warp == 0) {
+      const WarpScan scan(p);
+      U = scan.total;
+      r0 = attn::range_begin(me, U, G);
+      r1 = attn::range_begin(me + 1, U, G);
+      if (r0 < r1) {
+        const int3 seq = scan.find(r0);
+        const int nblk = seq.z / p.n_groups;
+        const int grp = (r0 - seq.y) / nblk;
+        st = make_int4(seq.x, grp, (r0 - seq.y) - grp * nblk, 0);
+      }
+      if (lane == 0) {
+        range_s = make_int4(r0, r1, U, 0);
+        start_s = st;
+        if (me == 0) {
+          p.total_units[0] = U;
+          p.total_units[1] = -1;  // a call planning for itself replaces any kept plan
+        }
+      }
     }
     for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
       if (kept) lens_s[b] = length_of(p, b);
       if (blockIdx.x == 0) report_bad_length(p, b);
     }
     attn::zero_empty<T, HD>(p, blockIdx.x, G, [&](int b) { return length_of(p, b) == 0; });
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-      p.total_units[0] = U;
-      p.total_units[1] = -1;  // a call planning for itself replaces any kept plan
-    }
-    if (kept) __syncthreads();
+    __syncthreads();
+    r0 = range_s.x, r1 = range_s.y, U = range_s.z;
+    st = start_s;
   } else if (p.plan_in_kernel) {
     // scan the units per sequence in the (still unused) stages
     int* cu_s = reinterpret_cast<int*>(smem);  // [B + 1]
@@ -274,8 +288,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<T, HD, NT>)
     if (threadIdx.x == nt - 1) cu_s[p.B] = run;
     __syncthreads();
     U = cu_s[p.B];
-    const int r0 = attn::range_begin(me, U, G);
-    if (r0 < attn::range_begin(me + 1, U, G)) {
+    r0 = attn::range_begin(me, U, G);
+    r1 = attn::range_begin(me + 1, U, G);
+    if (r0 < r1) {
       const int b = attn::seq_of_unit(cu_s, p.B, r0);
       const int nblk = (cu_s[b + 1] - cu_s[b]) / p.n_groups;
       const int grp = (r0 - cu_s[b]) / nblk;
@@ -289,10 +304,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<T, HD, NT>)
     __syncthreads();  // (the stages are the rings' from here on)
   } else {
     U = __ldcg(p.total_units);
+    r0 = attn::range_begin(me, U, G);
+    r1 = attn::range_begin(me + 1, U, G);
     st = __ldcg(p.starts + me);
   }
-  const int r0 = attn::range_begin(me, U, G);
-  const int r1 = attn::range_begin(me + 1, U, G);
   const int rows_per_group = p.hg_size * p.rep;
   if (r0 >= r1) {
     if (threadIdx.x == 0) p.splits[me] = make_int4(-1, 0, 0, 0);

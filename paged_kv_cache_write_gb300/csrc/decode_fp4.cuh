@@ -40,7 +40,7 @@ using fp8::length_of;
 using fp8::report_bad_length;
 
 constexpr int kWarps = 8;       // of a CTA at the most: a head group's
-constexpr int kMaxBlocks = 8;   // of a warp of a cluster
+constexpr int kMaxBlocks = 32;  // of a warp of a cluster: a warp's lanes hold their ids
 constexpr int kMaxStages = 12;  // of a warp's ring
 constexpr int kSmemMax = 226 * 1024;  // of an SM's CTAs
 
@@ -429,9 +429,10 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
 // kMaxBlocks * C blocks, the parts combined through distributed shared memory (no
 // workspace, no joining launch).
 template <typename T, int HD, int NT>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<T, HD, NT>)
     decode_cluster_kernel(const DecodeParams p, const Pools pools) {
   extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int S = kStages<T, HD, NT>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int C = p.cluster;
   const int rank = static_cast<int>(cluster_ctarank());
@@ -439,26 +440,37 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int b = seg / p.n_groups;
   const int grp = seg - b * p.n_groups;
   const int rows_per_group = p.hg_size * p.rep;
-  float* part_o = reinterpret_cast<float*>(smem + p.part_off);  // [rows_per_group][HD]
-  float* part_ml = part_o + rows_per_group * HD;                // [rows_per_group][2]
+  // a warp's ring, afterwards its part [rep][HD]; behind the rings the parts' references
+  // and sums [rows_per_group][2]
+  const int room = p.nstages;  // bytes
+  uint8_t* ring = smem + warp * room;
+  float* part_o = reinterpret_cast<float*>(ring);
+  float* part_ml = reinterpret_cast<float*>(smem + p.part_off);
 
   attn::pdl_wait();
   attn::pdl_launch_dependents();
   const int L = length_of(p, b);
   const int nblk = (L + kBS - 1) / kBS;
-  const int j0 = rank * nblk / C, n = (rank + 1) * nblk / C - j0;  // n <= p.nstages
+  const int j0 = rank * nblk / C, n = (rank + 1) * nblk / C - j0;  // n <= kMaxBlocks
   if (blockIdx.x == 0 && threadIdx.x == 0)
     p.total_units[1] = -1;  // a call planning for itself replaces any kept plan
   if (rank == 0 && grp == 0 && threadIdx.x == 0) report_bad_length(p, b);
   const int kv_head = grp * p.hg_size + warp;
-  const uint8_t* tiles = smem + warp * p.nstages * Tile<HD>::kBytes;
-  {
-    const Fetcher<HD> fetch(pools, p.n_kv, p.num_blocks, p.err);
-    const int ids = lane < n ? p.bt[int64_t(b) * p.W + j0 + lane] : 0;
-    for (int i = 0; i < n; ++i)
-      fetch.block(smem_addr(tiles) + i * Tile<HD>::kBytes, __shfl_sync(0xffffffffu, ids, i), kv_head);
-    commit_copies();
-  }
+  const Fetcher<HD> fetch(pools, p.n_kv, p.num_blocks, p.err);
+  const int ids = lane < n ? p.bt[int64_t(b) * p.W + j0 + lane] : 0;
+  const uint32_t ring_at = smem_addr(ring);
+  uint32_t fill = 0;  // offset of the next stage to fill (a ring with room for all is never full)
+  int fed = 0;
+  auto feed = [&]() {
+    if (fed < n) {
+      fetch.block(ring_at + fill, __shfl_sync(0xffffffffu, ids, fed), kv_head);
+      fill = fill == (S - 1) * Tile<HD>::kBytes ? 0 : fill + Tile<HD>::kBytes;
+      ++fed;
+    }
+    commit_copies();  // (an empty group past the last block: waits count groups)
+  };
+#pragma unroll 1
+  for (int i = 0; i < S; ++i) feed();
   using RowsT = Rows<T, HD, NT, false>;
   const T* q = static_cast<const T*>(p.q) + (int64_t(b) * p.n_heads + int64_t(kv_head) * p.rep) * HD;
   RowsT rows;
@@ -466,20 +478,29 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   rows.begin([&](int r) -> const T* { return r < p.rep ? q + r * HD : nullptr; },
              [&](int) { return L - 1; }, p.scale_log2 * pools.k_scale[kv_head],
              pools.v_scale[kv_head]);
-  wait_copies<0>();
-  for (int i = 0; i < n;) {
-    const int jp = (j0 + i) * kBS;
-    const uint8_t* t = tiles + i * Tile<HD>::kBytes;
-    if (RowsT::PAIR == 2 && i + 1 < n) {
-      const uint8_t* two[2] = {t, t + Tile<HD>::kBytes};
-      rows.template blocks<2, true>(two, jp, L - jp);
-      i += 2;
-    } else {
-      const uint8_t* one[1] = {t};
-      rows.template blocks<1, true>(one, jp, L - jp);
-      ++i;
+  uint32_t at = 0;
+  auto take = [&](auto nb, int j) {
+    constexpr int NB = decltype(nb)::value;
+    const uint8_t* t[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      t[i] = ring + at;
+      at = at == (S - 1) * Tile<HD>::kBytes ? 0 : at + Tile<HD>::kBytes;
     }
+    wait_copies<S - NB>();
+    rows.template blocks<NB, true>(t, j * kBS, L - j * kBS);
+    __syncwarp();
+#pragma unroll 1
+    for (int i = 0; i < NB; ++i) feed();
+  };
+  int i = 0;
+  for (; i + RowsT::TAKE <= n; i += RowsT::TAKE)
+    take(std::integral_constant<int, RowsT::TAKE>{}, j0 + i);
+  if (RowsT::TAKE > 2 && i + 2 <= n) {
+    take(std::integral_constant<int, 2>{}, j0 + i);
+    i += 2;
   }
+  if (RowsT::TAKE > 1 && i < n) take(std::integral_constant<int, 1>{}, j0 + i);
   T* out = static_cast<T*>(p.out) + (int64_t(b) * p.n_heads + int64_t(grp) * rows_per_group) * HD;
   if (C == 1) {
     rows.store([&](int r) -> T* { return r < p.rep ? out + (warp * p.rep + r) * HD : nullptr; });
@@ -487,15 +508,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   }
   // this CTA's part
   rows.store_partial(
-      [&](int r) -> float* { return r < p.rep ? part_o + (warp * p.rep + r) * HD : nullptr; },
+      [&](int r) -> float* { return r < p.rep ? part_o + r * HD : nullptr; },
       [&](int r) -> float* { return part_ml + (warp * p.rep + r) * 2; });
 
   cluster_sync();  // every CTA's partial is in its shared memory
   // CTA `rank` combines float4s [rank E / C, (rank + 1) E / C) of the group's E
-  const int E = rows_per_group * HD / 4;
+  const int per_warp = p.rep * HD / 4;
+  const int E = p.hg_size * per_warp;
   const int e0 = rank * E / C, e1 = (rank + 1) * E / C;
   for (int e = e0 + static_cast<int>(threadIdx.x); e < e1; e += static_cast<int>(blockDim.x)) {
-    const int r = e / (HD / 4);
+    const int r = e / (HD / 4), w = e / per_warp;
+    const float* o_at = reinterpret_cast<const float*>(smem + w * room) + (e - w * per_warp) * 4;
     float2 ml[kMaxCluster];
     float4 oc[kMaxCluster];
 #pragma unroll
@@ -504,7 +527,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       oc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (c < C) {
         ml[c] = ld_cluster_f32x2(cluster_map(part_ml + r * 2, c));
-        oc[c] = ld_cluster_f32x4(cluster_map(part_o + e * 4, c));
+        oc[c] = ld_cluster_f32x4(cluster_map(o_at, c));
       }
     }
     float M = -INFINITY;
@@ -659,7 +682,6 @@ struct DecodeFp4 {
     if (e != cudaSuccess) return e;
     per_sm = std::max(1, std::min(per_sm, 16));  // 16: what the workspace is sized for
     int G = sm_count() * per_sm;
-    const int wave = G / kCtas;
     if (a.max_ctas > 0 && a.max_ctas < G) G = a.max_ctas;
     const int nmax = p.max_len / kBS + (p.max_len % kBS != 0);
     const int64_t max_units = int64_t(a.num_seqs) * p.n_groups * nmax;
@@ -683,17 +705,32 @@ struct DecodeFp4 {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
 
-    // Latency-bound batches, by the rule of the bf16 decode: the longest sequence at most
-    // 64 blocks and the clusters within two waves.
-    const int C = std::max(1, std::min(kMaxCluster, (nmax + 3) / 4));
-    const int64_t cluster_ctas = int64_t(p.B) * p.n_groups * C;
-    if (a.max_ctas == 0 && nmax <= kMaxBlocks * kMaxCluster && cluster_ctas <= 2 * int64_t(wave)) {
+    // Batches of sequences that a cluster can take whole.  A block takes a warp the same
+    // 0.6 us whether it has an SM for itself or shares it with fifteen others (it is its
+    // chain of dependent steps), so the fewer a warp has the better: as many CTAs to a
+    // sequence as the GPU runs at once, but one where that is at most two steps for its
+    // warps.  64 sequences of 8 x 64, 32 heads: of 128 tokens 5.4 us (two CTAs each 5.9,
+    // streamed 10.7), of 512 9.3 (14.1), of 2,048 23.6 (26.2); 700 sequences of 512 tokens
+    // of 8 x 128, 64 heads, one CTA each, 84 (92).  Clusters with many
+    // blocks a warp that leave much of the GPU idle lose to a stream: 1 sequence of 2,048
+    // tokens of 8 x 128 13.8 us (11.7; 8 sequences 14.2, 15.8), 16 sequences of 4,096
+    // 35.9 (29.8).
+    const int slots = sm_count() * per_sm;
+    const int64_t groups = int64_t(a.num_seqs) * p.n_groups;
+    int C = nmax <= 8 ? 1 : std::min(kMaxCluster, (nmax + 3) / 4);
+    // (clusters lie within GPCs, which leaves up to a tenth of the SMs' places empty, where
+    // an SM holds one CTA and clusters are of 7 or 8 a quarter)
+    auto fits = [&](int c) {
+      return groups * c * 20 <= int64_t(slots) * (c < 7 ? 18 : per_sm < 2 ? 13 : c == 7 ? 17 : 18);
+    };
+    while (C > 1 && !fits(C)) --C;
+    const int blocks = std::max(1, (nmax + C - 1) / C);  // a warp's
+    const int least = blocks <= 8 ? 0 : blocks <= 16 ? slots / 6 : slots * 3 / 4;
+    if (a.max_ctas == 0 && blocks <= kMaxBlocks && groups * C >= least) {
       p.cluster = C;
-      p.nstages = std::max(1, (nmax + C - 1) / C);
-      p.part_off = static_cast<int>(ring_bytes(hg, p.nstages));
-      const size_t rows = size_t(hg) * p.rep;
-      const size_t need = p.part_off + rows * HD * 4 + (rows * 2 * 4 + 15) / 16 * 16;
-      if (need > size_t(kSmemMax)) return cudaErrorInvalidValue;
+      p.nstages = (std::max(std::min(kDepth, blocks) * Tile<HD>::kBytes, p.rep * HD * 4) + 127) / 128 * 128;
+      p.part_off = hg * p.nstages;
+      const size_t need = p.part_off + (size_t(hg) * p.rep * 2 * 4 + 15) / 16 * 16;
       static KernelSetup cluster_setup;
       e = kernel_setup(cluster_setup, decode_cluster_kernel<T, HD, NT>, kSmemMax, kWarps * 32, nullptr);
       if (e != cudaSuccess) return e;
@@ -702,7 +739,7 @@ struct DecodeFp4 {
       attr[1].val.clusterDim.y = 1;
       attr[1].val.clusterDim.z = 1;
       cfg.numAttrs = 2;
-      cfg.gridDim = dim3(static_cast<unsigned>(cluster_ctas));
+      cfg.gridDim = dim3(static_cast<unsigned>(groups * C));
       cfg.blockDim = dim3(hg * 32);
       cfg.dynamicSmemBytes = need;
       e = cudaLaunchKernelEx(&cfg, decode_cluster_kernel<T, HD, NT>, p, pools);

@@ -308,6 +308,54 @@ def test_prefill_hidden_nan_stays_hidden(head_dim, dtype):
         clean.check(out[:at], q[:at], [0] * at, range(at), held=4)
 
 
+@pytest.mark.parametrize("seqs,heads,n_kv,head_dim", [(300, 8, 8, 64), (150, 16, 8, 128),
+                                                      (700, 6, 3, 64), (600, 4, 2, 128)])
+def test_prefill_many_chunks(seqs, heads, n_kv, head_dim):
+    """Far more work items than the GPU takes at once, in both orders of them (more than 512
+    sequences have the natural one), with NaNs that some queries see: every sequence's rows are
+    those of a call for it alone, and as the oracle has them."""
+    import paged_kv_cache_write_gb300 as pkv
+    rng = np.random.default_rng(seqs)
+    lens = rng.integers(1, 150, size=seqs)
+    new = np.minimum(lens, rng.integers(0, 150, size=seqs))
+    lens[5], new[5] = 700, 600
+    bt = Batch(lens, n_kv=n_kv, head_dim=head_dim, seed=seqs)
+    t = int(lens.sum())
+    k, v = bt.draw(t), bt.draw(t)
+    end = np.cumsum(lens)
+    # every third sequence: a NaN value at a position that part of its queries see
+    at = np.where((np.arange(seqs) % 3 == 0) & (new > 1), lens - new // 2, lens)
+    for b in np.flatnonzero(at < lens):
+        v[end[b] - lens[b] + at[b], b % n_kv, 17] = float("nan")
+    bt.write(bt.slots(lens, lens), k, v)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    q = bt.queries(int(cu[-1]), heads)
+    out = bt.prefill(q, lens, new)
+    bt.no_error()
+    rep = heads // n_kv
+    nan = out.isnan()
+    for b in range(seqs):
+        rows, first = nan[cu[b]:cu[b + 1]].cpu(), int(at[b] - (lens[b] - new[b]))
+        hit = torch.zeros_like(rows)
+        hit[first:, (b % n_kv) * rep:(b % n_kv + 1) * rep, 16:32] = bool(at[b] < lens[b])
+        assert torch.equal(rows, hit), b
+    dq = guarded_copy(q)
+    for b in list(range(0, seqs, 37)) + [5]:
+        c = int(new[b])
+        if c == 0:
+            continue
+        alone = pkv.paged_attention_prefill_fp4(
+            dq[cu[b]:cu[b + 1]], ints([0, c]), *bt.cache, bt.bt[b:b + 1], ints(lens[b:b + 1]),
+            1.0 / np.sqrt(head_dim), c, int(lens[b]), err=bt.err)
+        torch.cuda.synchronize()
+        assert torch.equal(alone.view(torch.int16), out[cu[b]:cu[b + 1]].view(torch.int16)), b
+    some = [(b, i) for b in range(1, seqs, 11) if at[b] == lens[b]
+            for i in range(0, int(new[b]), 23)]
+    at_rows = [cu[b] + i for b, i in some]
+    bt.check(out[at_rows], q[at_rows], [b for b, _ in some],
+             [int(lens[b] - new[b] + i) for b, i in some], held=4)
+
+
 def test_prefill_bad_device_data():
     import paged_kv_cache_write_gb300 as pkv
     for hd, dtype in ((32, torch.bfloat16), (64, torch.bfloat16), (128, torch.float32)):

@@ -684,7 +684,8 @@ typedef struct pkv_norm_rope_desc {
  *               otherwise.
  *   A token whose position is outside [0, num_positions) is reported
  *   (PKV_DEVERR_LENGTH) and gets zeros.
- *   Supported: head_dim a multiple of 16 up to 256.
+ *   Supported: head_dim a multiple of 16 up to 256; n_heads and n_kv up to 2^20 and
+ *   num_tokens up to 2^30 here and in the writes below (PKV_ERR_RANGE).
  */
 pkv_status pkv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                             int32_t dtype, int32_t num_tokens, int32_t n_heads, int32_t n_kv,
@@ -727,8 +728,8 @@ pkv_status pkv_qk_norm_rope_write(const void* q, int64_t q_stride, const void* k
  *
  * pool->dtype is PKV_FP4_E2M1, pool->head_dim counts elements: a multiple of 16 up
  * to 256 (attention: 16, 32, 64 or 128, with block_size 16); n_kv at most 65,535;
- * num_blocks * block_size and num_blocks * n_kv below 2^31.  `dtype` is the type of k, v, q and the
- * outputs (PKV_F32 or PKV_BF16).
+ * num_blocks * block_size and num_blocks * n_kv below 2^31.  `dtype` is the type of
+ * k, v, q and the outputs (PKV_F32 or PKV_BF16).
  *
  * A block is copied on write with two pkv_copy_blocks calls: one on the pools
  * described as bf16 with head_dim / 4 (the bytes are copied as they are), one on
@@ -794,14 +795,15 @@ pkv_status pkv_kv_gather_fp4(const void* k_pool, const void* v_pool, const void*
  * counts this step's token (write it first).  A sequence of length 0 gets zeros; slots
  * past the length are never used, whatever bytes they hold.
  *
- * The work split, and with it what results depend on, is that of
- * pkv_paged_attention_decode: logical positions, lengths and max_ctas, never physical
- * block ids; identical calls give identical bits.  Keys and values
- * enter exactly (code times group scale, the head's scale in the score and the output);
- * scores, softmax sums and outputs are held in fp32.  For bf16, weights are rounded to 11
- * significand bits before they multiply V, those below 2^-18 of a row's largest to fewer;
- * for fp32 queries and weights keep 22.  A query element more than 2^28 below its row's
- * largest loses bits.
+ * The work split follows the number of sequences, their lengths, max_seq_len and
+ * max_ctas (0: as many as the GPU runs at once; otherwise that many at most share the
+ * batch), and so, in the last bits, do results; physical block ids never matter, and
+ * identical calls give identical bits.  A max_seq_len near the longest length gives the
+ * better split.  Keys and values enter exactly (code times group scale, the head's scale
+ * in the score and the output); scores, softmax sums and outputs are held in fp32.  For
+ * bf16, weights are rounded to 11 significand bits before they multiply V, those below
+ * 2^-18 of a row's largest to fewer; for fp32 queries and weights keep 22.  A query
+ * element more than 2^28 below its row's largest loses bits.
  *
  *   q, out      [num_seqs, n_heads, head_dim] of `dtype`, 16-byte aligned
  *   workspace   at least pkv_decode_fp4_workspace_bytes(...) bytes, 16-byte aligned;
@@ -826,7 +828,8 @@ pkv_status pkv_paged_attention_decode_fp4(
  * pkv_paged_attention_prefill_fp4 - pkv_paged_attention_prefill over a 4-bit cache:
  * causal attention of each sequence's query chunk over its paged history (the chunk's
  * own K/V written first).  A key or value that a query may not see does not reach its
- * output, NaN included.  It needs no workspace.  Precision as for the decode.  cu_q_lens, and which rows are left as they were, as for
+ * output, NaN included.  It needs no workspace.  Precision as for the decode.
+ * cu_q_lens, and which rows are left as they were, as for
  * pkv_paged_attention_prefill_fp8; supported shapes as for the decode.
  */
 pkv_status pkv_paged_attention_prefill_fp4(

@@ -2,21 +2,26 @@
 // (mathematics and layouts of the tiles in fp4_rows.cuh).
 //
 // Bound by reading the cache, 9 / 8 x n_kv x head_dim bytes a token, and close behind by
-// the instructions that turn codes into f16 operands: some 290 a block and head of 128,
-// where the SM's schedulers have 397 in the time that the block takes to arrive.  So
+// the instructions that turn codes into f16 operands: 292 a block and head of 128 (187 of
+// 64), where the SM's schedulers have 397 in the time that the block takes to arrive.  So
 // nothing is spent on synchronisation: a head's rows of a block lie together in the
 // pools (four runs: K and V, codes and scales, 2.3 KB at head_dim 128), and each warp
 // fetches its own into a ring of its own, by asynchronous 16-byte copies of all its lanes
 // as soon as it has left a stage.  No warp waits for another, and there is no barrier.
 // (Bulk copies would be issued one by one, some 25 instructions each: 142 us for 256
-// sequences of 16 - 8,192 tokens, 64 heads on 8 of 128.)
+// sequences of 16 - 8,192 tokens, 64 heads on 8 of 128, which take 108 so.)
 //
-// Work split: equal contiguous ranges of (sequence, head group, block) units, one per CTA
-// of a persistent grid, a warp for each KV head of the group (so that the heads of a
-// block, which lie together, are read at about the same time: ranges of (sequence, head,
-// block) units for each warp by itself reach 5.7 TB/s where these reach 6.3); a joining
-// kernel for the groups that several CTAs share; one thread-block cluster per (sequence, head group) for batches too small to
-// stream, combined through distributed shared memory.
+// Work split: one CTA or one thread-block cluster per (sequence, head group), combined
+// through distributed shared memory, where that fills the GPU evenly enough; else equal
+// contiguous ranges of (sequence, head group, block) units, one per CTA of a persistent
+// grid, and a joining kernel for the groups that several CTAs share.  Either way a warp for
+// each KV head of the group, so that the heads of a block, which lie together, are read at
+// about the same time (ranges of (sequence, head, block) units for each warp by itself: 117
+// us for those 256 sequences, 94 for the copies alone; these 111 and 90).
+//
+// Those 256 sequences: 108 us, 5.0 TB/s, of which the joining launch takes 6.3 and the
+// partial results 2.5; issue slots are 63% taken, the ALUs 54%.  64 sequences of 512 - 2,048
+// tokens, 32 heads on 8 of 64: 22.5 us in clusters of four.
 #pragma once
 
 #include <algorithm>
@@ -231,8 +236,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<T, HD, NT>)
   int* lens_s = reinterpret_cast<int*>(smem + p.part_off);  // [kKeptLens]
   const bool kept = p.plan_in_kernel && p.part_off != 0 && p.B <= kKeptLens;
   if (p.B <= 32 * kLaneSeqs) {
-    // (one warp finds the CTA's place for all: each for itself, the scans and divisions
-    // were a third of what 64 sequences of 1,024 tokens issue)
+    // (one warp finds the CTA's place for all: 0.2 - 0.3 us less than each for itself)
     __shared__ int4 range_s, start_s;
     if (warp == 0) {
       const WarpScan scan(p);
@@ -424,10 +428,9 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
-// Batches too small to stream: one cluster of C CTAs per (sequence, head group), a warp
-// per head of the group, each CTA a contiguous part of the sequence's at most
-// kMaxBlocks * C blocks, the parts combined through distributed shared memory (no
-// workspace, no joining launch).
+// One cluster of C CTAs per (sequence, head group), a warp per head of the group, each CTA
+// a contiguous part of the sequence's at most kMaxBlocks * C blocks, the parts combined
+// through distributed shared memory: no lengths to scan, no workspace, no joining launch.
 template <typename T, int HD, int NT>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<T, HD, NT>)
     decode_cluster_kernel(const DecodeParams p, const Pools pools) {

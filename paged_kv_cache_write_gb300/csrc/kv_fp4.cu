@@ -2,7 +2,8 @@
 //
 // Bound by HBM: 9 / 16 byte an element in and 2 or 4 out.  A CTA reads back a
 // window of 32 tokens, found by one pass over the offsets; an item is as many
-// elements as fill one 16-byte store, so that a warp's stores are contiguous.
+// elements as fill one 16-byte store, so that a warp's stores are contiguous.  64 sequences
+// of 512 - 2,048 tokens of 8 x 64 as bf16: 36.4 us, 5.7 TB/s (a copy 6.7).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -20,7 +21,7 @@ namespace {
 constexpr int kThreads = kWindowThreads;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 2;   // rows a warp reads at once
-constexpr int kSteps = 2;  // and steps of 32 items in each (four rows: 39 us for 36.6, below)
+constexpr int kSteps = 2;  // and steps of 32 items in each (four rows: 39 us for those 36.4)
 
 struct GatherParams {
   const uint8_t *k_pool, *v_pool, *k_groups, *v_groups;

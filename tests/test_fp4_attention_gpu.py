@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from fp4_step import Batch, ints
+from fp4_step import Batch, f64, ints
 from gpu_step import check_canaries, guarded_copy, guarded_empty
 
 pytestmark = pytest.mark.gpu
@@ -233,6 +233,28 @@ def test_decode_captured_and_on_streams(max_ctas, n):
     torch.cuda.synchronize()
     assert torch.equal(outs[0], alone[0]) and torch.equal(outs[1], alone[1])
     bt.no_error()
+
+
+@pytest.mark.parametrize("n_kv,head_dim", [(1, 64), (2, 128), (2, 32)])
+def test_f32_sums_over_long_sequences(n_kv, head_dim):
+    """Outputs of fp32 calls do not drift with the length.  The sums over 256 blocks are rounded
+    at each (a random walk of sqrt(256 / 3) steps of 2^-24: 0.6e-6) and the scores, of a few
+    units, are good to some 0.3e-6; sums that are cut off instead would be 256 x 2^-25 = 7.6e-6
+    too small."""
+    n, c = 4096, 24
+    bt = Batch([n], n_kv=n_kv, head_dim=head_dim, dtype="f32", seed=1, scale=2.0 ** -6)
+    k, v = bt.draw(n, 0.5), 1.0 + 0.25 * torch.randn(n, n_kv, head_dim, generator=bt.g)
+    bt.write(bt.slots([n], [n]), k, v.float())
+    q = bt.queries(c, 2 * n_kv, mag=0.2)
+    outs = [(bt.prefill(q, [n], [c]), range(n - c, n))]
+    for ctas in (0, 1, 7):
+        outs.append((bt.decode(q[-1:], max_ctas=ctas), [n - 1]))
+    bt.no_error()
+    for out, lasts in outs:
+        for i, last in enumerate(lasts):
+            ref, _ = bt.reference(f64(q[i - len(lasts)]), 0, last)
+            off = np.linalg.norm(f64(out[i]) - ref) / np.linalg.norm(ref)
+            assert off <= 1.5e-6, (off, i, len(lasts))
 
 
 # ----------------------------------------------------------------- prefill

@@ -378,6 +378,49 @@ def test_prefill_many_chunks(seqs, heads, n_kv, head_dim):
              [int(lens[b] - new[b] + i) for b, i in some], held=4)
 
 
+@pytest.mark.parametrize("head_dim,dtype", [(64, "bf16"), (128, "bf16"), (64, "f32")])
+def test_prefill_captured_and_at_once(head_dim, dtype):
+    """Two calls that run side by side (streams given as objects and as handles), each with more
+    work than the GPU takes at once, and a captured one over new queries, give what each gives
+    alone."""
+    import paged_kv_cache_write_gb300 as pkv
+    rng = np.random.default_rng(9)
+    lens = rng.integers(1, 200, size=90)
+    bt = Batch(lens, n_kv=4, head_dim=head_dim, dtype=dtype, seed=9)
+    bt.fill()
+    t = int(lens.sum())
+    qs = [guarded_copy(bt.queries(t, 8)) for _ in range(2)]
+    cu, sl = ints(np.concatenate([[0], np.cumsum(lens)])), ints(lens)
+
+    def call(q, out, stream=None):
+        return pkv.paged_attention_prefill_fp4(q, cu, *bt.cache, bt.bt, sl, 0.125, int(lens.max()),
+                                               int(lens.max()), out=out, err=bt.err, stream=stream)
+
+    alone = [call(q, torch.empty_like(q)).clone() for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.full_like(q, 7.0) for q in qs]
+    torch.cuda.synchronize()
+    for i in range(12):
+        for s, q, o in zip(streams, qs, outs):
+            call(q, o, stream=s if i % 2 else s.cuda_stream)
+    torch.cuda.synchronize()
+    for o, ref in zip(outs, alone):
+        assert torch.equal(o, ref)
+    static, out = qs[0].clone(), torch.empty_like(qs[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(static, out)
+        call(static, out)
+    for k in (1, 0, 1):
+        static.copy_(qs[k])
+        out.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, alone[k])
+    bt.no_error()
+
+
 def test_prefill_bad_device_data():
     import paged_kv_cache_write_gb300 as pkv
     for hd, dtype in ((32, torch.bfloat16), (64, torch.bfloat16), (128, torch.float32)):

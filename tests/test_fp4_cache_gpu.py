@@ -190,6 +190,32 @@ def test_a_shared_block_is_copied_then_written(n_kv, head_dim):
     bt.assert_same_cache()
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_write_and_read_back_on_a_stream(handle):
+    """Calls on a stream of their own, behind work that they have to wait for."""
+    bt = Batch([30, 50], n_kv=4, head_dim=64, seed=5)
+    t = 80
+    k, v = (guarded_copy(bt.draw(t)) for _ in range(2))
+    at, lens, cu = ints(bt.slots(bt.lens, bt.lens), np.int64), ints(bt.lens), ints([0, 30, 80])
+    late_k, late_v = torch.zeros_like(k), torch.zeros_like(v)
+    st = torch.cuda.Stream()
+    where = st.cuda_stream if handle else st
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(2_000_000)
+        late_k.copy_(k)
+        late_v.copy_(v)
+    bt.pkv.kv_write_fp4(late_k, late_v, at, *bt.cache, err=bt.err, stream=where)
+    x, y = bt.pkv.kv_gather_fp4(*bt.cache, bt.bt, lens, cu, t, err=bt.err, stream=where)
+    st.synchronize()
+    bt.take(bt.slots(bt.lens, bt.lens), f64(k), f64(v))
+    bt.assert_same_cache()
+    rows = [bt.rows(b, n) for b, n in enumerate(bt.lens)]
+    assert np.array_equal(f64(x), np.concatenate([r[0] for r in rows]))
+    assert np.array_equal(f64(y), np.concatenate([r[1] for r in rows]))
+    bt.no_error()
+
+
 def test_captured_write_and_read_back():
     bt = Batch([30, 50], n_kv=4, head_dim=64, seed=4)
     t = 80

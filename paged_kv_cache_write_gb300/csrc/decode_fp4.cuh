@@ -708,16 +708,17 @@ struct DecodeFp4 {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
 
-    // Batches of sequences that a cluster can take whole.  A block takes a warp the same
-    // 0.6 us whether it has an SM for itself or shares it with fifteen others (it is its
-    // chain of dependent steps), so the fewer a warp has the better: as many CTAs to a
-    // sequence as the GPU runs at once, but one where that is at most two steps for its
-    // warps.  64 sequences of 8 x 64, 32 heads: of 128 tokens 5.4 us (two CTAs each 5.9,
-    // streamed 10.7), of 512 9.3 (14.1), of 2,048 23.6 (26.2); 700 sequences of 512 tokens
-    // of 8 x 128, 64 heads, one CTA each, 84 (92).  Clusters with many
-    // blocks a warp that leave much of the GPU idle lose to a stream: 1 sequence of 2,048
-    // tokens of 8 x 128 13.8 us (11.7; 8 sequences 14.2, 15.8), 16 sequences of 4,096
-    // 35.9 (29.8).
+    // Batches of sequences that a cluster can take whole.  A block takes a warp about the
+    // same time (0.55 us at 64, 0.75 at 128) whether it has an SM for itself or shares it
+    // with fifteen others (it is its chain of dependent steps), so the fewer a warp has the
+    // better: as many CTAs to a sequence as the GPU runs at once, but one where that is at
+    // most two steps for its warps.  A stream shares the blocks out evenly, but pays some 6
+    // us for its scan, its partial results and its join (9 where groups are narrow): so
+    // clusters as long as their warps have few blocks more, if all sequences were of the
+    // longest length.  64 sequences of 8 x 64, 32 heads: of 128 tokens 5.4 us (two CTAs each
+    // 5.9, streamed 10.7), of 512 9.3 (14.1), of 2,048 23.6 (26.2); 20 of 4,096 22.5 (21.3);
+    // 700 of 512 tokens of 8 x 128, 64 heads, one CTA each, 84 (92); 16 of 4,096 35.9 (29.8);
+    // 11 of 1,211 of 3 x 64, 9 heads, 6.8 (13.0); 46 of 2,202 of 3 x 128 18.3 (16.3).
     const int slots = sm_count() * per_sm;
     const int64_t groups = int64_t(a.num_seqs) * p.n_groups;
     int C = nmax <= 8 ? 1 : std::min(kMaxCluster, (nmax + 3) / 4);
@@ -728,8 +729,9 @@ struct DecodeFp4 {
     };
     while (C > 1 && !fits(C)) --C;
     const int blocks = std::max(1, (nmax + C - 1) / C);  // a warp's
-    const int least = blocks <= 8 ? 0 : blocks <= 16 ? slots / 6 : slots * 3 / 4;
-    if (a.max_ctas == 0 && blocks <= kMaxBlocks && groups * C >= least) {
+    const int more = blocks - static_cast<int>(max_units / G);  // than a stream's warps would have
+    const int most = HD == 128 ? 9 : hg < 4 ? 16 : 12;
+    if (a.max_ctas == 0 && blocks <= kMaxBlocks && more <= most) {
       p.cluster = C;
       p.nstages = (std::max(std::min(kDepth, blocks) * Tile<HD>::kBytes, p.rep * HD * 4) + 127) / 128 * 128;
       p.part_off = hg * p.nstages;

@@ -688,7 +688,10 @@ struct DecodeFp4 {
     if (a.max_ctas > 0 && a.max_ctas < G) G = a.max_ctas;
     const int nmax = p.max_len / kBS + (p.max_len % kBS != 0);
     const int64_t max_units = int64_t(a.num_seqs) * p.n_groups * nmax;
-    if (max_units < G) G = static_cast<int>(std::max<int64_t>(1, max_units));
+    // (parts of four blocks at the least: one sequence of 4,096 tokens of 8 x 128 takes 10.4
+    // us so, in parts of one block 17.1, of eight 12.4)
+    const int part = a.max_ctas > 0 ? 1 : 4;
+    if (max_units < int64_t(part) * G) G = static_cast<int>(std::max<int64_t>(1, max_units / part));
     if (G > 65535) return cudaErrorInvalidValue;  // split entries pack CTA indices in 16 bits
     p.grid = G;
     const DecodeWs L(a.num_seqs, G, size_t(hg) * p.rep, HD);
@@ -729,7 +732,8 @@ struct DecodeFp4 {
     };
     while (C > 1 && !fits(C)) --C;
     const int blocks = std::max(1, (nmax + C - 1) / C);  // a warp's
-    const int more = blocks - static_cast<int>(max_units / G);  // than a stream's warps would have
+    // (than an even share)
+    const int more = blocks - static_cast<int>(max_units / std::max<int64_t>(1, std::min<int64_t>(slots, max_units)));
     const int most = HD == 128 ? 9 : hg < 4 ? 16 : 12;
     if (a.max_ctas == 0 && blocks <= kMaxBlocks && more <= most) {
       p.cluster = C;

@@ -733,7 +733,8 @@ struct DecodeFp4 {
     while (C > 1 && !fits(C)) --C;
     const int blocks = std::max(1, (nmax + C - 1) / C);  // a warp's
     // (than an even share)
-    const int more = blocks - static_cast<int>(max_units / std::max<int64_t>(1, std::min<int64_t>(slots, max_units)));
+    const int64_t shares = std::max<int64_t>(1, std::min<int64_t>(slots, max_units));
+    const int more = blocks - static_cast<int>(max_units / shares);
     const int most = HD == 128 ? 9 : hg < 4 ? 16 : 12;
     if (a.max_ctas == 0 && blocks <= kMaxBlocks && more <= most) {
       p.cluster = C;
@@ -757,8 +758,10 @@ struct DecodeFp4 {
     p.nstages = kDepth;
     p.part_off = kept != 0 ? static_cast<int>(ring_bytes(hg, kDepth)) : 0;  // the kept lengths
     // every CTA scans the lengths in its stages; larger batches have a plan kernel
-    p.plan_in_kernel = a.num_seqs <= 32 * kLaneSeqs ||
-                       (a.num_seqs <= kKernelPlanSeqs && size_t(a.num_seqs + 1 + 32) * 4 <= size_t(hg) * kDepth * Tile<HD>::kBytes);
+    p.plan_in_kernel =
+        a.num_seqs <= 32 * kLaneSeqs ||
+        (a.num_seqs <= kKernelPlanSeqs &&
+         size_t(a.num_seqs + 1 + 32) * 4 <= size_t(hg) * kDepth * Tile<HD>::kBytes);
     if (!p.plan_in_kernel) {
       attn::decode_plan_kernel<T, HD><<<1, 1024, 0, stream>>>(p);
       if ((e = cudaGetLastError()) != cudaSuccess) return e;

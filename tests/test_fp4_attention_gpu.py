@@ -68,6 +68,16 @@ def test_decode_few_long_sequences(heads, n_kv, head_dim, lens, dtype):
     _decode_case(heads, n_kv, head_dim, dtype, lens, 0, seed=heads)
 
 
+@pytest.mark.parametrize("seqs,longest,heads,n_kv,head_dim,dtype", [
+    (40, 1500, 16, 8, 64, "bf16"), (40, 1500, 8, 8, 128, "bf16"), (20, 2000, 16, 8, 64, "f32"),
+    (280, 500, 8, 8, 16, "bf16"), (330, 500, 8, 8, 16, "f32"), (9, 1900, 12, 1, 64, "bf16")])
+def test_decode_many_blocks_a_warp(seqs, longest, heads, n_kv, head_dim, dtype):
+    """Whole sequences to a CTA or a cluster, with more blocks to a warp than it holds at once."""
+    lens = np.random.default_rng(seqs).integers(0, longest + 1, size=seqs)
+    lens[3] = longest
+    _decode_case(heads, n_kv, head_dim, dtype, lens, 0, seed=seqs)
+
+
 @pytest.mark.parametrize("lens", [[16, 5], [16, 0, 900], [0, 1]])
 def test_decode_calls_in_a_row(lens):
     """Each call reads what the call before it wrote, where few groups, or none, are

@@ -121,6 +121,7 @@ typedef enum pkv_dtype {
 #define PKV_DEVERR_TIMEOUT    16  /* a pipeline wait gave up (kernel returned early) */
 #define PKV_DEVERR_PREFIX     32  /* a table does not start with the declared shared prefix */
 #define PKV_DEVERR_PLAN       64  /* a planned call whose plan was made for other sizes     */
+#define PKV_DEVERR_SCALE     128  /* a 4-bit write's head scale no power of two, 2^-60 .. 2^60 */
 
 /* Shape of one layer's K pool (the V pool has the same shape). */
 typedef struct pkv_pool_desc {
@@ -721,8 +722,9 @@ pkv_status pkv_qk_norm_rope_write(const void* q, int64_t q_stride, const void* k
  *   - g, the scale of its KV head for the whole cache: k_scale, v_scale fp32 [n_kv],
  *     powers of two in 2^-60 .. 2^60 (an argument of every entry, chosen by the
  *     caller so that a row's largest elements, over 6 g, lie well within e4m3's
- *     2^-6 .. 448).  The reading entries take any positive finite g in those
- *     bounds.
+ *     2^-6 .. 448).  A write with another g for some head reports it
+ *     (PKV_DEVERR_SCALE) and stores nothing of that head's keys (values); the
+ *     reading entries take any positive finite g in those bounds.
  * A head's rows of a block lie together, so that whole blocks of any number of
  * heads start on 16 bytes.  Pools and groups are 16-byte aligned.
  *

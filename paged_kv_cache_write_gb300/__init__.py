@@ -42,7 +42,7 @@ PKV_BF16 = 1
 PKV_FP8_E4M3 = 2
 PKV_FP4_E2M1 = 3
 DEVERR = {"block_id": 1, "slot": 2, "table_width": 4, "length": 8, "timeout": 16, "prefix": 32,
-          "plan": 64}
+          "plan": 64, "scale": 128}
 
 
 class PoolDesc(ctypes.Structure):
@@ -836,7 +836,8 @@ def kv_write_fp4(k, v, slot_mapping, k_pool, v_pool, k_groups, v_groups, k_scale
     slot_mapping [T]: pools of e2m1 codes, two to a byte, uint8 [num_blocks, n_kv,
     block_size, head_dim / 2]; a ``torch.float8_e4m3fn`` scale per 16 elements of a
     row, [num_blocks, n_kv, block_size, head_dim / 16]; and a float32 scale per KV
-    head, a power of two, [n_kv], which the caller chooses once for the cache.
+    head, a power of two, [n_kv], which the caller chooses once for the cache (another is
+    reported in ``err``, and that head not written).
 
     A token's codes depend on that token alone.  Values past 2,688 x its head's
     scale saturate; a group's scale loses precision below 0.1 x it.

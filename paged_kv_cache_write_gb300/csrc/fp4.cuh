@@ -56,6 +56,12 @@ __device__ __forceinline__ float pow2_inverse(float g) {
   return __uint_as_float(0x7f000000u - __float_as_uint(g));
 }
 
+// Whether g is a head's scale that codes can be made for: a power of two, 2^-60 .. 2^60.
+__device__ __forceinline__ bool is_head_scale(float g) {
+  const uint32_t u = __float_as_uint(g);
+  return (u & 0x007fffffu) == 0u && u - (67u << 23) <= (120u << 23);
+}
+
 // a / d, where a is the exact sum of the returned value and a remainder: rounded
 // to nearest, but odd where it is not exact, so that a later rounding to fewer
 // bits decides as on the quotient itself (a border between two codes has an even

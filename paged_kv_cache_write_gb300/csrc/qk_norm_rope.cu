@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<TURN>)
   const int kind = col < p.q_cols ? 0 : col < p.q_cols + p.kv_cols ? 1 : 2;
   const int h = (kind == 0 ? col : col - p.q_cols - (kind - 1) * p.kv_cols) * (32 / LPH) + sub;
   // (head_dim / 16 need not fill the LPH lanes, nor the heads the last column)
-  const bool mine = l * 16 < a.head_dim && h < (kind == 0 ? a.n_heads : a.n_kv);
+  bool mine = l * 16 < a.head_dim && h < (kind == 0 ? a.n_heads : a.n_kv);
   // ---- the lane's two vectors: dims da .. da + 7 and db .. db + 7
   const int half = a.rot / 2;
   int da = l * 16, db = da + 8;
@@ -175,6 +175,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<TURN>)
     codes_at = static_cast<uint8_t*>(kind == 2 ? a.v_pool : a.k_pool) + row * (a.head_dim / 2);
     groups_at = (kind == 2 ? a.v_groups : a.k_groups) + row * (a.head_dim / 16);
     if (mine) g = (kind == 2 ? a.v_scale : a.k_scale)[h];
+    if (!fp4::is_head_scale(g)) {  // (its inverse would not be one: no codes for this head)
+      report(a.err, PKV_DEVERR_SCALE);
+      mine = false;
+      g = 1.f;
+    }
   } else {
     dst = static_cast<T*>(kind == 2 ? a.v_pool : a.k_pool) + int64_t(h) * a.head_dim;
   }

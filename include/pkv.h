@@ -802,10 +802,13 @@ pkv_status pkv_kv_gather_fp4(const void* k_pool, const void* v_pool, const void*
  * batch), and so, in the last bits, do results; physical block ids never matter, and
  * identical calls give identical bits.  A max_seq_len near the longest length gives the
  * better split.  Keys and values enter exactly (code times group scale, the head's scale
- * in the score and the output); scores, softmax sums and outputs are held in fp32.  For
- * bf16, weights are rounded to 11 significand bits before they multiply V, those below
- * 2^-18 of a row's largest to fewer; for fp32 queries and weights keep 22.  A query
- * element more than 2^28 below its row's largest loses bits.
+ * in the score and the output); scores, softmax sums and outputs are held in fp32.
+ *   bf16  Weights are rounded to 11 significand bits before they multiply V, those below
+ *         2^-18 of a row's largest to fewer (off by up to 2^-29 of it).  Query elements
+ *         are exact down to 2^-28 of their row's largest.
+ *   fp32  Weights keep 22 bits down to 2^-18 of a row's largest; smaller ones are off by
+ *         up to 2^-40 of it.  Query elements keep 22 bits down to 2^-17 of their row's
+ *         largest; smaller ones are off by up to 2^-39 of it.  Output sums are rounded.
  *
  *   q, out      [num_seqs, n_heads, head_dim] of `dtype`, 16-byte aligned
  *   workspace   at least pkv_decode_fp4_workspace_bytes(...) bytes, 16-byte aligned;

@@ -16,10 +16,16 @@
 // in f16 once it is multiplied by the power of two that brings its largest element
 // to 2^14 .. 2^15 (undone in the score's factor).  Weights are rounded to f16 (11
 // bits, where a bf16 output has 8).  fp32 queries and weights are split in two f16
-// terms (22 bits): HILO.  The tensor cores cut their sums off instead of rounding them, and
-// over a long sequence that adds up, so for fp32 each block's product is added to the output
-// by itself: of 2,048 tokens of heads of 128, 256 queries each, outputs are off by 0.97e-6
-// for 4.8e-6, in 164 us for 145.  (The scores' products too: 0.51e-6, 181 us.)
+// terms (22 bits): HILO.  A query's second term ends at f16's 2^-24, which is 2^-38 of its
+// row's largest element.  A weight's would end at 2^-28 of the reference's, and lose what
+// many small weights have in common (4,096 equal ones 2^-18 of the first: 1e-4), so it is
+// taken times 2^11 and its product with V divided by that: 22 bits down to 2^-18 (64
+// sequences of 512 - 2,048 tokens, 32 heads on 8 of 64, 29.7 us for 28.2; prefill of 4 chunks
+// of 256 at the end of 1,000 tokens, 8 heads on 4 of 128, 88.7 for 83.2).
+// The tensor cores cut their sums off instead of rounding them, and over a long sequence
+// that adds up, so for fp32 each block's product is added to the output by itself: of 2,048
+// tokens of heads of 128, 256 queries each, outputs are off by 0.97e-6 for 4.8e-6, in 164 us
+// for 145.  (The scores' products too: 0.51e-6, 181 us.)
 //
 // Tokens and head dims are the 16 rows of the A operand and the query rows the 8
 // columns of B, so eight query heads of a KV head fill a tile.
@@ -58,6 +64,9 @@ using fp8::unpack_f16x2;
 
 constexpr float kWeightLog2 = 4.f;     // log2 of the reference's weight
 constexpr float kWeightMax = 65504.f;  // f16's largest
+// An fp32 weight's second term times 2^11: at most 2^4, half a step of the largest f16
+// number, so it stays within f16, and is a normal number where the first term is one.
+constexpr float kLowUp = 2048.f, kLowDown = 1.f / 2048.f;
 // No reference yet: below every score that fp32 holds by more than it rounds away, so
 // that a visible key's weight comes out infinite and a hidden one's (-inf) zero.
 constexpr float kNone = -3.0e38f;
@@ -348,8 +357,8 @@ struct Rows {
           pb[nt][0][h] = transpose_8x8(hi);
           if constexpr (HILO) {
             const float2 f = unpack_f16x2(hi);
-            pb[nt][1][h] =
-                transpose_8x8(pack_f16x2(pw[nb][nt][2 * h] - f.x, pw[nb][nt][2 * h + 1] - f.y));
+            pb[nt][1][h] = transpose_8x8(pack_f16x2((pw[nb][nt][2 * h] - f.x) * kLowUp,
+                                                    (pw[nb][nt][2 * h + 1] - f.y) * kLowUp));
           }
         }
       const uint32_t s0 = scales_f16x2(vs[nb][0], vs[nb][1]);  // of the tokens' pairs
@@ -372,9 +381,10 @@ struct Rows {
           for (int nt = 0; nt < NT; ++nt) {
             if constexpr (HILO) {
               float d[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_f16_16816(d, a0, a1, a2, a3, pb[nt][1][0], pb[nt][1][1]);
 #pragma unroll
-              for (int pt = 0; pt < PARTS; ++pt)
-                mma_f16_16816(d, a0, a1, a2, a3, pb[nt][pt][0], pb[nt][pt][1]);
+              for (int k = 0; k < 4; ++k) d[k] *= kLowDown;
+              mma_f16_16816(d, a0, a1, a2, a3, pb[nt][0][0], pb[nt][0][1]);
 #pragma unroll
               for (int k = 0; k < 4; ++k) o[nt][4 * i + e][k] += d[k];
             } else {

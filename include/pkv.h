@@ -805,7 +805,10 @@ pkv_status pkv_kv_gather_fp4(const void* k_pool, const void* v_pool, const void*
  * in the score and the output); scores, softmax sums and outputs are held in fp32.
  *   bf16  Weights are rounded to 11 significand bits before they multiply V, those below
  *         2^-18 of a row's largest to fewer (off by up to 2^-29 of it).  Query elements
- *         are exact down to 2^-28 of their row's largest.
+ *         are exact down to 2^-28 of their row's largest.  The tensor cores cut output
+ *         sums off: a sum over n tokens in a row (a CTA's share of a sequence; a whole
+ *         one in a prefill) is too small by some 2^-23 for every 16 of them, which reaches
+ *         an output's own half step, 2^-8, at 500,000.
  *   fp32  Weights keep 22 bits down to 2^-18 of a row's largest; smaller ones are off by
  *         up to 2^-40 of it.  Query elements keep 22 bits down to 2^-17 of their row's
  *         largest; smaller ones are off by up to 2^-39 of it.  Output sums are rounded.

@@ -39,3 +39,22 @@ def test_small_weights_keep_22_bits(drop, head_dim):
     for out in outs:
         off = np.abs(f64(out)[0, 0] / ref - 1).max()
         assert off <= tol, (off, tol)
+
+
+@pytest.mark.parametrize("head_dim", [32, 128])
+def test_bf16_sums_over_a_very_long_sequence(head_dim):
+    """Output sums that one CTA takes over the whole sequence are cut off at every product:
+    too small by up to 2^-23 for each 16 tokens, beside the output's own half step, and its
+    weights' 2^-11 (f16), of either sign."""
+    n = 131_077
+    bt = Batch([n], n_kv=1, head_dim=head_dim, seed=2, scale=2.0 ** -4)
+    k, v = bt.draw(n, 0.2), (1.0 + 0.25 * torch.randn(n, 1, head_dim, generator=bt.g)).to(bt.dtype)
+    bt.write(bt.slots([n], [n]), k, v)
+    q = bt.queries(3, 2, mag=0.3)
+    outs = [(bt.decode(q[-1:], max_ctas=1), [n - 1]), (bt.prefill(q, [n], [3]), range(n - 3, n))]
+    bt.no_error()
+    for out, lasts in outs:
+        for i, last in enumerate(lasts):
+            ref, _ = bt.reference(f64(q[i - len(lasts)]), 0, last)
+            off = np.abs(f64(out[i]) - ref) / np.abs(ref)
+            assert off.max() <= 2.0 ** -8 + n / 16 * 2.0 ** -23 + 2.0 ** -11, off.max()

@@ -6,6 +6,8 @@ Each .cu translation unit is compiled in parallel to an object under
 runtime is linked statically, so the library depends only on the driver.
 ``_binding.so`` (csrc/binding.cpp) is compiled beside them with the host
 compiler against the installed PyTorch's headers, and links to ``libpkv.so``.
+The library alone, for users of the C ABI, needs neither PyTorch nor Python's
+headers: run this file as a script.
 
     python -m paged_kv_cache_write_gb300.build [--force] [--verbose]
 """
@@ -46,22 +48,41 @@ def _sources():
 
 
 def _deps():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    """What the library is built from, and what the extension is besides it."""
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != "binding.cpp"]
     files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     files.append(os.path.abspath(__file__))
     return files
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+def _newer(target, files) -> bool:
+    """Whether the target exists and none of the files is newer."""
+    if not os.path.exists(target):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(f) <= t for f in files)
 
 
-def _binding_commands():
+def library_up_to_date() -> bool:
+    return _newer(LIB, _deps())
+
+
+def binding_up_to_date() -> bool:
+    return _newer(BINDING, [os.path.join(CSRC, "binding.cpp"), *_deps()])
+
+
+def up_to_date() -> bool:
+    return library_up_to_date() and (_torch() is None or binding_up_to_date())
+
+
+def _torch():
+    """PyTorch's folder, or None where it is not installed."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
+
+
+def _binding_commands(torch):
     """Commands that compile and link _binding.so."""
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     obj = os.path.join(BUILD, "binding.o")
     cxx = os.environ.get("CXX", "g++")
@@ -74,52 +95,62 @@ def _binding_commands():
     return compile_, link
 
 
+def _start(cmd, verbose):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def _finish(p, verbose):
+    """The process's return code and output."""
+    text = p.communicate()[0].decode(errors="replace")
+    if p.returncode == 0 and verbose and text.strip():
+        print(text)
+    return p.returncode, text
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link libpkv.so and _binding.so if any source is newer; return the
-    library's path."""
-    if not force and up_to_date():
+    """Compile and link libpkv.so, and where PyTorch is installed _binding.so, if any
+    source is newer; return the library's path.  The library needs nvcc alone, and is there
+    whatever becomes of the extension: what fails in that is raised after it."""
+    library = force or not library_up_to_date()
+    torch = _torch()
+    if torch is None:
+        print("PyTorch is not installed: libpkv.so is built without the Python extension",
+              file=sys.stderr)
+    binding = torch is not None and (library or not binding_up_to_date())
+    if not library and not binding:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
     procs = []
     objs = []
-    for src in _sources():
+    for src in _sources() if library else []:
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
-        cmd = [cc, *ARCH, *NVCC_FLAGS, *extra_flags, "-c", src, "-o", obj]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    compile_binding, link_binding = _binding_commands()
-    if verbose:
-        print(" ".join(compile_binding), flush=True)
-    procs.append(("binding.cpp", subprocess.Popen(compile_binding, stdout=subprocess.PIPE,
-                                                  stderr=subprocess.STDOUT)))
-    failed = []
-    for src, p in procs:
-        out, _ = p.communicate()
-        text = out.decode(errors="replace")
-        if p.returncode != 0:
-            failed.append((src, text))
-        elif verbose and text.strip():
-            print(text)
+        procs.append((src, _start([cc, *ARCH, *NVCC_FLAGS, *extra_flags, "-c", src, "-o", obj], verbose)))
+    if binding:
+        compile_binding, link_binding = _binding_commands(torch)
+        compiling = _start(compile_binding, verbose)
+    done = [(src, *_finish(p, verbose)) for src, p in procs]
+    failed = [(src, text) for src, rc, text in done if rc]
+    binding_rc, binding_text = _finish(compiling, verbose) if binding else (0, "")
     if failed:
         msg = "\n".join(f"--- {s}\n{t}" for s, t in failed)
         raise RuntimeError(f"compilation failed:\n{msg}")
-    tmp = LIB + ".tmp"
-    cmd = [cc, *ARCH, "-shared", "-Xlinker", "-soname=libpkv.so", "-o", tmp, *objs]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-    if r.returncode != 0:
-        raise RuntimeError("nvcc link failed:\n" + r.stdout.decode(errors="replace"))
-    os.replace(tmp, LIB)
-    if verbose:
-        print(" ".join(link_binding), flush=True)
-    r = subprocess.run(link_binding, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-    if r.returncode != 0:
-        raise RuntimeError("link of the binding failed:\n" + r.stdout.decode(errors="replace"))
-    os.replace(BINDING + ".tmp", BINDING)
+    if library:
+        tmp = LIB + ".tmp"
+        cmd = [cc, *ARCH, "-shared", "-Xlinker", "-soname=libpkv.so", "-o", tmp, *objs]
+        rc, text = _finish(_start(cmd, verbose), False)
+        if rc:
+            raise RuntimeError("nvcc link failed:\n" + text)
+        os.replace(tmp, LIB)
+    if binding and binding_rc == 0:
+        binding_rc, binding_text = _finish(_start(link_binding, verbose), False)
+    if binding_rc:
+        raise RuntimeError(f"{LIB} is built, but its Python extension is not:\n{binding_text}")
+    if binding:
+        os.replace(BINDING + ".tmp", BINDING)
     return LIB
 
 

@@ -763,7 +763,7 @@ def _load_binding():
         try:
             _native = importlib.import_module("._binding", __name__)
         except ImportError as e:
-            raise ImportError(f"{HERE}/_binding.so cannot be loaded: build it with "
+            raise ImportError(f"the extension in {HERE} cannot be loaded: build it with "
                               f"`python -m paged_kv_cache_write_gb300.build` ({e})") from e
     return _native
 

@@ -1,11 +1,13 @@
 """Build libpkv.so (the C-ABI library) in-tree for sm_103a with nvcc, and
-_binding.so, the CPython extension over some of its entries.
+_binding, the CPython extension over some of its entries.
 
 Each .cu translation unit is compiled in parallel to an object under
 ``_build/``, then linked into ``libpkv.so`` next to this file.  The CUDA
 runtime is linked statically, so the library depends only on the driver.
-``_binding.so`` (csrc/binding.cpp) is compiled beside them with the host
-compiler against the installed PyTorch's headers, and links to ``libpkv.so``.
+``_binding.<ABI>.so`` (csrc/binding.cpp) is compiled beside them with the host
+compiler against the installed PyTorch's headers, and links to ``libpkv.so``.  It
+holds for that interpreter and that PyTorch only: it is named after the one, knows
+the other's version, and is built again when what it was built with has changed.
 The library alone, for users of the C ABI, needs neither PyTorch nor Python's
 headers: run this file as a script.
 
@@ -16,6 +18,7 @@ from __future__ import annotations
 import argparse
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -26,7 +29,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpkv.so")
-BINDING = os.path.join(HERE, "_binding.so")
+BINDING = os.path.join(HERE, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
+BINDING_STAMP = os.path.join(BUILD, "binding.stamp")  # the commands that made it
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
@@ -68,7 +72,14 @@ def library_up_to_date() -> bool:
 
 
 def binding_up_to_date() -> bool:
-    return _newer(BINDING, [os.path.join(CSRC, "binding.cpp"), *_deps()])
+    torch = _torch()
+    if torch is None or not _newer(BINDING, [os.path.join(CSRC, "binding.cpp"), *_deps()]):
+        return False
+    try:
+        with open(BINDING_STAMP) as f:
+            return f.read() == _stamp(torch)
+    except OSError:
+        return False
 
 
 def up_to_date() -> bool:
@@ -81,12 +92,26 @@ def _torch():
     return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
 
 
+def _torch_version(torch):
+    """torch.__version__, without importing it."""
+    with open(os.path.join(torch, "version.py")) as f:
+        found = re.search(r"^__version__\s*=\s*'([^']*)'", f.read(), re.M)
+    if found is None:
+        raise RuntimeError(f"no version in {torch}/version.py")
+    return found.group(1)
+
+
+def _stamp(torch):
+    return "\n".join([sys.version, *(" ".join(c) for c in _binding_commands(torch))])
+
+
 def _binding_commands(torch):
-    """Commands that compile and link _binding.so."""
+    """Commands that compile and link the extension."""
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     obj = os.path.join(BUILD, "binding.o")
     cxx = os.environ.get("CXX", "g++")
     compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-w", "-I", INCLUDE,
+                f'-DPKV_TORCH_VERSION="{_torch_version(torch)}"',
                 "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(cuda, "include"),
                 "-isystem", sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "binding.cpp"),
                 "-o", obj]
@@ -110,7 +135,7 @@ def _finish(p, verbose):
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link libpkv.so, and where PyTorch is installed _binding.so, if any
+    """Compile and link libpkv.so, and where PyTorch is installed the extension, if any
     source is newer; return the library's path.  The library needs nvcc alone, and is there
     whatever becomes of the extension: what fails in that is raised after it."""
     library = force or not library_up_to_date()
@@ -151,6 +176,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         raise RuntimeError(f"{LIB} is built, but its Python extension is not:\n{binding_text}")
     if binding:
         os.replace(BINDING + ".tmp", BINDING)
+        with open(BINDING_STAMP, "w") as f:
+            f.write(_stamp(torch))
     return LIB
 
 

@@ -440,4 +440,22 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+// Tensors are read through the layouts of the PyTorch that this was compiled against, so
+// another one is refused.
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* torch = PyImport_ImportModule("torch");
+  PyObject* version = torch ? PyObject_GetAttrString(torch, "__version__") : nullptr;
+  PyObject* text = version ? PyObject_Str(version) : nullptr;
+  const char* found = text ? PyUnicode_AsUTF8(text) : nullptr;
+  PyObject* m = nullptr;
+  if (found != nullptr) {
+    if (std::string(found) == PKV_TORCH_VERSION)
+      m = PyModule_Create(&module);
+    else
+      PyErr_Format(PyExc_ImportError, "built for PyTorch %s, this is %s", PKV_TORCH_VERSION, found);
+  }
+  Py_XDECREF(text);
+  Py_XDECREF(version);
+  Py_XDECREF(torch);
+  return m;
+}

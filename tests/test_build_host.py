@@ -3,8 +3,10 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 import pytest
+import torch
 
 from paged_kv_cache_write_gb300 import build as real
 
@@ -78,3 +80,31 @@ def test_the_library_is_there_when_the_extension_fails(tmp_path):
     stamp = tree.library.stat().st_mtime_ns
     r = tree.run()
     assert r.returncode != 0 and tree.library.stat().st_mtime_ns == stamp
+
+
+def test_the_extension_belongs_to_an_interpreter_and_a_pytorch(tree):
+    """Named after the one, built again for another version or other flags of the other."""
+    assert tree.run().returncode == 0
+    (made,) = tree.extensions()
+    assert made.name == "_binding" + sysconfig.get_config_var("EXT_SUFFIX")
+    library, stamp = tree.library.stat().st_mtime_ns, made.stat().st_mtime_ns
+    assert tree.run().returncode == 0 and made.stat().st_mtime_ns == stamp
+    kept = tree.pkg / "_build" / "binding.stamp"
+    text = kept.read_text()
+    assert torch.__version__ in text and sys.version in text
+    kept.write_text(text.replace(torch.__version__, "1.0"))
+    assert tree.run().returncode == 0
+    assert made.stat().st_mtime_ns > stamp and tree.library.stat().st_mtime_ns == library
+    assert kept.read_text() == text
+
+
+def test_an_extension_for_another_pytorch_is_refused():
+    """As an import in a process whose PyTorch says that it is another one."""
+    real.build()
+    code = ("import torch; torch.__version__ = '1.0'\n"
+            "import paged_kv_cache_write_gb300 as pkv\n"
+            "try:\n    pkv._load_binding()\nexcept ImportError as e:\n    print(e)\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(real.__file__)),
+                       stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+    assert f"built for PyTorch {torch.__version__}, this is 1.0" in r.stdout

@@ -46,7 +46,7 @@
 // Bound by the softmax warps: 1,640 cycles a key tile, of which exponentials and
 // conversions alone are 1,000 (the MMAs: 1,330 at head_dim 128), and what a job adds, some
 // 7,000 at 64 and 12,000 at 128 (queries in, first scores, outputs).  64 heads on 8 of 128,
-// 4 chunks of 512 after 990 - 3,018 tokens: 145 us, 1,026 TFLOP/s; 2 chunks of 1,024 that
+// 4 chunks of 512 after 990 - 3,018 tokens: 142.5 - 145 us, 1,026 TFLOP/s at the least; 2 chunks of 1,024 that
 // end at 4,096 tokens 223 us, 1,080.  32 heads on 8 of 64, whole prompts: 2 of 4,096 tokens
 // 228 us, 603; 32 of 256 195.
 //
@@ -54,8 +54,12 @@
 // CTAs of one row tile, two on an SM, hide each other's start and end but took 28% longer
 // for 8 chunks of 1,024 of 32 heads on 8 of 64, 10% for 30 prompts of 33 - 612 tokens.
 //
-// 16 warps leave 128 registers a thread, and no loop may spill: with 200 KB of shared
-// memory little L1 is left, and a reload from local memory costs an L2 round trip.
+// 16 warps leave 128 registers a thread, and a loop that spills pays for it: with 200 KB of
+// shared memory little L1 is left, and a reload from local memory costs an L2 round trip.
+// (For heads of 128 a thread stores 8 bytes there and reads 16, for 64 none.)
+//
+// Output sums stay in TMEM over the whole sequence.  The tensor cores cut them off: an
+// output is too small by some 2^-23 for every 16 keys, 6.5e-4 over 131,072.
 //
 // Values past the sequence's end are stored as zeros (scales taken as zero).  A group
 // of values under a NaN scale that some row of the tile may not see is stored as zeros

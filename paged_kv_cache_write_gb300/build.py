@@ -95,7 +95,7 @@ def _torch():
 def _torch_version(torch):
     """torch.__version__, without importing it."""
     with open(os.path.join(torch, "version.py")) as f:
-        found = re.search(r"^__version__\s*=\s*'([^']*)'", f.read(), re.M)
+        found = re.search(r"""^__version__\s*=\s*['"]([^'"]*)['"]""", f.read(), re.M)
     if found is None:
         raise RuntimeError(f"no version in {torch}/version.py")
     return found.group(1)

@@ -18,7 +18,7 @@
 // bits, where a bf16 output has 8).  fp32 queries and weights are split in two f16
 // terms (22 bits): HILO.  A query's second term ends at f16's 2^-24, which is 2^-38 of its
 // row's largest element.  A weight's would end at 2^-28 of the reference's, and lose what
-// many small weights have in common (4,096 equal ones 2^-18 of the first: 1e-4), so it is
+// many small weights have in common (1,024 equal ones 2^-17 of the first: 1e-4), so it is
 // taken times 2^11 and its product with V divided by that: 22 bits down to 2^-18 (64
 // sequences of 512 - 2,048 tokens, 32 heads on 8 of 64, 29.7 us for 28.2; prefill of 4 chunks
 // of 256 at the end of 1,000 tokens, 8 heads on 4 of 128, 88.7 for 83.2).
